@@ -61,6 +61,12 @@ extern "C" {
 #define FP4IDX_MAX_TOPK 4096
 #define FP4IDX_MAX_CONTEXT 65536
 #define FP4IDX_MAX_HIDDEN 16384 /* hidden size limit of fp4idx_quant_q_w */
+#define FP4IDX_LATENT_VALUE 512  /* value dims of a latent row: its first 512 */
+#define FP4IDX_LATENT_MAX_HEADS 128
+#define FP4IDX_LATENT_MAX_ROWS (1 << 20)
+#define FP4IDX_LATENT_MAX_TREE_WORDS 8 /* 256 drafted tokens a sequence */
+#define FP4IDX_PREFILL_KEY 192   /* expanded attention: 128 dims of the head's own key, 64 shared rotated dims */
+#define FP4IDX_PREFILL_VALUE 128
 #define FP4IDX_TOPK_NOALLOC_MAX_BYTES (16u * 1024u * 1024u) /* fixed scratch of fp4idx_topk_noalloc */
 
 typedef enum {
@@ -75,7 +81,8 @@ typedef enum {
   FP4IDX_ERR_BAD_LENGTH = 8,   /* device: context length < 0 or above max_context / page-table width */
   FP4IDX_ERR_SCHEDULE = 9,     /* schedule built for another row count or grid, or its selection
                                   counters were left non-zero by a call that failed: rebuild it */
-  FP4IDX_ERR_SCRATCH_LIMIT = 10 /* fp4idx_topk_noalloc: the call needs more than its fixed scratch */
+  FP4IDX_ERR_SCRATCH_LIMIT = 10, /* fp4idx_topk_noalloc: the call needs more than its fixed scratch */
+  FP4IDX_ERR_CAPACITY = 11       /* device: fp4idx_plan_step ran out of rows, stores or free pages */
 } fp4idx_status;
 
 /* Human-readable name of a status code (static string). */
@@ -400,6 +407,141 @@ int fp4idx_topk_values(const float* logits, int64_t logits_stride, const int32_t
                        float* values, void* stream);
 int fp4idx_topk_merge(const float* cand_values, const int32_t* cand_idx, int64_t n_rows, int32_t n_shards, int32_t k,
                       void* workspace, size_t workspace_bytes, int32_t* topk_idx, int32_t* status_dev, void* stream);
+
+/*
+ * Step plan -- the maps that the other entry points take, built on the device from
+ * request lengths: page table, cache slots, row positions, row sequences, context
+ * lengths.  The pages build them on the host (prefill rows: floor((p+1)/4)); this is an
+ * interface addition, so that a captured step needs no host work.
+ * Sequence b has c = cached_lens[b] tokens and gets n = new_lens[b] more.  One cache
+ * entry stands for `ratio` tokens (4 for the compressed index keys, 1 for one entry a
+ * token): floor(c/ratio) entries exist, those up to floor((c+n)/ratio) are stored by
+ * this step.
+ *   cached_lens, new_lens [n_seqs] int32, n_seqs <= 65536; ratio 1..64
+ *   free_pages [n_free] int32  page ids to take, from index *free_head on (free_head:
+ *                              device int32, nullable = 0); n_free may be 0
+ *   page_table [n_seqs, max_pages] int32 (read, and written where a sequence grows):
+ *              holds the pages of the entries that exist; pages for the new entries are
+ *              taken in sequence order and written behind them
+ *   q_positions, row_seq, context_lens [max_rows] int32 (written): row i of the step is
+ *              a new token of sequence row_seq[i] at position p = c + (its index among
+ *              the new tokens), context length floor((p+1)/ratio).  Rows behind the last
+ *              one: position 0, sequence 0, context length 0 (padding).
+ *   store_positions, store_slots [max_stores] int32 (written): per new entry its index
+ *              in the sequence and its slot page*64 + j; behind the last one 0 and -1
+ *              (padding, skipped by the store kernels).
+ *   cu_rows, cu_context [n_seqs+1] int32 (written): offsets of the sequences' rows, and
+ *              of their entries after the step, each packed in sequence order
+ *   counts [4] int32 (written): rows, stores, pages taken, sequences planned
+ * *free_head and cached_lens are not written: the caller adds counts[2] and new_lens
+ * when the step is done (a repeated call gives the same result).
+ * Sequences are planned in order; the first whose rows, stores or pages do not fit in
+ * max_rows, max_stores or the free pages, and all behind it, get no rows, pages or
+ * context (CAPACITY).  A sequence with a negative length, or more entries than
+ * 64*max_pages, gets none either (BAD_LENGTH); those behind it are planned.  An entry
+ * whose page id is negative or above 2^25-1 gets slot -1 (BAD_PAGE).  The outputs must
+ * not overlap one another or the inputs.  All pointers 4-byte aligned.
+ */
+int fp4idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int32_t ratio,
+                     const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* page_table,
+                     int32_t max_pages, int32_t* q_positions, int32_t* row_seq, int32_t* context_lens,
+                     int64_t max_rows, int32_t* store_positions, int32_t* store_slots, int64_t max_stores,
+                     int32_t* cu_rows, int32_t* cu_context, int32_t* counts, int32_t* status_dev, void* stream);
+
+/*
+ * Latent store -- the write side of the cache that the attention behind the indexer
+ * reads.  A latent row has `width` (512 or 576) bf16 values; all of them are the key of
+ * its token, the first 512 its value, shared by all heads.
+ *   kv         [n_rows, width] bf16
+ *   positions, slots, eps, cos_sin, max_pos  as fp4idx_store_k
+ *   norm_w     [512] bf16
+ *   cache      [num_pages, 64, width] bf16 (written): token j of page p at slot p*64 + j
+ * Row: y = x * rsqrt(mean(x^2 over dims 0..511) + eps) * norm_w on dims 0..511, then
+ * RoPE on the last 64 dims, pairs (i, i+32) as in the index keys (width 512: the
+ * normalised dims 448..511; width 576: dims 512..575, which are not normalised).  fp32
+ * throughout, rounded to bf16 once.
+ * Device errors: BAD_PAGE, BAD_POSITION; the row is skipped.  Slots of one call must be
+ * distinct.
+ */
+int fp4idx_store_latent(const uint16_t* kv, int64_t n_rows, int32_t width, const int32_t* positions,
+                        const int32_t* slots, const uint16_t* norm_w, float eps, const uint16_t* cos_sin,
+                        int32_t max_pos, uint16_t* cache, int64_t num_pages, int32_t* status_dev, void* stream);
+
+/*
+ * Absorbed latent attention over a selection of tokens -- what the selection of
+ * fp4idx_logits_topk is for:
+ *   s[h,i] = scale * q[t,h,:] . k[topk_idx[t,i],:]       (key: all `width` dims)
+ *   out[t,h,:] = sum_i softmax_i(s[h,i]) k[topk_idx[t,i], 0..511]
+ *   lse[t,h]   = log sum_i exp(s[h,i])
+ *   q          [n_rows, n_heads, width] bf16, queries in latent space; n_heads 1..128
+ *   cache      [num_pages, 64, width] bf16; page_table [num_seqs, max_pages], row_seq as above
+ *   topk_idx   [n_rows, k] int32 token positions of the row's sequence; entries < 0 are
+ *              skipped; a position listed twice counts twice
+ *   context_lens [n_rows] int32, nullable: when given, only the first
+ *              min(k, context_lens[t]) entries of the row are read (those that
+ *              fp4idx_topk fills); negative counts as 0
+ *   out        [n_rows, n_heads, 512] bf16 (written); lse [n_rows, n_heads] fp32 (nullable)
+ * A row with no token gets out = 0 and lse = -inf.  Only listed tokens are read: what the
+ * rest of the cache holds (NaN included) does not matter.  Scores, softmax and sums are
+ * fp32; the weights are rounded to bf16 for the second product, the output once.
+ * workspace: fp4idx_latent_attn_workspace_bytes(n_rows, n_heads) bytes, 16-byte aligned,
+ * nothing in it needs to be initialised; calls that may overlap need one each.
+ * Device errors: BAD_PAGE (row_seq outside [0, num_seqs), a position's page id outside
+ * the cache), BAD_LENGTH (a position >= 64*max_pages); the token (the row for row_seq) is
+ * skipped.  TIMEOUT: outputs are then not valid.
+ */
+size_t fp4idx_latent_attn_workspace_bytes(int64_t max_rows, int32_t n_heads);
+int fp4idx_latent_attn_topk(const uint16_t* q, int64_t n_rows, int32_t n_heads, int32_t width, const uint16_t* cache,
+                            int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int32_t max_pages,
+                            const int32_t* row_seq, const int32_t* topk_idx, int32_t k, const int32_t* context_lens,
+                            float scale, void* workspace, size_t workspace_bytes, uint16_t* out, float* lse,
+                            int32_t* status_dev, void* stream);
+
+/*
+ * Absorbed latent attention over the whole context, with an optional tree of drafted
+ * tokens: as fp4idx_latent_attn_topk over the tokens s < context_lens[t] of the row's
+ * sequence and, where tree_mask is given, the tokens context_lens[t] + j whose bit j of
+ * the row's mask is set (bit j of word j/32; a drafted token's own bit and those of the
+ * tokens above it in the tree).
+ *   context_lens [n_rows] int32; max_context: host-known upper bound of
+ *              context_lens[t] + (highest set bit + 1), at most 64*max_pages
+ *   tree_mask  [n_rows, mask_words] uint32 bit patterns (nullable with mask_words 0),
+ *              mask_words <= FP4IDX_LATENT_MAX_TREE_WORDS
+ * Adjacent rows of one sequence share the reads of the cache when their heads fit one
+ * pass together (n_heads <= 32).  Device errors as above; BAD_LENGTH (a context length
+ * < 0, or one past max_context, drafted tokens included): the row has no token.
+ */
+int fp4idx_latent_attn(const uint16_t* q, int64_t n_rows, int32_t n_heads, int32_t width, const uint16_t* cache,
+                       int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int32_t max_pages,
+                       const int32_t* row_seq, const int32_t* context_lens, int32_t max_context,
+                       const uint32_t* tree_mask, int32_t mask_words, float scale, void* workspace,
+                       size_t workspace_bytes, uint16_t* out, float* lse, int32_t* status_dev, void* stream);
+
+/*
+ * Expanded latent attention -- prompts, where each head's keys and values have been
+ * expanded from the latent rows (the cheaper form while the context is shorter than the
+ * selection).  Causal, over packed sequences:
+ *   s[i,j,h] = scale * (q[i,h,0..127] . kv[j,h,0..127] + q[i,h,128..191] . k_rope[j,:])
+ *   out[i,h,:] = sum_j softmax_j(s[i,j,h]) kv[j,h,128..255],  lse as above
+ *   q      [n_q, n_heads, 192] bf16;  kv [n_kv, n_heads, 256] bf16 (128 key dims, then 128
+ *          value dims);  k_rope [n_kv, 64] bf16, shared by the heads;  n_heads 1..1024
+ *   cu_q, cu_kv [n_seqs+1] int32  offsets of the sequences' rows, non-decreasing from >= 0;
+ *          query i of a sequence with nq queries and nkv keys sees its keys
+ *          j <= nkv - nq + i (the queries are the last nq tokens); none where that is < 0
+ *   max_q, max_kv  host-known upper bounds of a sequence's queries and keys
+ *   out    [n_q, n_heads, 128] bf16, lse [n_q, n_heads] fp32 (nullable): written for the
+ *          rows of sequences only (rows from cu_q[n_seqs] on are left as they were)
+ * A row that sees no key gets out = 0 and lse = -inf.  Keys and values behind a
+ * sequence's end do not matter (NaN included); within a sequence a non-finite value row
+ * may also reach the up to 255 query rows before it.  fp32 scores, softmax and sums; the
+ * weights are rounded to bf16 for the second product, the output once.
+ * Device errors: BAD_LENGTH (offsets that decrease, leave the arrays or exceed max_q /
+ * max_kv: the sequence is skipped).  TIMEOUT: outputs are then not valid.
+ */
+int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const uint16_t* kv, int64_t n_kv,
+                          const uint16_t* k_rope, const int32_t* cu_q, const int32_t* cu_kv, int64_t n_seqs,
+                          int32_t max_q, int32_t max_kv, float scale, uint16_t* out, float* lse, int32_t* status_dev,
+                          void* stream);
 
 /*
  * Test support for the logits kernels' bounded waits (failure detection), with no

@@ -28,7 +28,7 @@ STATUS = {
     0: "ok", 1: "invalid argument", 2: "unsupported shape", 3: "CUDA error", 4: "workspace too small",
     5: "page id or slot outside the cache", 6: "pipeline wait timed out", 7: "RoPE position outside the table",
     8: "context length out of range", 9: "schedule does not match the call",
-    10: "call needs more than the fixed top-k scratch",
+    10: "call needs more than the fixed top-k scratch", 11: "plan ran out of rows, stores or free pages",
 }
 
 
@@ -83,6 +83,16 @@ _SIGS = {
     "fp4idx_topk_merge_workspace_bytes": (_sz, [_i64, _i32, _i32]),
     "fp4idx_topk_values": (ctypes.c_int, [_vp, _i64, _vp, _i64, _i32, _vp, _vp]),
     "fp4idx_topk_merge": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _sz, _vp, _vp, _vp]),
+    "fp4idx_plan_step": (ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _vp,
+                                        _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "fp4idx_store_latent": (ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _f32, _vp, _i32, _vp, _i64, _vp, _vp]),
+    "fp4idx_latent_attn_workspace_bytes": (_sz, [_i64, _i32]),
+    "fp4idx_latent_attn_topk": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _vp,
+                                               _f32, _vp, _sz, _vp, _vp, _vp, _vp]),
+    "fp4idx_latent_attn": (ctypes.c_int, [_vp, _i64, _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _vp, _i32,
+                                          _f32, _vp, _sz, _vp, _vp, _vp, _vp]),
+    "fp4idx_latent_prefill": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _vp,
+                                             _vp, _vp, _vp]),
     "fp4idx_test_pipeline_waits": (ctypes.c_int, [_i32, _i64]),
     "fp4idx_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32), _vp]),
 }
@@ -404,6 +414,148 @@ def topk_merge(cand_values, cand_idx, workspace, topk_idx, status=None, stream=N
                                 _ptr(topk_idx, "topk_idx", _I32, T * k), _ptr(status, "status", _I32, 1, nullable=True),
                                 _stream_ptr(stream))
     _check("fp4idx_topk_merge", rc)
+
+
+# ------------------------------------------------------------------ latent attention
+LATENT_VALUE = 512
+PREFILL_KEY = 192
+PREFILL_VALUE = 128
+
+
+class _Args:
+    """Argument checks of one call: every tensor on the current device, contiguous, of the
+    right type and at least the size that the call reads or writes; gives its address."""
+
+    __slots__ = ("device", "stream")
+
+    def __init__(self, stream):
+        self.device = torch.cuda.current_device()
+        self.stream = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
+
+    def __call__(self, t, name, dtypes, numel):
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
+            raise ValueError("%s must be a CUDA tensor on the current device" % name)
+        if t.dtype not in dtypes:
+            raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+        if t.numel() < numel:
+            raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
+        return t.data_ptr()
+
+    def optional(self, t, name, dtypes, numel):
+        return None if t is None else self(t, name, dtypes, numel)
+
+
+def alloc_latent_cache(num_pages, width=576, device="cuda"):
+    """Latent cache [num_pages, 64, width] bf16, zeroed; width 512 or 576."""
+    return torch.zeros((num_pages, PAGE_TOKENS, width), dtype=torch.bfloat16, device=device)
+
+
+def plan_step(cached_lens, new_lens, ratio, free_pages, page_table, q_positions, row_seq, context_lens,
+              store_positions, store_slots, cu_rows, cu_context, counts, free_head=None, status=None, stream=None):
+    """The maps of a step from its request lengths (fp4idx_plan_step): page_table is extended
+    in place, the other outputs are written; their lengths are the call's capacities."""
+    arg = _Args(stream)
+    B, rows, stores = cached_lens.numel(), q_positions.numel(), store_positions.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError("page_table must be [n_seqs, max_pages] with n_seqs = %d" % B)
+    rc = _lib.fp4idx_plan_step(
+        arg(cached_lens, "cached_lens", _I32, B), arg(new_lens, "new_lens", _I32, B), B, ratio,
+        arg(free_pages, "free_pages", _I32, 0), free_pages.numel(), arg.optional(free_head, "free_head", _I32, 1),
+        arg(page_table, "page_table", _I32, 0), page_table.shape[1], arg(q_positions, "q_positions", _I32, 0),
+        arg(row_seq, "row_seq", _I32, rows), arg(context_lens, "context_lens", _I32, rows), rows,
+        arg(store_positions, "store_positions", _I32, 0), arg(store_slots, "store_slots", _I32, stores), stores,
+        arg(cu_rows, "cu_rows", _I32, B + 1), arg(cu_context, "cu_context", _I32, B + 1),
+        arg(counts, "counts", _I32, 4), arg.optional(status, "status", _I32, 1), arg.stream)
+    _check("fp4idx_plan_step", rc)
+
+
+def store_latent(kv, positions, slots, norm_w, eps, cos_sin, cache, status=None, stream=None):
+    """RMSNorm (dims 0..511), RoPE (last 64 dims) and the scatter of latent rows [n, width]
+    into the paged cache [num_pages, 64, width]."""
+    arg = _Args(stream)
+    if kv.dim() != 2 or cache.dim() != 3 or cache.shape[1] != PAGE_TOKENS or cache.shape[2] != kv.shape[1]:
+        raise ValueError("kv must be [n_rows, width] and cache [num_pages, 64, width]")
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
+        raise ValueError("cos_sin must be [max_pos, 64]")
+    n, width = kv.shape
+    rc = _lib.fp4idx_store_latent(
+        arg(kv, "kv", _BF16, 0), n, width, arg(positions, "positions", _I32, n), arg(slots, "slots", _I32, n),
+        arg(norm_w, "norm_w", _BF16, LATENT_VALUE), eps, arg(cos_sin, "cos_sin", _BF16, 0), cos_sin.shape[0],
+        arg(cache, "cache", _BF16, 0), cache.shape[0], arg.optional(status, "status", _I32, 1), arg.stream)
+    _check("fp4idx_store_latent", rc)
+
+
+def latent_attn_workspace_bytes(max_rows, n_heads) -> int:
+    return int(_lib.fp4idx_latent_attn_workspace_bytes(max_rows, n_heads))
+
+
+def _latent_shapes(q, cache, page_table):
+    if q.dim() != 3 or cache.dim() != 3 or cache.shape[1] != PAGE_TOKENS or cache.shape[2] != q.shape[2]:
+        raise ValueError("q must be [n_rows, heads, width] and cache [num_pages, 64, width]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [num_seqs, max_pages]")
+    return q.shape
+
+
+def latent_attn_topk(q, cache, page_table, row_seq, topk_idx, scale, workspace, out, lse=None, context_lens=None,
+                     status=None, stream=None):
+    """Absorbed latent attention of q [T, H, width] over the tokens that topk_idx [T, k] lists:
+    out [T, H, 512] bf16, lse [T, H] fp32 (workspace: latent_attn_workspace_bytes)."""
+    arg = _Args(stream)
+    T, H, width = _latent_shapes(q, cache, page_table)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError("topk_idx must be [n_rows, k]")
+    rc = _lib.fp4idx_latent_attn_topk(
+        arg(q, "q", _BF16, 0), T, H, width, arg(cache, "cache", _BF16, 0), cache.shape[0],
+        arg(page_table, "page_table", _I32, 0), page_table.shape[0], page_table.shape[1],
+        arg(row_seq, "row_seq", _I32, T), arg(topk_idx, "topk_idx", _I32, 0), topk_idx.shape[1],
+        arg.optional(context_lens, "context_lens", _I32, T), scale, arg(workspace, "workspace", _U8, 0),
+        workspace.numel(), arg(out, "out", _BF16, T * H * LATENT_VALUE), arg.optional(lse, "lse", _F32, T * H),
+        arg.optional(status, "status", _I32, 1), arg.stream)
+    _check("fp4idx_latent_attn_topk", rc)
+
+
+def latent_attn(q, cache, page_table, row_seq, context_lens, max_context, scale, workspace, out, lse=None,
+                tree_mask=None, status=None, stream=None):
+    """Absorbed latent attention of q [T, H, width] over each row's whole context and, with
+    tree_mask [T, words] int32, the drafted tokens behind it whose bits are set."""
+    arg = _Args(stream)
+    T, H, width = _latent_shapes(q, cache, page_table)
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] == 0:
+            raise ValueError("tree_mask must be [n_rows, words]")
+        words = tree_mask.shape[1]
+    rc = _lib.fp4idx_latent_attn(
+        arg(q, "q", _BF16, 0), T, H, width, arg(cache, "cache", _BF16, 0), cache.shape[0],
+        arg(page_table, "page_table", _I32, 0), page_table.shape[0], page_table.shape[1],
+        arg(row_seq, "row_seq", _I32, T), arg(context_lens, "context_lens", _I32, T), int(max_context),
+        arg.optional(tree_mask, "tree_mask", _I32, 0), words, scale, arg(workspace, "workspace", _U8, 0),
+        workspace.numel(), arg(out, "out", _BF16, T * H * LATENT_VALUE), arg.optional(lse, "lse", _F32, T * H),
+        arg.optional(status, "status", _I32, 1), arg.stream)
+    _check("fp4idx_latent_attn", rc)
+
+
+def latent_prefill(q, kv, k_rope, cu_q, cu_kv, max_q, max_kv, scale, out, lse=None, status=None, stream=None):
+    """Expanded causal latent attention over packed prompts: q [n_q, H, 192], kv [n_kv, H, 256]
+    (128 key dims, 128 value dims), k_rope [n_kv, 64]; out [n_q, H, 128] bf16, lse [n_q, H]."""
+    arg = _Args(stream)
+    if q.dim() != 3 or q.shape[2] != PREFILL_KEY:
+        raise ValueError("q must be [n_q, heads, 192]")
+    n_q, H, _ = q.shape
+    if kv.dim() != 3 or tuple(kv.shape[1:]) != (H, PREFILL_VALUE + 128):
+        raise ValueError("kv must be [n_kv, heads, 256]")
+    n_kv, B = kv.shape[0], cu_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_q must be [n_seqs + 1]")
+    rc = _lib.fp4idx_latent_prefill(
+        arg(q, "q", _BF16, 0), n_q, H, arg(kv, "kv", _BF16, 0), n_kv, arg(k_rope, "k_rope", _BF16, n_kv * 64),
+        arg(cu_q, "cu_q", _I32, B + 1), arg(cu_kv, "cu_kv", _I32, B + 1), B, int(max_q), int(max_kv), scale,
+        arg(out, "out", _BF16, n_q * H * PREFILL_VALUE), arg.optional(lse, "lse", _F32, n_q * H),
+        arg.optional(status, "status", _I32, 1), arg.stream)
+    _check("fp4idx_latent_prefill", rc)
 
 
 def test_pipeline_waits(idle_producers: bool, wait_limit_ns: int = 0) -> None:
