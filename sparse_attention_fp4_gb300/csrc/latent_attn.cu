@@ -1,128 +1,838 @@
-// Absorbed latent attention: one latent row a token is the key of every head (all its dims)
-// and their value (its first 512).
+// Absorbed latent attention on the tensor cores: one latent row a token is the key of every
+// head (all its dims) and their value (its first 512).
 //
-// A CTA per (row, head).  Its eight warps take the row's tokens in turn; a lane holds its
-// share of the query and of the output, and each warp keeps a running maximum and sum
-// (rescaling its output when the maximum grows), joined at the end.
+//   S^T[tokens, columns] = K Q^T            M = 64 tokens, N = columns, K = width
+//   P^T = exp2(c S^T - m)                   c = scale log2(e), m: the columns' reference
+//   O^T[dims, columns] += V^T P^T           M = 128 dims (four times), N = columns, K = 64
+//
+// A column is a (row, head) pair; up to 64 share a pass over the tokens.  The transposed form
+// keeps the tensor cores' M full with tokens and dims however few the heads are, and lets
+// the same bytes in shared memory be both operands: a tile of 64 tokens is loaded once, as
+// 128-byte-swizzled blocks of 64 dims, which the first product reads with K = dims contiguous
+// and the second with M = dims contiguous.
+//
+// One persistent CTA an SM:
+//   warps 0-3   softmax: S^T from tensor memory, masks, exp2, P^T to shared memory; at the end
+//               of a segment the output
+//   warp 4      one thread issues the MMAs
+//   warp 5      copies a segment's queries
+//   the others  groups of four warps, one per stage, copy tiles with 16-byte cp.async (rows of
+//               listed tokens or of a page; tokens that no row sees become zero rows)
+// The work is the list of all units' tiles (a unit: one row, or adjacent rows of a sequence,
+// and up to 64 columns), cut into equal runs of tiles, one a CTA, whatever the lengths are.
+// A unit cut between CTAs leaves each piece's unnormalised output, maximum and sum in the
+// workspace; combine_kernel joins them in order (the same bits every time).
+//
+// The reference m of a column is not its running maximum: it is only raised when a score
+// passes it by more than 8 (in powers of two), so that in nearly all tiles the output in
+// tensor memory needs no rescaling and the warps exchange one vote.  The result does not
+// depend on m; weights stay below 2^8.
 #include <algorithm>
+#include <cmath>
 
 #include "launchers.cuh"
+#include "mma_bf16.cuh"
+#include "pipeline.cuh"
 
 namespace fp4idx {
 namespace {
 
-constexpr int kWarps = 8;
+using pipe::Ctl;
+using pipe::kFull;
 
-__device__ __forceinline__ void unpack(const uint4& u, float* v) {
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xFFFF0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xFFFF0000u);
-  v[4] = __uint_as_float(u.z << 16); v[5] = __uint_as_float(u.z & 0xFFFF0000u);
-  v[6] = __uint_as_float(u.w << 16); v[7] = __uint_as_float(u.w & 0xFFFF0000u);
+constexpr int kTile = 64;         // tokens a tile: one page
+constexpr int kMaxCtas = 160;     // slots of the workspace
+constexpr int kCols = 64;         // columns of a workspace slot
+constexpr int kValue = FP4IDX_LATENT_VALUE;
+constexpr int kMmaWarp = 4;
+constexpr int kQueryWarp = 5;
+constexpr int kLoadWarp = 6;      // first loader warp
+constexpr int kMaxGroup = 8;      // rows a unit
+constexpr float kRaise = 8.f;
+
+struct Params {
+  LatentArgs a;
+  int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
+  uint64_t wait_limit_ns;
+  int32_t idle_producers;
+};
+
+// Workspace: per slot (two a CTA) a record, the columns' m and l, and the output.
+struct Record {
+  int32_t r0, rows, hb, flags;
+};
+constexpr int kBegins = 1, kEnds = 2, kUsed = 4;
+struct Work {
+  Record* rec;
+  float* ml;
+  float* o;
+};
+__host__ __device__ __forceinline__ Work work_view(void* ws) {
+  uint8_t* p = reinterpret_cast<uint8_t*>(ws);
+  Work w;
+  w.rec = reinterpret_cast<Record*>(p);
+  w.ml = reinterpret_cast<float*>(p + 2 * kMaxCtas * sizeof(Record));
+  w.o = w.ml + 2 * kMaxCtas * 2 * kCols;
+  return w;
+}
+constexpr size_t kWorkBytes =
+    2 * kMaxCtas * (sizeof(Record) + 2 * kCols * sizeof(float) + (size_t)kCols * kValue * sizeof(float));
+
+// ---------------------------------------------------------------- the list of tiles
+// Tokens that row t sees: its plain length, and the end of what it sees (0, 0: nothing).
+__device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& len, int& end, int& err) {
+  const int seq = a.row_seq[t];
+  len = end = 0;
+  if (seq < 0 || seq >= a.num_seqs) {
+    err = FP4IDX_ERR_BAD_PAGE;
+    return;
+  }
+  if (a.idx) {
+    len = end = a.context_lens ? max(0, min(a.k, a.context_lens[t])) : a.k;
+    return;
+  }
+  const int n = a.context_lens[t];
+  int extra = 0;
+  for (int w = 0; w < a.words; w++) {
+    const uint32_t m = a.tree[(int64_t)t * a.words + w];
+    if (m) extra = 32 * w + 32 - __clz(m);
+  }
+  if (n < 0 || (int64_t)n + extra > a.max_context) {
+    err = FP4IDX_ERR_BAD_LENGTH;
+    return;
+  }
+  len = n;
+  end = n + extra;
+}
+__device__ __forceinline__ bool row_sees(const LatentArgs& a, int t, int len, int end, int pos) {
+  if (pos < len) return true;
+  if (pos >= end) return false;
+  const int j = pos - len;
+  return (a.tree[(int64_t)t * a.words + (j >> 5)] >> (j & 31)) & 1;
 }
 
-template <int kWidth>
-__global__ void __launch_bounds__(kWarps * 32) latent_attn_kernel(const LatentArgs a) {
-  __shared__ float part_o[kWarps][512], part_m[kWarps], part_l[kWarps];
-  const int t = blockIdx.x / a.heads, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int seq = a.row_seq[t];
-  int n = 0, len = 0;  // entries to look at; plain context length
-  if (seq < 0 || seq >= a.num_seqs) {
-    if (threadIdx.x == 0) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-  } else if (a.idx) {
-    n = a.context_lens ? max(0, min(a.k, a.context_lens[t])) : a.k;
-  } else {
-    len = a.context_lens[t];
-    int extra = 0;
-    for (int w = 0; w < a.words; w++) {
-      const uint32_t m = a.tree[(int64_t)t * a.words + w];
-      if (m) extra = 32 * w + 32 - __clz(m);
-    }
-    if (len < 0 || (int64_t)len + extra > a.max_context) {
-      if (threadIdx.x == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-    } else {
-      n = len + extra;
-    }
+// The unit that starts at row r0: adjacent rows of one sequence, up to p.group.
+struct Unit {
+  int r0, rows, seq, tiles;
+  int min_len;  // every row sees the tokens before it
+};
+__device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool report) {
+  u.r0 = r0;
+  u.rows = 0;
+  u.seq = p.a.row_seq[r0];
+  u.min_len = INT32_MAX;
+  int most = 0;
+  do {
+    int len, end, err = 0;
+    row_span(p.a, r0 + u.rows, len, end, err);
+    if (err && report) record_error(p.a.status, err);
+    u.min_len = min(u.min_len, len);
+    most = max(most, end);
+    u.rows++;
+  } while (u.rows < p.group && r0 + u.rows < p.a.n_rows && p.a.row_seq[r0 + u.rows] == u.seq);
+  u.tiles = max(1, (most + kTile - 1) / kTile);  // an empty unit still writes its zeros
+}
+
+// A run of tiles [t0, t1) of a unit's column block.
+struct Seg {
+  Unit u;
+  int hb, t0, t1;
+  int64_t left;  // tiles of the CTA from t0 on
+};
+__device__ __forceinline__ bool next_seg(const Params& p, Seg& s) {
+  s.left -= s.t1 - s.t0;
+  if (s.left <= 0) return false;
+  if (++s.hb == p.hb) {
+    s.hb = 0;
+    load_unit(p, s.u.r0 + s.u.rows, s.u, false);
   }
-  float q0[8], q1[8], q2[8], o0[8] = {}, o1[8] = {};
-  const uint16_t* q = a.q + (int64_t)blockIdx.x * kWidth;
-  unpack(*reinterpret_cast<const uint4*>(q + lane * 8), q0);
-  unpack(*reinterpret_cast<const uint4*>(q + 256 + lane * 8), q1);
-  unpack(kWidth == 576 && lane < 8 ? *reinterpret_cast<const uint4*>(q + 512 + lane * 8) : make_uint4(0, 0, 0, 0), q2);
-  float m = -INFINITY, l = 0.f;
-  for (int i = warp; i < n; i += kWarps) {
-    int pos = i;
-    if (a.idx) {
-      pos = a.idx[(int64_t)t * a.k + i];
-      if (pos < 0) continue;
-    } else if (i >= len) {
-      const int j = i - len;
-      if (!((a.tree[(int64_t)t * a.words + j / 32] >> (j & 31)) & 1)) continue;
-    }
-    if (pos / kPage >= a.max_pages) {
-      if (lane == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-      continue;
-    }
-    const int page = a.page_table[(int64_t)seq * a.max_pages + pos / kPage];
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-      continue;
-    }
-    const uint16_t* k = a.cache + ((int64_t)page * kPage + pos % kPage) * kWidth;
-    float k0[8], k1[8], k2[8], s = 0.f;
-    unpack(*reinterpret_cast<const uint4*>(k + lane * 8), k0);
-    unpack(*reinterpret_cast<const uint4*>(k + 256 + lane * 8), k1);
+  s.t0 = 0;
+  s.t1 = (int)min((int64_t)s.u.tiles, s.left);
+  return true;
+}
+
+// ---------------------------------------------------------------- the CTA's run
+// All threads: finds the CTA's first unit and tile.  Rows are taken blockDim.x at a time; the
+// first pass sums the tiles, the second finds the run's start.
+struct ScanShared {
+  int64_t sums[32];
+  int32_t starts[32];
+  int32_t found_row;
+  int64_t found_off;
+};
+__device__ __forceinline__ int64_t block_scan(int64_t v, ScanShared& sh, int64_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
-    for (int d = 0; d < 8; d++) s += q0[d] * k0[d] + q1[d] * k1[d];
-    if (kWidth == 576 && lane < 8) {
-      unpack(*reinterpret_cast<const uint4*>(k + 512 + lane * 8), k2);
-#pragma unroll
-      for (int d = 0; d < 8; d++) s += q2[d] * k2[d];
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    s *= a.scale;
-    const float m1 = fmaxf(m, s), keep = m1 == -INFINITY ? 1.f : expf(m - m1);
-    const float p = m1 == -INFINITY ? 0.f : expf(s - m1);
-    m = m1;
-    l = l * keep + p;
-#pragma unroll
-    for (int d = 0; d < 8; d++) {
-      o0[d] = o0[d] * keep + p * k0[d];
-      o1[d] = o1[d] * keep + p * k1[d];
-    }
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(kFull, v, d);
+    if (lane >= d) v += u;
   }
-#pragma unroll
-  for (int d = 0; d < 8; d++) {
-    part_o[warp][lane * 8 + d] = o0[d];
-    part_o[warp][256 + lane * 8 + d] = o1[d];
-  }
-  if (lane == 0) {
-    part_m[warp] = m;
-    part_l[warp] = l;
+  if (lane == 31) sh.sums[warp] = v;
+  __syncthreads();
+  int64_t before = 0;
+  total = 0;
+  for (int w = 0; w < warps; w++) {
+    const int64_t s = sh.sums[w];
+    if (w < warp) before += s;
+    total += s;
   }
   __syncthreads();
-  float top = -INFINITY, total = 0.f;
-  for (int w = 0; w < kWarps; w++) top = fmaxf(top, part_m[w]);
-  for (int w = 0; w < kWarps; w++) total += part_m[w] == -INFINITY ? part_l[w] : part_l[w] * expf(part_m[w] - top);
-  for (int d = threadIdx.x; d < 512; d += kWarps * 32) {
-    float o = 0.f;
-    for (int w = 0; w < kWarps; w++) o += part_m[w] == -INFINITY ? part_o[w][d] : part_o[w][d] * expf(part_m[w] - top);
-    o = total == 0.f ? 0.f : o / total;
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(o));
-    a.out[(int64_t)blockIdx.x * 512 + d] = (uint16_t)r;
+  return before + v;
+}
+// Tiles (over all head blocks) of the unit that starts at row base + threadIdx.x, 0 if none
+// does; `run` carries the first row of the last run of one sequence from chunk to chunk.
+__device__ __forceinline__ int64_t unit_weight(const Params& p, int base, int& run, ScanShared& sh, bool report) {
+  const int t = base + (int)threadIdx.x;
+  const bool in = t < p.a.n_rows;
+  bool starts = in;
+  if (p.group > 1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int first = in && (t == 0 || p.a.row_seq[t] != p.a.row_seq[t - 1]) ? t : -1;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int u = __shfl_up_sync(kFull, first, d);
+      if (lane >= d) first = max(first, u);
+    }
+    if (lane == 31) sh.starts[warp] = first;
+    __syncthreads();
+    int last = run;
+    for (int w = 0; w < warps; w++) {
+      if (w < warp) first = max(first, sh.starts[w]);
+      last = max(last, sh.starts[w]);
+    }
+    first = max(first, run);
+    __syncthreads();
+    run = last;
+    starts = in && (t - first) % p.group == 0;
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[blockIdx.x] = total == 0.f ? -INFINITY : top + logf(total);
+  if (!starts) return 0;
+  Unit u;
+  load_unit(p, t, u, report);
+  return (int64_t)u.tiles * p.hb;
+}
+__device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
+  const int n = p.a.n_rows, step = blockDim.x;
+  const bool report = blockIdx.x == 0;
+  int64_t all = 0, w = 0, incl = 0, total;
+  int run = -1;
+  for (int base = 0; base < n; base += step) {
+    w = unit_weight(p, base, run, sh, report);
+    incl = block_scan(w, sh, total);
+    all += total;
+  }
+  const int64_t runs = min((int64_t)gridDim.x, all);  // at least one tile each
+  if (blockIdx.x >= runs) return false;
+  const int64_t lo = all * blockIdx.x / runs, hi = all * (blockIdx.x + 1) / runs;
+  int64_t carry = 0;
+  run = -1;
+  for (int base = 0; base < n; base += step) {
+    if (n > step) {
+      w = unit_weight(p, base, run, sh, false);
+      incl = block_scan(w, sh, total);
+    }
+    const int64_t end = carry + incl;
+    if (lo < end && lo >= end - w) {
+      sh.found_row = base + threadIdx.x;
+      sh.found_off = lo - (end - w);
+    }
+    carry += total;
+    if (lo < carry) break;
+  }
+  __syncthreads();
+  load_unit(p, sh.found_row, s.u, false);
+  s.hb = (int)(sh.found_off / s.u.tiles);
+  s.t0 = (int)(sh.found_off % s.u.tiles);
+  s.left = hi - lo;
+  s.t1 = (int)min((int64_t)s.u.tiles, s.t0 + s.left);
+  return true;
+}
+
+// ---------------------------------------------------------------- shared memory
+template <int kWidth, int kN>
+struct Shape {
+  static constexpr int kChunks = kWidth / 64;
+  static constexpr uint32_t kStageBytes = kChunks * kTile * 128;
+  static constexpr uint32_t kQChunk = kN * 128;
+  // a third stage where it fits (width 512 with at most 16 columns)
+  static constexpr int kStages = 3 * kStageBytes + (kChunks + 1) * kQChunk <= 225 * 1024 ? 3 : 2;
+  static constexpr int kThreads = (kLoadWarp + 4 * kStages) * 32;
+  static constexpr uint32_t kOffQ = kStages * kStageBytes;
+  static constexpr uint32_t kOffP = kOffQ + kChunks * kQChunk;
+  static constexpr uint32_t kOffSeen = kOffP + kN * 128;          // [stage][64] rows that see the token
+  static constexpr uint32_t kOffRed = kOffSeen + kStages * kTile;  // [4][kN] floats
+  static constexpr uint32_t kOffM = kOffRed + 4 * kN * 4;          // [kN]
+  static constexpr uint32_t kOffF = kOffM + kN * 4;                // [kN]
+  static constexpr uint32_t kOffBar = kOffF + kN * 4;
+  // kfull[stages], kempty[stages], qfull, qempty, sfull[2], pfull, done
+  static constexpr int kBars = 2 * kStages + 6;
+  static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+  static constexpr uint32_t kBytes = kOffMisc + 16 + 1024;  // and the base's alignment
+  static constexpr uint32_t kTmemCols = kN == 64 ? 512 : kN == 32 ? 256 : 128;
+};
+// The scan's scratch lies in the query buffer, which is not in use yet.
+
+template <int kWidth, int kN>
+__global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ Params p) {
+  using S = Shape<kWidth, kN>;
+  constexpr int kStages = S::kStages, kChunks = S::kChunks, kJ = kN / 8;
+  extern __shared__ uint8_t smem_raw[];
+  const LatentArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t sb = ptx::smem_addr(smem);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + S::kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc + 4);
+  auto bar = [&](int i) { return sb + S::kOffBar + i * 8; };
+  const auto kfull = [&](int s) { return bar(s); };
+  const auto kempty = [&](int s) { return bar(kStages + s); };
+  const uint32_t qfull = bar(2 * kStages), qempty = bar(2 * kStages + 1), pfull = bar(2 * kStages + 4),
+                 done = bar(2 * kStages + 5);
+  const auto sfull = [&](int b) { return bar(2 * kStages + 2 + b); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; s++) {
+      ptx::mbar_init(kfull(s), 128);
+      ptx::mbar_init(kempty(s), 1);
+    }
+    ptx::mbar_init(qfull, 32);
+    ptx::mbar_init(qempty, 1);
+    ptx::mbar_init(sfull(0), 1);
+    ptx::mbar_init(sfull(1), 1);
+    ptx::mbar_init(pfull, 128);
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+  Seg seg;
+  const bool any = first_seg(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
+  Work wk = work_view(a.workspace);
+  if (threadIdx.x == 0) {
+    wk.rec[2 * blockIdx.x] = Record{0, 0, 0, 0};
+    wk.rec[2 * blockIdx.x + 1] = Record{0, 0, 0, 0};
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctl ctl{abort_flag, a.status, p.wait_limit_ns};
+  const uint32_t tm_s = tmem + 4 * kN;  // two S^T buffers behind the output
+
+  if (any && warp >= kLoadWarp) {
+    // ------------------------------------------------------------ loaders
+    const int grp = (warp - kLoadWarp) >> 2, tid = threadIdx.x - (kLoadWarp + 4 * grp) * 32;
+    const int wrow = (tid >> 5) * 16 + (lane >> 3), piece = lane & 7;
+    uint32_t kctr = 0;
+    int t = seg.t0;
+    bool have = !p.idle_producers;
+    // moves to this group's next tile, n tiles on
+    auto advance = [&](int n) {
+      kctr += n;
+      t += n;
+      while (t >= seg.t1) {
+        n = t - seg.t1;
+        if (!next_seg(p, seg)) {
+          have = false;
+          return;
+        }
+        t = seg.t0 + n;
+      }
+    };
+    const uint16_t* src[4];
+    uint32_t seen[4];  // rows of the unit that see the thread's tokens
+    auto look_up = [&]() {
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        int pos = t * kTile + wrow + g * 4;
+        uint32_t rows = 0;
+        if (a.idx) {
+          if (pos < seg.u.min_len) {
+            pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
+            rows = pos >= 0;
+          }
+        } else if (pos < seg.u.min_len) {
+          rows = (1u << seg.u.rows) - 1;
+        } else {
+          for (int r = 0; r < seg.u.rows; r++) {
+            int len, end, err;
+            row_span(a, seg.u.r0 + r, len, end, err);
+            rows |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos) << r;
+          }
+        }
+        src[g] = a.cache;
+        seen[g] = 0;
+        if (rows) {
+          if (pos / kPage >= a.max_pages) {
+            record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+          } else {
+            const int32_t page = a.page_table[(int64_t)seg.u.seq * a.max_pages + pos / kPage];
+            if (page < 0 || page >= a.num_pages) {
+              record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+            } else {
+              src[g] = a.cache + ((int64_t)page * kPage + pos % kPage) * kWidth;
+              seen[g] = rows;
+            }
+          }
+        }
+      }
+    };
+    if (have && grp > 0) advance(grp);
+    if (have) look_up();
+    while (have) {
+      const int s = kctr % kStages;
+      if (!pipe::wait_warp(kempty(s), ((kctr / kStages) & 1) ^ 1, ctl)) break;
+      const uint32_t dst = sb + s * S::kStageBytes;
+#pragma unroll
+      for (int c = 0; c < kChunks; c++)
+#pragma unroll
+        for (int g = 0; g < 4; g++)
+          mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64 + piece * 8,
+                          seen[g] ? 16 : 0);
+      if (piece == 0) {
+#pragma unroll
+        for (int g = 0; g < 4; g++) smem[S::kOffSeen + s * kTile + wrow + g * 4] = (uint8_t)seen[g];
+      }
+      const uint32_t full = kfull(s);
+      advance(kStages);
+      if (have) look_up();  // while the copies are in flight
+      mma::cp_async_wait_all();
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(full);
+    }
+    mma::cp_async_wait_all();
+  } else if (any && warp == kQueryWarp) {
+    // ------------------------------------------------------------ queries
+    uint32_t ictr = 0;
+    do {
+      if (!pipe::wait_warp(qempty, (ictr & 1) ^ 1, ctl)) break;
+      const int r0 = lane >> 3, pc = lane & 7;
+      for (int col = r0; col < kN; col += 4) {
+        const int r = col / p.hp, h = col % p.hp, head = seg.hb * p.hs + h;
+        const bool in = r < seg.u.rows && h < p.hs && head < a.heads;
+        const uint16_t* q = in ? a.q + ((int64_t)(seg.u.r0 + r) * a.heads + head) * kWidth + pc * 8 : a.q;
+        const uint32_t dst = sb + S::kOffQ + mma::sw128(col, pc);
+#pragma unroll
+        for (int c = 0; c < kChunks; c++) mma::cp_async16(dst + c * S::kQChunk, q + (in ? c * 64 : 0), in ? 16 : 0);
+      }
+      mma::cp_async_wait_all();
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(qfull);
+      ictr++;
+    } while (next_seg(p, seg));
+  } else if (any && warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue (lane 0)
+    if (lane == 0) {
+      constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
+      constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
+      uint32_t kctr = 0, ictr = 0;
+      auto issue_s = [&](uint32_t k) {
+        ptx::tc_fence_after();
+        const uint32_t kb = sb + (k % kStages) * S::kStageBytes, qb = sb + S::kOffQ, d = tm_s + (k & 1) * kN;
+#pragma unroll
+        for (int c = 0; c < kChunks; c++)
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            mma::mma_ss(d, mma::desc_sw128(kb + c * (kTile * 128) + i * 32, 0, 1024),
+                        mma::desc_sw128(qb + c * S::kQChunk + i * 32, 0, 1024), kIdS, c | i);
+        ptx::mma_commit(sfull(k & 1));
+      };
+      bool ok = true;
+      do {
+        const uint32_t n = seg.t1 - seg.t0;
+        ok = pipe::poll(qfull, ictr & 1, ctl, true);
+        uint32_t issued = 0;
+        for (uint32_t i = 0; ok && i < n; i++, kctr++) {
+          if (issued == i) {
+            ok = pipe::poll(kfull(kctr % kStages), (kctr / kStages) & 1, ctl, true);
+            if (!ok) break;
+            issue_s(kctr);
+            if (++issued == n) ptx::mma_commit(qempty);
+          }
+          // until the weights are there, the next tile's scores are issued as soon as it is
+          if (issued < n && !ptx::mbar_try_wait(pfull, kctr & 1)) {
+            const uint64_t t0 = ptx::globaltimer();
+            for (uint32_t it = 1;; it++) {
+              const uint32_t k = kctr + 1;
+              if (ptx::mbar_try_wait(kfull(k % kStages), (k / kStages) & 1)) {
+                issue_s(k);
+                if (++issued == n) ptx::mma_commit(qempty);
+                break;
+              }
+              if (ptx::mbar_try_wait(pfull, kctr & 1)) break;
+              if ((it & 63u) == 0) {
+                if (*ctl.abort) ok = false;
+                else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
+                if (!ok) break;
+              }
+            }
+            if (!ok) break;
+          }
+          ok = pipe::poll(pfull, kctr & 1, ctl, true);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t vb = sb + (kctr % kStages) * S::kStageBytes, pb = sb + S::kOffP;
+#pragma unroll
+          for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+            for (int b = 0; b < 4; b++)
+              mma::mma_ss(tmem + b * kN, mma::desc_sw128(vb + b * (2 * kTile * 128) + ks * 2048, kTile * 128, 1024),
+                          mma::desc_sw128(pb + ks * 32, 0, 1024), kIdO, i > 0 || ks > 0);
+          ptx::mma_commit(kempty(kctr % kStages));
+        }
+        ictr++;
+      } while (ok && next_seg(p, seg));
+      // nothing of this CTA's may be under way in the tensor cores when it ends
+      ptx::mma_commit(done);
+      pipe::poll(done, 0, ctl, false);
+    }
+    __syncwarp();
+  } else if (any && warp < 4) {
+    // ------------------------------------------------------------ softmax and output
+    const float cs = a.scale * 1.4426950408889634f;
+    const int quad = lane & 3, r8 = lane >> 2;
+    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem + S::kOffRed);
+    float* sm_m = reinterpret_cast<float*>(smem + S::kOffM);
+    float* sm_f = reinterpret_cast<float*>(smem + S::kOffF);
+    const int tok = warp * 16 + r8;  // and tok + 8
+    uint32_t kctr = 0;
+    bool ok = true, first_of_cta = true;
+    do {
+      const int n = seg.t1 - seg.t0;
+      const uint32_t everyone = (1u << seg.u.rows) - 1;
+      float m[2 * kJ], l[2 * kJ];  // of the thread's columns 8 j + 2 quad + {0, 1}
+#pragma unroll
+      for (int j = 0; j < 2 * kJ; j++) {
+        m[j] = -INFINITY;
+        l[j] = 0.f;
+      }
+      for (int i = 0; i < n; i++, kctr++) {
+        const int st = kctr % kStages;
+        // a warp whose wait ran out goes on to the next vote, so that all four leave together
+        ok = ok && pipe::wait_warp(kfull(st), (kctr / kStages) & 1, ctl) &&
+             pipe::wait_warp(sfull(kctr & 1), (kctr >> 1) & 1, ctl);
+        ptx::tc_fence_after();
+        float v[4 * kJ];
+        mma::ld_16x256b<kJ>(tm_s + (kctr & 1) * kN + lanes, v);
+        const uint32_t see0 = smem[S::kOffSeen + st * kTile + tok], see1 = smem[S::kOffSeen + st * kTile + tok + 8];
+        if (!__all_sync(kFull, see0 == everyone && see1 == everyone)) {
+          if (seg.u.rows > 1) {
+            // A token that some rows see and others do not stays in the second product.  If
+            // it is not finite (then no score of it is), its value row is zeroed and the
+            // columns that see it get a NaN weight: NaN for those, nothing for the others.
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+              const uint32_t see = half ? see1 : see0;
+              bool odd = see != 0 && see != everyone;
+#pragma unroll
+              for (int j = 0; j < kJ; j++) odd = odd && !(fabsf(v[4 * j + 2 * half]) < INFINITY) && !(fabsf(v[4 * j + 2 * half + 1]) < INFINITY);
+              const uint32_t all = __ballot_sync(kFull, odd) >> (lane & 28) & 15u;
+              if (all == 15u) {
+                for (int c = quad; c < kValue / 8; c += 4)
+                  *reinterpret_cast<uint4*>(smem + st * S::kStageBytes + (c >> 3) * (kTile * 128) +
+                                            mma::sw128(tok + 8 * half, c & 7)) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < kJ; j++) v[4 * j + 2 * half] = v[4 * j + 2 * half + 1] = NAN;
+              }
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < kJ; j++) {
+            const int r = 8 * j / p.hp;
+            const bool in0 = (see0 >> r) & 1, in1 = (see1 >> r) & 1;
+            v[4 * j] = in0 ? v[4 * j] * cs : -INFINITY;
+            v[4 * j + 1] = in0 ? v[4 * j + 1] * cs : -INFINITY;
+            v[4 * j + 2] = in1 ? v[4 * j + 2] * cs : -INFINITY;
+            v[4 * j + 3] = in1 ? v[4 * j + 3] * cs : -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4 * kJ; j++) v[j] *= cs;
+        }
+        bool above = !ok;
+#pragma unroll
+        for (int j = 0; j < kJ; j++) {
+          above = above || fmaxf(v[4 * j], v[4 * j + 2]) > m[2 * j] + kRaise ||
+                  fmaxf(v[4 * j + 1], v[4 * j + 3]) > m[2 * j + 1] + kRaise;
+        }
+        const bool raise = mma::bar_any(1, 128, above);
+        if (raise) {
+          if (mma::bar_any(1, 128, !ok)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int j = 0; j < kJ; j++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              float x = fmaxf(v[4 * j + e], v[4 * j + 2 + e]);
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+              if (r8 == 0) red[warp * kN + 8 * j + 2 * quad + e] = x;
+            }
+          }
+          ptx::named_bar_sync(1, 128);
+#pragma unroll
+          for (int j = 0; j < kJ; j++) {
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+              const int c = 8 * j + 2 * quad + e;
+              const float x = fmaxf(fmaxf(red[c], red[kN + c]), fmaxf(red[2 * kN + c], red[3 * kN + c]));
+              const float m1 = fmaxf(m[2 * j + e], x);
+              const float f = m1 == m[2 * j + e] ? 1.f : mma::exp2_approx(m[2 * j + e] - m1);
+              if (warp == 0 && r8 == 0) sm_f[c] = f;
+              l[2 * j + e] *= f;
+              m[2 * j + e] = m1;
+            }
+          }
+          ptx::named_bar_sync(1, 128);  // red is read, sm_f is written
+        }
+        uint32_t pk[2 * kJ];
+#pragma unroll
+        for (int j = 0; j < kJ; j++) {
+          const float m0 = m[2 * j] == -INFINITY ? 0.f : m[2 * j], m1 = m[2 * j + 1] == -INFINITY ? 0.f : m[2 * j + 1];
+          const float p0 = mma::exp2_approx(v[4 * j] - m0), p1 = mma::exp2_approx(v[4 * j + 1] - m1);
+          const float p2 = mma::exp2_approx(v[4 * j + 2] - m0), p3 = mma::exp2_approx(v[4 * j + 3] - m1);
+          l[2 * j] += p0 + p2;
+          l[2 * j + 1] += p1 + p3;
+          pk[2 * j] = mma::pack_bf16(p0, p1);
+          pk[2 * j + 1] = mma::pack_bf16(p2, p3);
+        }
+        // the last tile's product has read P^T, and the output may be rescaled
+        if (kctr > 0) {
+          const uint32_t last = kctr - 1;
+          ok = pipe::wait_warp(kempty(last % kStages), (last / kStages) & 1, ctl);
+          if (!ok) continue;
+        }
+        if (raise) {
+          if (i > 0) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 4 * kN; b += 16) {
+              float o[16];
+              mma::ld_32x16(tmem + b + lanes, o);
+#pragma unroll
+              for (int e = 0; e < 16; e++) o[e] *= sm_f[(b % kN) + e];
+              mma::st_32x16(tmem + b + lanes, o);
+            }
+            ptx::tmem_wait_st();
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kJ; j += 2) {
+          const int col = 8 * (j + (lane >> 4)) + (lane & 7), tb = 2 * warp + ((lane >> 3) & 1);
+          mma::stmatrix_x4_trans(sb + S::kOffP + mma::sw128(col, tb), pk[2 * j], pk[2 * j + 1], pk[2 * j + 2], pk[2 * j + 3]);
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(pfull);
+      }
+      if (mma::bar_any(1, 128, !ok)) break;
+      // ---- the segment's output
+      const bool begins = seg.t0 == 0, ends = seg.t1 == seg.u.tiles, whole = begins && ends;
+#pragma unroll
+      for (int j = 0; j < 2 * kJ; j++) {
+        l[j] += __shfl_xor_sync(kFull, l[j], 4);
+        l[j] += __shfl_xor_sync(kFull, l[j], 8);
+        l[j] += __shfl_xor_sync(kFull, l[j], 16);
+        const int c = 8 * (j >> 1) + 2 * quad + (j & 1);
+        if (r8 == 0) red[warp * kN + c] = l[j];
+        if (r8 == 0 && warp == 0) sm_m[c] = m[j];
+      }
+      ptx::named_bar_sync(1, 128);
+      const int slot = 2 * blockIdx.x + (first_of_cta ? 0 : 1);
+      first_of_cta = false;
+      if (threadIdx.x < kN) {
+        const int c = threadIdx.x;
+        const float total = red[c] + red[kN + c] + red[2 * kN + c] + red[3 * kN + c];
+        if (whole) {
+          sm_f[c] = total == 0.f ? 0.f : 1.f / total;
+          const int r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
+          if (a.lse && r < seg.u.rows && h < p.hs && head < a.heads)
+            a.lse[(int64_t)(seg.u.r0 + r) * a.heads + head] =
+                total == 0.f ? -INFINITY : (sm_m[c] + log2f(total)) * 0.6931471805599453f;
+        } else {
+          wk.ml[slot * 2 * kCols + c] = sm_m[c];
+          wk.ml[slot * 2 * kCols + kCols + c] = total;
+        }
+      }
+      if (!whole && threadIdx.x == 0)
+        wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
+      const uint32_t last = kctr - 1;
+      ok = pipe::wait_warp(kempty(last % kStages), (last / kStages) & 1, ctl);
+      if (mma::bar_any(1, 128, !ok)) break;
+      ptx::tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 4 * kN; b += 16) {
+        float o[16];
+        mma::ld_32x16(tmem + b + lanes, o);
+        const int dim = (b / kN) * 128 + warp * 32 + lane;
+#pragma unroll
+        for (int e = 0; e < 16; e++) {
+          const int c = (b % kN) + e;
+          if (whole) {
+            const int r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
+            if (r < seg.u.rows && h < p.hs && head < a.heads)
+              a.out[((int64_t)(seg.u.r0 + r) * a.heads + head) * kValue + dim] =
+                  (uint16_t)mma::pack_bf16(o[e] * sm_f[c], 0.f);
+          } else {
+            wk.o[((int64_t)slot * kCols + c) * kValue + dim] = o[e];
+          }
+        }
+      }
+      ptx::tc_fence_before();
+      ptx::named_bar_sync(1, 128);  // red, sm_m and sm_f are free again
+    } while (next_seg(p, seg));
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
+}
+
+// ---------------------------------------------------------------- joining the pieces
+// Block (c, y): the unit whose first piece is CTA c's, columns 8 y .. 8 y + 7; its next pieces
+// are the first segments of the CTAs that follow.  Three groups of eight warps take the pieces
+// in turn, a warp one column; the groups' sums are added in order.
+constexpr int kJoinGroups = 3, kJoinThreads = kJoinGroups * 256;
+__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p, int ctas) {
+  __shared__ float sh_o[kJoinGroups - 1][8][kValue];
+  __shared__ int sh_last;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const LatentArgs& a = p.a;
+  const Work wk = work_view(a.workspace);
+  const int c0 = blockIdx.x;
+  int slot0 = 2 * c0 + 1;
+  Record rec = wk.rec[slot0];
+  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) rec = wk.rec[--slot0];
+  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) return;
+  if (threadIdx.x == 0) sh_last = ctas;
+  __syncthreads();
+  const int cx = c0 + 1 + (int)threadIdx.x;
+  if (cx < ctas && (wk.rec[2 * cx].flags & (kUsed | kBegins | kEnds)) == (kUsed | kEnds)) atomicMin(&sh_last, cx);
+  __syncthreads();
+  if (sh_last >= ctas) return;  // a run that gave up
+  const int n = sh_last - c0 + 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp >> 3, cl = warp & 7;
+  const int col = blockIdx.y * 8 + cl;
+  const int r = col / p.hp, h = col % p.hp, head = rec.hb * p.hs + h;
+  const bool in = r < rec.rows && h < p.hs && head < a.heads;
+  auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
+  float top = -INFINITY, total = 0.f;
+  float o[16] = {};
+  if (in) {
+    for (int i = lane; i < n; i += 32) top = fmaxf(top, wk.ml[slot_of(i) * 2 * kCols + col]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
+    if (top == -INFINITY) top = 0.f;
+    for (int i = lane; i < n; i += 32) {
+      const float* ml = wk.ml + slot_of(i) * 2 * kCols + col;
+      total += mma::exp2_approx(ml[0] - top) * ml[kCols];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+#pragma unroll 2
+    for (int i = grp; i < n; i += kJoinGroups) {
+      const int s = slot_of(i);
+      const float f = mma::exp2_approx(wk.ml[s * 2 * kCols + col] - top);
+      const float4* x = reinterpret_cast<const float4*>(wk.o + ((int64_t)s * kCols + col) * kValue) + lane;
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const float4 y = x[32 * q];
+        o[4 * q] += f * y.x;
+        o[4 * q + 1] += f * y.y;
+        o[4 * q + 2] += f * y.z;
+        o[4 * q + 3] += f * y.w;
+      }
+    }
+  }
+  if (grp > 0) {
+#pragma unroll
+    for (int q = 0; q < 4; q++)
+      *reinterpret_cast<float4*>(&sh_o[grp - 1][cl][q * 128 + lane * 4]) =
+          make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+  }
+  __syncthreads();
+  if (grp > 0 || !in) return;
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  const int64_t row = (int64_t)(rec.r0 + r) * a.heads + head;
+#pragma unroll
+  for (int q = 0; q < 4; q++) {
+#pragma unroll
+    for (int g = 0; g < kJoinGroups - 1; g++) {
+      const float4 y = *reinterpret_cast<const float4*>(&sh_o[g][cl][q * 128 + lane * 4]);
+      o[4 * q] += y.x;
+      o[4 * q + 1] += y.y;
+      o[4 * q + 2] += y.z;
+      o[4 * q + 3] += y.w;
+    }
+    *reinterpret_cast<uint2*>(a.out + row * kValue + q * 128 + lane * 4) =
+        make_uint2(mma::pack_bf16(o[4 * q] * inv, o[4 * q + 1] * inv),
+                   mma::pack_bf16(o[4 * q + 2] * inv, o[4 * q + 3] * inv));
+  }
+  if (lane == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+}
+
+template <int kWidth, int kN>
+cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t stream) {
+  using S = Shape<kWidth, kN>;
+  static_assert(S::kBytes <= 232448, "shared memory of a CTA");
+  static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
+  const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN>);
+  cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
+  if (e != cudaSuccess) return e;
+  latent_attn_kernel<kWidth, kN><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !may_split) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, kN / 8, 1);
+  cfg.blockDim = dim3(kJoinThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, combine_kernel, p, ctas);
 }
 
 }  // namespace
 
-size_t latent_attn_workspace_bytes(int64_t, int32_t) { return 256; }
+size_t latent_attn_workspace_bytes(int64_t, int32_t) { return kWorkBytes; }
 
-cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool, cudaStream_t stream) {
-  auto kernel = width == 576 ? latent_attn_kernel<576> : latent_attn_kernel<512>;
-  kernel<<<(unsigned)(a.n_rows * a.heads), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool selected, cudaStream_t stream) {
+  Params p{};
+  p.a = a;
+  p.hb = (a.heads + kCols - 1) / kCols;
+  p.hs = (a.heads + p.hb - 1) / p.hb;
+  p.hp = (p.hs + 7) / 8 * 8;
+  p.group = 1;
+  if (!selected) {
+    // rows of one sequence share a pass when their columns fit; no more than a sequence has
+    const int per_seq = (int)std::min<int64_t>(kMaxGroup, ((int64_t)a.n_rows + a.num_seqs - 1) / a.num_seqs);
+    p.group = std::max(1, std::min(per_seq, kCols / p.hp));
+  }
+  p.wait_limit_ns = pipeline_wait_limit_ns();
+  p.idle_producers = pipeline_idle_producers() ? 1 : 0;
+  int sms = 0, dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int ctas = std::min(sms, kMaxCtas);
+  const bool may_split = (selected ? a.k : a.max_context) > kTile;
+  const int cols = p.group * p.hp;
+  if (width == 576) {
+    if (cols <= 16) return launch<576, 16>(p, ctas, may_split, stream);
+    if (cols <= 32) return launch<576, 32>(p, ctas, may_split, stream);
+    return launch<576, 64>(p, ctas, may_split, stream);
+  }
+  if (cols <= 16) return launch<512, 16>(p, ctas, may_split, stream);
+  if (cols <= 32) return launch<512, 32>(p, ctas, may_split, stream);
+  return launch<512, 64>(p, ctas, may_split, stream);
 }
 
 }  // namespace fp4idx

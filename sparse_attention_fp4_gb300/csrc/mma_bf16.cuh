@@ -1,0 +1,138 @@
+// tcgen05 helpers of the bf16 attention kernels: descriptors of 128-byte-swizzled operands,
+// the bf16 MMA, tensor-memory loads and stores, cp.async and stmatrix.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace fp4idx {
+namespace mma {
+
+// Operands lie in shared memory as rows of 128 bytes (64 bf16), eight rows an atom of 1,024
+// bytes whose 16-byte pieces are stored at piece ^ (row & 7).  K-major: rows are M or N,
+// `sbo` bytes between groups of eight rows; the 16 elements of K of one MMA start 32 bytes
+// after the last one's.  M-major (the transposed use of the same bytes): rows are K, `lbo`
+// bytes between runs of 64 M, `sbo` between groups of eight K.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
+         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// kind::f16: D f32, A and B bf16; a_m_major: A is stored with M contiguous.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_m_major, bool b_n_major) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_m_major ? 1u : 0u) << 15) | ((b_n_major ? 1u : 0u) << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] x B[smem]^T, issued by one thread.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory offset of 16-byte piece `piece` of row `row` of a swizzled block.
+__device__ __forceinline__ uint32_t sw128(uint32_t row, uint32_t piece) {
+  return row * 128 + ((piece ^ (row & 7)) << 4);
+}
+
+// 16 bytes from global to shared memory, or 16 zero bytes (`bytes` = 0: nothing is read).
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Four 8x8 b16 matrices, each stored transposed: lane l gives the address of row l % 8 of
+// matrix l / 8; register i of lane l holds elements (row l / 4, cols 2 (l % 4) + {0, 1}) of
+// matrix i before the transposition.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Whether any of the `threads` threads at named barrier `id` has pred.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
+}
+
+#define FP4IDX_R8(o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+                     "=r"(r[o + 6]), "=r"(r[o + 7])
+// 16 lanes x 8 * kBlocks columns: v[4 j + {0, 1}] = (lane l / 4, columns 8 j + 2 (l % 4) +
+// {0, 1}), v[4 j + {2, 3}] the same columns of lane l / 4 + 8.  The load and its wait are one
+// statement.
+template <int kBlocks>
+__device__ __forceinline__ void ld_16x256b(uint32_t taddr, float* v) {
+  uint32_t r[4 * kBlocks];
+  if constexpr (kBlocks == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : FP4IDX_R8(0), FP4IDX_R8(8), FP4IDX_R8(16), FP4IDX_R8(24)
+        : "r"(taddr)
+        : "memory");
+  } else if constexpr (kBlocks == 4) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : FP4IDX_R8(0), FP4IDX_R8(8)
+        : "r"(taddr)
+        : "memory");
+  } else {
+    static_assert(kBlocks == 2, "");
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+        : FP4IDX_R8(0)
+        : "r"(taddr)
+        : "memory");
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * kBlocks; i++) v[i] = __uint_as_float(r[i]);
+}
+// 32 lanes x 16 columns, one lane a thread; the load and its wait are one statement.
+__device__ __forceinline__ void ld_32x16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : FP4IDX_R8(0), FP4IDX_R8(8)
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+#undef FP4IDX_R8
+__device__ __forceinline__ void st_32x16(uint32_t taddr, const float* v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; i++) r[i] = __float_as_uint(v[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+}  // namespace mma
+}  // namespace fp4idx
