@@ -12,10 +12,12 @@
 // and the second with M = dims contiguous.
 //
 // One persistent CTA an SM:
-//   warps 0-3   softmax: S^T from tensor memory, masks, exp2, P^T to shared memory; at the end
+//   warps 0-3   (0-7 with 64 columns, half of them each) softmax: S^T from tensor memory, masks, exp2, P^T to shared memory; at the end
 //               of a segment the output
-//   warp 4      one thread issues the MMAs
-//   warp 5      copies a segment's queries
+//   then a warp that issues the MMAs,
+//   a warp      that copies a segment's queries,
+//   a warp      that walks kAhead tiles ahead of the softmax and prefetches their tokens into L2, so
+//               that two stages in shared memory suffice to stream from HBM
 //   the others  groups of four warps, one per stage, copy tiles with 16-byte cp.async (rows of
 //               listed tokens or of a page; tokens that no row sees become zero rows)
 // The work is the list of all units' tiles (a unit: one row, or adjacent rows of a sequence,
@@ -44,9 +46,9 @@ constexpr int kTile = 64;         // tokens a tile: one page
 constexpr int kMaxCtas = 160;     // slots of the workspace
 constexpr int kCols = 64;         // columns of a workspace slot
 constexpr int kValue = FP4IDX_LATENT_VALUE;
-constexpr int kMmaWarp = 4;
-constexpr int kQueryWarp = 5;
-constexpr int kLoadWarp = 6;      // first loader warp
+// roles behind the softmax warps
+constexpr int kMmaRole = 0, kQueryRole = 1, kAheadRole = 2, kLoadRole = 3;
+constexpr uint32_t kAhead = 5;    // tiles that the prefetches are ahead of the softmax
 constexpr int kMaxGroup = 8;      // rows a unit
 constexpr float kRaise = 8.f;
 
@@ -255,6 +257,9 @@ struct Shape {
   static constexpr uint32_t kQChunk = kN * 128;
   // a third stage where it fits (width 512 with at most 16 columns)
   static constexpr int kStages = 3 * kStageBytes + (kChunks + 1) * kQChunk <= 225 * 1024 ? 3 : 2;
+  static constexpr int kSoftWarps = kN == 64 ? 8 : 4;
+  static constexpr int kMmaWarp = kSoftWarps + kMmaRole, kQueryWarp = kSoftWarps + kQueryRole;
+  static constexpr int kAheadWarp = kSoftWarps + kAheadRole, kLoadWarp = kSoftWarps + kLoadRole;
   static constexpr int kThreads = (kLoadWarp + 4 * kStages) * 32;
   static constexpr uint32_t kOffQ = kStages * kStageBytes;
   static constexpr uint32_t kOffP = kOffQ + kChunks * kQChunk;
@@ -274,7 +279,9 @@ struct Shape {
 template <int kWidth, int kN>
 __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ Params p) {
   using S = Shape<kWidth, kN>;
-  constexpr int kStages = S::kStages, kChunks = S::kChunks, kJ = kN / 8;
+  constexpr int kStages = S::kStages, kChunks = S::kChunks, kSoft = S::kSoftWarps * 32;
+  constexpr int kMmaWarp = S::kMmaWarp, kQueryWarp = S::kQueryWarp, kAheadWarp = S::kAheadWarp, kLoadWarp = S::kLoadWarp;
+  constexpr int kMyCols = kN * 4 / S::kSoftWarps, kJ = kMyCols / 8;  // columns of a softmax warp
   extern __shared__ uint8_t smem_raw[];
   const LatentArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -301,9 +308,10 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::mbar_init(qempty, 1);
     ptx::mbar_init(sfull(0), 1);
     ptx::mbar_init(sfull(1), 1);
-    ptx::mbar_init(pfull, 128);
+    ptx::mbar_init(pfull, kSoft);
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
+    *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = 0;  // tiles that the softmax has begun
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
@@ -341,9 +349,15 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         t = seg.t0 + n;
       }
     };
-    const uint16_t* src[4];
-    uint32_t seen[4];  // rows of the unit that see the thread's tokens
-    auto look_up = [&]() {
+    // A tile's tokens are looked up two steps ahead: positions, then page ids; each value is
+    // used an iteration after its load was issued.
+    int pos1[4], pos2[4];        // of the group's next tile, and of the one after it
+    uint32_t rows1[4], rows2[4];  // rows of the unit that see the token, if its position is valid
+    int32_t page1[4];
+    int seq2 = 0;
+    bool have1 = false;
+    auto positions = [&]() {  // of the walker's tile
+      seq2 = seg.u.seq;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         int pos = t * kTile + wrow + g * 4;
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         if (a.idx) {
           if (pos < seg.u.min_len) {
             pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
-            rows = pos >= 0;
+            rows = 1;
           }
         } else if (pos < seg.u.min_len) {
           rows = (1u << seg.u.rows) - 1;
@@ -362,45 +376,65 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
             rows |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos) << r;
           }
         }
-        src[g] = a.cache;
-        seen[g] = 0;
-        if (rows) {
-          if (pos / kPage >= a.max_pages) {
-            record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+        pos2[g] = pos;
+        rows2[g] = rows;
+      }
+    };
+    auto pages = [&]() {
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        pos1[g] = pos2[g];
+        rows1[g] = rows2[g] && pos2[g] >= 0 ? rows2[g] : 0;
+        page1[g] = -1;
+        if (rows1[g]) {
+          if (pos1[g] / kPage < a.max_pages) {
+            page1[g] = a.page_table[(int64_t)seq2 * a.max_pages + pos1[g] / kPage];
           } else {
-            const int32_t page = a.page_table[(int64_t)seg.u.seq * a.max_pages + pos / kPage];
-            if (page < 0 || page >= a.num_pages) {
-              record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-            } else {
-              src[g] = a.cache + ((int64_t)page * kPage + pos % kPage) * kWidth;
-              seen[g] = rows;
-            }
+            record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+            rows1[g] = 0;
           }
         }
       }
     };
     if (have && grp > 0) advance(grp);
-    if (have) look_up();
-    while (have) {
-      const int s = kctr % kStages;
-      if (!pipe::wait_warp(kempty(s), ((kctr / kStages) & 1) ^ 1, ctl)) break;
+    uint32_t kcur = kctr;
+    if (have) {
+      have1 = true;
+      positions();
+      pages();
+      advance(kStages);
+      if (have) positions();
+    }
+    while (have1) {
+      const int s = kcur % kStages;
+      const uint16_t* src[4];
+      uint32_t bytes[4];
+      if (!pipe::wait_warp(kempty(s), ((kcur / kStages) & 1) ^ 1, ctl)) break;
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        const bool in = page1[g] >= 0 && page1[g] < a.num_pages;
+        if (!in && rows1[g]) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+        src[g] = in ? a.cache + ((int64_t)page1[g] * kPage + pos1[g] % kPage) * kWidth + piece * 8 : a.cache;
+        bytes[g] = in ? 16 : 0;
+        if (piece == 0) smem[S::kOffSeen + s * kTile + wrow + g * 4] = (uint8_t)(in ? rows1[g] : 0);
+      }
       const uint32_t dst = sb + s * S::kStageBytes;
 #pragma unroll
       for (int c = 0; c < kChunks; c++)
 #pragma unroll
         for (int g = 0; g < 4; g++)
-          mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64 + piece * 8,
-                          seen[g] ? 16 : 0);
-      if (piece == 0) {
-#pragma unroll
-        for (int g = 0; g < 4; g++) smem[S::kOffSeen + s * kTile + wrow + g * 4] = (uint8_t)seen[g];
+          mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
+      have1 = have;
+      const uint32_t kdone = kcur;
+      kcur = kctr;
+      if (have) {
+        pages();
+        advance(kStages);
+        if (have) positions();
       }
-      const uint32_t full = kfull(s);
-      advance(kStages);
-      if (have) look_up();  // while the copies are in flight
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(full);
+      ptx::mbar_arrive(kfull(kdone % kStages));
     }
     mma::cp_async_wait_all();
   } else if (any && warp == kQueryWarp) {
@@ -422,82 +456,122 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       ptx::mbar_arrive(qfull);
       ictr++;
     } while (next_seg(p, seg));
+  } else if (any && warp == kAheadWarp) {
+    // ------------------------------------------------------------ prefetches (two tokens a lane)
+    uint32_t kctr = 0;
+    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8);
+    bool on = !p.idle_producers;
+    do {
+      for (int t = seg.t0; on && t < seg.t1; t++, kctr++) {
+        if (kctr < kStages) continue;  // the loaders are at these already
+        const uint64_t t0 = ptx::globaltimer();
+        while ((int32_t)(kctr - __shfl_sync(kFull, *progress, 0)) > (int32_t)kAhead) {
+          __nanosleep(100);
+          const int stop = *ctl.abort || ptx::globaltimer() - t0 > ctl.timeout_ns;  // only a hint: no error
+          if (__shfl_sync(kFull, stop, 0)) {
+            on = false;
+            break;
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 2; g++) {
+          int pos = t * kTile + lane + 32 * g;
+          bool some = pos < (a.idx ? seg.u.min_len : seg.u.tiles * kTile) && seg.u.seq >= 0 && seg.u.seq < a.num_seqs;
+          if (some && a.idx) pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
+          if (some && pos >= 0 && pos / kPage < a.max_pages) {
+            const int32_t page = a.page_table[(int64_t)seg.u.seq * a.max_pages + pos / kPage];
+            if (page >= 0 && page < a.num_pages) {
+              const uint8_t* row = reinterpret_cast<const uint8_t*>(a.cache + ((int64_t)page * kPage + pos % kPage) * kWidth);
+#pragma unroll
+              for (int c = 0; c < kWidth * 2; c += 128) pipe::prefetch_l2(row + c);
+            }
+          }
+        }
+      }
+    } while (on && next_seg(p, seg));
   } else if (any && warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue (lane 0)
-    if (lane == 0) {
-      constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
-      constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
-      uint32_t kctr = 0, ictr = 0;
-      auto issue_s = [&](uint32_t k) {
-        ptx::tc_fence_after();
-        const uint32_t kb = sb + (k % kStages) * S::kStageBytes, qb = sb + S::kOffQ, d = tm_s + (k & 1) * kN;
+    // ------------------------------------------------------------ MMA issue (the warp as one)
+    constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
+    constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
+    const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0), pd = mma::desc_lo(sb + S::kOffP, 0);
+    uint32_t kctr = 0, ictr = 0;
+    auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(kFull, ptx::mbar_test_wait(b, parity)) != 0; };
+    auto issue_s = [&](uint32_t k, bool last) {
+      ptx::tc_fence_after();
+      const uint32_t kd = mma::desc_lo(sb + (k % kStages) * S::kStageBytes, 0), d = tm_s + (k & 1) * kN;
+      if (mma::elect_one()) {
 #pragma unroll
         for (int c = 0; c < kChunks; c++)
 #pragma unroll
           for (int i = 0; i < 4; i++)
-            mma::mma_ss(d, mma::desc_sw128(kb + c * (kTile * 128) + i * 32, 0, 1024),
-                        mma::desc_sw128(qb + c * S::kQChunk + i * 32, 0, 1024), kIdS, c | i);
+            mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS,
+                        (c | i) != 0);
         ptx::mma_commit(sfull(k & 1));
-      };
-      bool ok = true;
-      do {
-        const uint32_t n = seg.t1 - seg.t0;
-        ok = pipe::poll(qfull, ictr & 1, ctl, true);
-        uint32_t issued = 0;
-        for (uint32_t i = 0; ok && i < n; i++, kctr++) {
-          if (issued == i) {
-            ok = pipe::poll(kfull(kctr % kStages), (kctr / kStages) & 1, ctl, true);
-            if (!ok) break;
-            issue_s(kctr);
-            if (++issued == n) ptx::mma_commit(qempty);
-          }
-          // until the weights are there, the next tile's scores are issued as soon as it is
-          if (issued < n && !ptx::mbar_try_wait(pfull, kctr & 1)) {
-            const uint64_t t0 = ptx::globaltimer();
-            for (uint32_t it = 1;; it++) {
-              const uint32_t k = kctr + 1;
-              if (ptx::mbar_try_wait(kfull(k % kStages), (k / kStages) & 1)) {
-                issue_s(k);
-                if (++issued == n) ptx::mma_commit(qempty);
-                break;
-              }
-              if (ptx::mbar_try_wait(pfull, kctr & 1)) break;
-              if ((it & 63u) == 0) {
-                if (*ctl.abort) ok = false;
-                else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
-                if (!ok) break;
-              }
-            }
-            if (!ok) break;
-          }
-          ok = pipe::poll(pfull, kctr & 1, ctl, true);
+        if (last) ptx::mma_commit(qempty);
+      }
+      __syncwarp();
+    };
+    bool ok = true;
+    do {
+      const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
+      ok = pipe::wait_warp(qfull, ictr & 1, ctl);
+      uint32_t issued = 0;
+      for (uint32_t i = 0; ok && i < n; i++, kctr++) {
+        if (issued == i) {
+          ok = pipe::wait_warp(kfull(kctr % kStages), (kctr / kStages) & 1, ctl);
           if (!ok) break;
-          ptx::tc_fence_after();
-          const uint32_t vb = sb + (kctr % kStages) * S::kStageBytes, pb = sb + S::kOffP;
+          issue_s(kctr, ++issued == n);
+        }
+        // until the weights are there, the next tile's scores are issued as soon as it is
+        if (issued < n && !ready(pfull, kctr & 1)) {
+          const uint64_t t0 = ptx::globaltimer();
+          const uint32_t k = kctr + 1;
+          for (uint32_t it = 1;; it++) {
+            if (ready(kfull(k % kStages), (k / kStages) & 1)) {
+              issue_s(k, ++issued == n);
+              break;
+            }
+            if (ready(pfull, kctr & 1)) break;
+            if ((it & 63u) == 0) {
+              if (*ctl.abort) ok = false;
+              else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
+              ok = __all_sync(kFull, ok);
+              if (!ok) break;
+            }
+          }
+          if (!ok) break;
+        }
+        ok = pipe::wait_warp(pfull, kctr & 1, ctl);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t vd = mma::desc_lo(sb + (kctr % kStages) * S::kStageBytes, kTile * 128);
+        if (mma::elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ks++)
 #pragma unroll
             for (int b = 0; b < 4; b++)
-              mma::mma_ss(tmem + b * kN, mma::desc_sw128(vb + b * (2 * kTile * 128) + ks * 2048, kTile * 128, 1024),
-                          mma::desc_sw128(pb + ks * 32, 0, 1024), kIdO, i > 0 || ks > 0);
+              mma::mma_ss(tmem + b * kN, vd + ((b * (2 * kTile * 128) + ks * 2048) >> 4), pd + ((ks * 32) >> 4), kIdO,
+                          ks > 0 || i > 0);
           ptx::mma_commit(kempty(kctr % kStages));
         }
-        ictr++;
-      } while (ok && next_seg(p, seg));
-      // nothing of this CTA's may be under way in the tensor cores when it ends
-      ptx::mma_commit(done);
-      pipe::poll(done, 0, ctl, false);
-    }
+        __syncwarp();
+      }
+      ictr++;
+    } while (ok && next_seg(p, seg));
+    // nothing of this CTA's may be under way in the tensor cores when it ends
+    if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
-  } else if (any && warp < 4) {
+    pipe::wait_warp(done, 0, ctl, false);
+  } else if (any && warp < S::kSoftWarps) {
     // ------------------------------------------------------------ softmax and output
     const float cs = a.scale * 1.4426950408889634f;
     const int quad = lane & 3, r8 = lane >> 2;
-    const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+    const int qw = warp & 3, col0 = (warp >> 2) * kMyCols;  // tensor-memory quarter, first column
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
     float* red = reinterpret_cast<float*>(smem + S::kOffRed);
     float* sm_m = reinterpret_cast<float*>(smem + S::kOffM);
     float* sm_f = reinterpret_cast<float*>(smem + S::kOffF);
-    const int tok = warp * 16 + r8;  // and tok + 8
+    const int tok = qw * 16 + r8;  // and tok + 8
     uint32_t kctr = 0;
     bool ok = true, first_of_cta = true;
     do {
@@ -514,9 +588,10 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         // a warp whose wait ran out goes on to the next vote, so that all four leave together
         ok = ok && pipe::wait_warp(kfull(st), (kctr / kStages) & 1, ctl) &&
              pipe::wait_warp(sfull(kctr & 1), (kctr >> 1) & 1, ctl);
+        if (threadIdx.x == 0) *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = kctr;
         ptx::tc_fence_after();
         float v[4 * kJ];
-        mma::ld_16x256b<kJ>(tm_s + (kctr & 1) * kN + lanes, v);
+        mma::ld_16x256b<kJ>(tm_s + (kctr & 1) * kN + col0 + lanes, v);
         const uint32_t see0 = smem[S::kOffSeen + st * kTile + tok], see1 = smem[S::kOffSeen + st * kTile + tok + 8];
         if (!__all_sync(kFull, see0 == everyone && see1 == everyone)) {
           if (seg.u.rows > 1) {
@@ -541,7 +616,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           }
 #pragma unroll
           for (int j = 0; j < kJ; j++) {
-            const int r = 8 * j / p.hp;
+            const int r = (col0 + 8 * j) / p.hp;
             const bool in0 = (see0 >> r) & 1, in1 = (see1 >> r) & 1;
             v[4 * j] = in0 ? v[4 * j] * cs : -INFINITY;
             v[4 * j + 1] = in0 ? v[4 * j + 1] * cs : -INFINITY;
@@ -558,9 +633,9 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           above = above || fmaxf(v[4 * j], v[4 * j + 2]) > m[2 * j] + kRaise ||
                   fmaxf(v[4 * j + 1], v[4 * j + 3]) > m[2 * j + 1] + kRaise;
         }
-        const bool raise = mma::bar_any(1, 128, above);
+        const bool raise = mma::bar_any(1, kSoft, above);
         if (raise) {
-          if (mma::bar_any(1, 128, !ok)) {
+          if (mma::bar_any(1, kSoft, !ok)) {
             ok = false;
             break;
           }
@@ -572,24 +647,24 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-              if (r8 == 0) red[warp * kN + 8 * j + 2 * quad + e] = x;
+              if (r8 == 0) red[qw * kN + col0 + 8 * j + 2 * quad + e] = x;
             }
           }
-          ptx::named_bar_sync(1, 128);
+          ptx::named_bar_sync(1, kSoft);
 #pragma unroll
           for (int j = 0; j < kJ; j++) {
 #pragma unroll
             for (int e = 0; e < 2; e++) {
-              const int c = 8 * j + 2 * quad + e;
+              const int c = col0 + 8 * j + 2 * quad + e;
               const float x = fmaxf(fmaxf(red[c], red[kN + c]), fmaxf(red[2 * kN + c], red[3 * kN + c]));
               const float m1 = fmaxf(m[2 * j + e], x);
               const float f = m1 == m[2 * j + e] ? 1.f : mma::exp2_approx(m[2 * j + e] - m1);
-              if (warp == 0 && r8 == 0) sm_f[c] = f;
+              if (qw == 0 && r8 == 0) sm_f[c] = f;
               l[2 * j + e] *= f;
               m[2 * j + e] = m1;
             }
           }
-          ptx::named_bar_sync(1, 128);  // red is read, sm_f is written
+          ptx::named_bar_sync(1, kSoft);  // red is read, sm_f is written
         }
         uint32_t pk[2 * kJ];
 #pragma unroll
@@ -612,26 +687,27 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           if (i > 0) {
             ptx::tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < 4 * kN; b += 16) {
+            for (int b = 0; b < 4 * kMyCols; b += 16) {
+              const int c = col0 + b % kMyCols, at = b / kMyCols * kN + c;
               float o[16];
-              mma::ld_32x16(tmem + b + lanes, o);
+              mma::ld_32x16(tmem + at + lanes, o);
 #pragma unroll
-              for (int e = 0; e < 16; e++) o[e] *= sm_f[(b % kN) + e];
-              mma::st_32x16(tmem + b + lanes, o);
+              for (int e = 0; e < 16; e++) o[e] *= sm_f[c + e];
+              mma::st_32x16(tmem + at + lanes, o);
             }
             ptx::tmem_wait_st();
           }
         }
 #pragma unroll
         for (int j = 0; j < kJ; j += 2) {
-          const int col = 8 * (j + (lane >> 4)) + (lane & 7), tb = 2 * warp + ((lane >> 3) & 1);
+          const int col = col0 + 8 * (j + (lane >> 4)) + (lane & 7), tb = 2 * qw + ((lane >> 3) & 1);
           mma::stmatrix_x4_trans(sb + S::kOffP + mma::sw128(col, tb), pk[2 * j], pk[2 * j + 1], pk[2 * j + 2], pk[2 * j + 3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         ptx::mbar_arrive(pfull);
       }
-      if (mma::bar_any(1, 128, !ok)) break;
+      if (mma::bar_any(1, kSoft, !ok)) break;
       // ---- the segment's output
       const bool begins = seg.t0 == 0, ends = seg.t1 == seg.u.tiles, whole = begins && ends;
 #pragma unroll
@@ -639,11 +715,11 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         l[j] += __shfl_xor_sync(kFull, l[j], 4);
         l[j] += __shfl_xor_sync(kFull, l[j], 8);
         l[j] += __shfl_xor_sync(kFull, l[j], 16);
-        const int c = 8 * (j >> 1) + 2 * quad + (j & 1);
-        if (r8 == 0) red[warp * kN + c] = l[j];
-        if (r8 == 0 && warp == 0) sm_m[c] = m[j];
+        const int c = col0 + 8 * (j >> 1) + 2 * quad + (j & 1);
+        if (r8 == 0) red[qw * kN + c] = l[j];
+        if (r8 == 0 && qw == 0) sm_m[c] = m[j];
       }
-      ptx::named_bar_sync(1, 128);
+      ptx::named_bar_sync(1, kSoft);
       const int slot = 2 * blockIdx.x + (first_of_cta ? 0 : 1);
       first_of_cta = false;
       if (threadIdx.x < kN) {
@@ -664,28 +740,45 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
       ok = pipe::wait_warp(kempty(last % kStages), (last / kStages) & 1, ctl);
-      if (mma::bar_any(1, 128, !ok)) break;
+      if (mma::bar_any(1, kSoft, !ok)) break;
       ptx::tc_fence_after();
+      // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
+      if (whole) {
 #pragma unroll 1
-      for (int b = 0; b < 4 * kN; b += 16) {
-        float o[16];
-        mma::ld_32x16(tmem + b + lanes, o);
-        const int dim = (b / kN) * 128 + warp * 32 + lane;
+        for (int r = 0; r < seg.u.rows; r++) {
+          const int head0 = seg.hb * p.hs, heads = min(p.hs, a.heads - head0);
+          uint16_t* dst = a.out + ((int64_t)(seg.u.r0 + r) * a.heads + head0) * kValue + qw * 32 + lane;
+#pragma unroll 1
+          for (int h = (warp >> 2) * 8; h < heads; h += 2 * S::kSoftWarps) {
+            const int c = r * p.hp + h;
+            float f[8];
 #pragma unroll
-        for (int e = 0; e < 16; e++) {
-          const int c = (b % kN) + e;
-          if (whole) {
-            const int r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
-            if (r < seg.u.rows && h < p.hs && head < a.heads)
-              a.out[((int64_t)(seg.u.r0 + r) * a.heads + head) * kValue + dim] =
-                  (uint16_t)mma::pack_bf16(o[e] * sm_f[c], 0.f);
-          } else {
-            wk.o[((int64_t)slot * kCols + c) * kValue + dim] = o[e];
+            for (int e = 0; e < 8; e++) f[e] = sm_f[c + e];
+#pragma unroll
+            for (int b = 0; b < 4; b++) {
+              float o[8];
+              mma::ld_32x8(tmem + b * kN + c + lanes, o);
+#pragma unroll
+              for (int e = 0; e < 8; e++)
+                if (h + e < heads) dst[(h + e) * kValue + b * 128] = (uint16_t)mma::pack_bf16(o[e] * f[e], 0.f);
+            }
+          }
+        }
+      } else {
+        float* dst = wk.o + (int64_t)slot * kCols * kValue + qw * 32 + lane;
+#pragma unroll 1
+        for (int c = col0; c < col0 + kMyCols; c += 8) {
+#pragma unroll
+          for (int b = 0; b < 4; b++) {
+            float o[8];
+            mma::ld_32x8(tmem + b * kN + c + lanes, o);
+#pragma unroll
+            for (int e = 0; e < 8; e++) dst[(c + e) * kValue + b * 128] = o[e];
           }
         }
       }
       ptx::tc_fence_before();
-      ptx::named_bar_sync(1, 128);  // red, sm_m and sm_f are free again
+      ptx::named_bar_sync(1, kSoft);  // red, sm_m and sm_f are free again
     } while (next_seg(p, seg));
   }
   ptx::tc_fence_before();

@@ -9,25 +9,38 @@ namespace mma {
 
 // Operands lie in shared memory as rows of 128 bytes (64 bf16), eight rows an atom of 1,024
 // bytes whose 16-byte pieces are stored at piece ^ (row & 7).  K-major: rows are M or N,
-// `sbo` bytes between groups of eight rows; the 16 elements of K of one MMA start 32 bytes
-// after the last one's.  M-major (the transposed use of the same bytes): rows are K, `lbo`
-// bytes between runs of 64 M, `sbo` between groups of eight K.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
+// 1,024 bytes (sbo) between groups of eight rows; the 16 elements of K of one MMA start 32
+// bytes after the last one's.  M-major (the transposed use of the same bytes): rows are K,
+// `lbo` bytes between runs of 64 M, 1,024 (sbo) between groups of eight K.
+//
+// A descriptor is kept as its low word (address and lbo) and its constant high word, so that
+// the step from one MMA to the next is one 32-bit addition of a constant: descriptors built
+// from addresses each time cost the issuing thread some 15 cycles an MMA.  The issuing warp
+// runs as one, with warp-uniform descriptors, and elects a thread for each burst: issued
+// from a branch of one lane, an MMA takes 46 cycles whatever its size, since the operands
+// then go through per-thread registers.  Measured for K = 16 and M x N on one SM: 64x16 24
+// cycles, 64x64 33, 128x64 48, 64x128 and 128x128 63, 128x256 123.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // sbo 1,024, version, 128-byte swizzle
 // kind::f16: D f32, A and B bf16; a_m_major: A is stored with M contiguous.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_m_major, bool b_n_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | ((a_m_major ? 1u : 0u) << 15) | ((b_n_major ? 1u : 0u) << 16) |
          ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
+// One thread of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 // D[tmem] (+)= A[smem] x B[smem]^T, issued by one thread.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"((uint32_t)accumulate), "r"(kDescHi)
       : "memory");
 }
 
@@ -120,6 +133,17 @@ __device__ __forceinline__ void ld_32x16(uint32_t taddr, float* v) {
       : "memory");
 #pragma unroll
   for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
+}
+// 32 lanes x 8 columns.
+__device__ __forceinline__ void ld_32x8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : FP4IDX_R8(0)
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
 }
 #undef FP4IDX_R8
 __device__ __forceinline__ void st_32x16(uint32_t taddr, const float* v) {
