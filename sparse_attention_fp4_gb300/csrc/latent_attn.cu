@@ -21,7 +21,7 @@
 //   the others  groups of four warps, one per stage, copy tiles with 16-byte cp.async (rows of
 //               listed tokens or of a page; tokens that no row sees become zero rows)
 // The work is the list of all units' tiles (a unit: one row, or adjacent rows of a sequence,
-// and up to 64 columns), cut into equal runs of tiles, one a CTA, whatever the lengths are.
+// and up to 64 columns), cut into runs of tiles, one a CTA, whatever the lengths are.
 // A unit cut between CTAs leaves each piece's unnormalised output, maximum and sum in the
 // workspace; combine_kernel joins them in order (the same bits every time).
 //
@@ -154,13 +154,27 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s) {
 }
 
 // ---------------------------------------------------------------- the CTA's run
-// All threads: finds the CTA's first unit and tile.  Rows are taken blockDim.x at a time; the
-// first pass sums the tiles, the second finds the run's start.
+// All threads find the CTA's first unit and tile.  Rows are taken blockDim.x at a time.
+//
+// Up to one unit a CTA, where that balances: each unit gets CTAs of its own, as many as it
+// takes for no CTA to have more than `most` tiles.  A CTA then has one piece, and 64 units of
+// 32 tiles make 128 pieces for the joining kernel instead of the 304 of an even cut over 152
+// CTAs (a piece's end costs as much as two tiles, and its 128 KB are written and read again).
+// Taken when `most` is at most an even share plus 1/16 and three tiles.
+// Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
+// edge moves to the edge (no piece then, for 1/20 more work).
+constexpr int kMaxWarps = 20;
 struct ScanShared {
-  int64_t sums[32];
-  int32_t starts[32];
-  int32_t found_row;
-  int64_t found_off;
+  int64_t sums[kMaxWarps];
+  int32_t starts[kMaxWarps];
+  int32_t enough[kMaxWarps];
+  int32_t tiles[kMaxWarps * 32];
+  Unit unit;
+  int32_t found_row, found_hb, found_t0, found_left;
+  int64_t cut[2];
+};
+struct Weight {
+  int32_t tiles, rows;  // of the unit that starts at the thread's row; 0 tiles: none does
 };
 __device__ __forceinline__ int64_t block_scan(int64_t v, ScanShared& sh, int64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -171,19 +185,19 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, ScanShared& sh, int64_t
   }
   if (lane == 31) sh.sums[warp] = v;
   __syncthreads();
-  int64_t before = 0;
-  total = 0;
-  for (int w = 0; w < warps; w++) {
-    const int64_t s = sh.sums[w];
-    if (w < warp) before += s;
-    total += s;
+  int64_t s = lane < warps ? sh.sums[lane] : 0;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t u = __shfl_up_sync(kFull, s, d);
+    if (lane >= d) s += u;
   }
+  total = __shfl_sync(kFull, s, 31);
+  const int64_t before = __shfl_sync(kFull, s, (warp + 31) & 31);
   __syncthreads();
-  return before + v;
+  return (warp ? before : 0) + v;
 }
-// Tiles (over all head blocks) of the unit that starts at row base + threadIdx.x, 0 if none
-// does; `run` carries the first row of the last run of one sequence from chunk to chunk.
-__device__ __forceinline__ int64_t unit_weight(const Params& p, int base, int& run, ScanShared& sh, bool report) {
+// `run` carries the first row of the last run of one sequence from chunk to chunk.
+__device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& run, ScanShared& sh, bool report) {
   const int t = base + (int)threadIdx.x;
   const bool in = t < p.a.n_rows;
   bool starts = in;
@@ -207,44 +221,96 @@ __device__ __forceinline__ int64_t unit_weight(const Params& p, int base, int& r
     run = last;
     starts = in && (t - first) % p.group == 0;
   }
-  if (!starts) return 0;
+  if (!starts) return Weight{0, 0};
   Unit u;
   load_unit(p, t, u, report);
-  return (int64_t)u.tiles * p.hb;
+  return Weight{u.tiles, u.rows};
 }
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
   const bool report = blockIdx.x == 0;
-  int64_t all = 0, w = 0, incl = 0, total;
+  int64_t all = 0, incl = 0, total;
   int run = -1;
+  Weight w{0, 0};
   for (int base = 0; base < n; base += step) {
     w = unit_weight(p, base, run, sh, report);
-    incl = block_scan(w, sh, total);
+    incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
     all += total;
   }
-  const int64_t runs = min((int64_t)gridDim.x, all);  // at least one tile each
-  if (blockIdx.x >= runs) return false;
-  const int64_t lo = all * blockIdx.x / runs, hi = all * (blockIdx.x + 1) / runs;
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  if (n <= step) {
+    sh.tiles[threadIdx.x] = w.tiles;
+    const int units = __syncthreads_count(w.tiles > 0) * p.hb;
+    if (units <= ctas) {
+      // each warp tries one number of tiles a CTA
+      const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = step >> 5;
+      const int least = (int)((all + ctas - 1) / ctas), span = (int)(all / ctas / 16) + 3;
+      const int gap = (span + warps - 1) / warps;
+      const int mine = least + warp * gap;
+      int need = 0;
+      for (int t = lane; t < n; t += 32) need += (sh.tiles[t] + mine - 1) / mine;
+      need = __reduce_add_sync(kFull, need) * p.hb;
+      if (lane == 0) sh.enough[warp] = need <= ctas;
+      __syncthreads();
+      const uint32_t yes = __ballot_sync(kFull, lane < warps && sh.enough[lane]);
+      if (yes) {
+        const int most = least + (__ffs(yes) - 1) * gap;
+        const int per = (w.tiles + most - 1) / most;
+        const int64_t end = block_scan((int64_t)per * p.hb, sh, total), begin = end - (int64_t)per * p.hb;
+        if (cta >= total) return false;
+        if (cta >= begin && cta < end) {
+          const int k = cta - (int)begin, j = k % per;
+          load_unit(p, threadIdx.x, sh.unit, false);
+          sh.found_hb = k / per;
+          sh.found_t0 = (int)((int64_t)w.tiles * j / per);
+          sh.found_left = (int)((int64_t)w.tiles * (j + 1) / per) - sh.found_t0;
+        }
+        __syncthreads();
+        s.u = sh.unit;
+        s.hb = sh.found_hb;
+        s.t0 = sh.found_t0;
+        s.left = sh.found_left;
+        s.t1 = s.t0 + sh.found_left;
+        return true;
+      }
+    }
+  }
+  if (threadIdx.x == 0) sh.cut[1] = all;
+  const int64_t x0 = all * cta / ctas, x1 = all * (cta + 1) / ctas, near = all / ctas / 20;
   int64_t carry = 0;
   run = -1;
+  __syncthreads();
   for (int base = 0; base < n; base += step) {
     if (n > step) {
       w = unit_weight(p, base, run, sh, false);
-      incl = block_scan(w, sh, total);
+      incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
     }
-    const int64_t end = carry + incl;
-    if (lo < end && lo >= end - w) {
-      sh.found_row = base + threadIdx.x;
-      sh.found_off = lo - (end - w);
+    const int64_t end = carry + incl, begin = end - (int64_t)w.tiles * p.hb;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      int64_t x = i ? x1 : x0;
+      if (x < begin || x >= end) continue;
+      const int off = (int)((x - begin) % w.tiles);
+      if (off <= near) x -= off;
+      else if (w.tiles - off <= near) x += w.tiles - off;
+      sh.cut[i] = x;
+      if (i == 0) {
+        const int64_t at = x - begin;
+        const bool past = x == end;
+        sh.found_row = base + (int)threadIdx.x + (past ? w.rows : 0);
+        sh.found_hb = past ? 0 : (int)(at / w.tiles);
+        sh.found_t0 = past ? 0 : (int)(at % w.tiles);
+      }
     }
     carry += total;
-    if (lo < carry) break;
+    if (x1 < carry) break;
   }
   __syncthreads();
+  s.left = sh.cut[1] - sh.cut[0];
+  if (s.left <= 0) return false;
   load_unit(p, sh.found_row, s.u, false);
-  s.hb = (int)(sh.found_off / s.u.tiles);
-  s.t0 = (int)(sh.found_off % s.u.tiles);
-  s.left = hi - lo;
+  s.hb = sh.found_hb;
+  s.t0 = sh.found_t0;
   s.t1 = (int)min((int64_t)s.u.tiles, s.t0 + s.left);
   return true;
 }
@@ -268,8 +334,8 @@ struct Shape {
   static constexpr uint32_t kOffM = kOffRed + 4 * kN * 4;          // [kN]
   static constexpr uint32_t kOffF = kOffM + kN * 4;                // [kN]
   static constexpr uint32_t kOffBar = kOffF + kN * 4;
-  // kfull[stages], kempty[stages], qfull, qempty, sfull[2], pfull, done
-  static constexpr int kBars = 2 * kStages + 6;
+  // kfull[stages][2], kempty[stages][2], qfull, qempty, sfull[2], pfull, done
+  static constexpr int kBars = 4 * kStages + 6;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
   static constexpr uint32_t kBytes = kOffMisc + 16 + 1024;  // and the base's alignment
   static constexpr uint32_t kTmemCols = kN == 64 ? 512 : kN == 32 ? 256 : 128;
@@ -289,20 +355,23 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
   const uint32_t sb = ptx::smem_addr(smem);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + S::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc + 4);
   auto bar = [&](int i) { return sb + S::kOffBar + i * 8; };
-  const auto kfull = [&](int s) { return bar(s); };
-  const auto kempty = [&](int s) { return bar(kStages + s); };
-  const uint32_t qfull = bar(2 * kStages), qempty = bar(2 * kStages + 1), pfull = bar(2 * kStages + 4),
-                 done = bar(2 * kStages + 5);
-  const auto sfull = [&](int b) { return bar(2 * kStages + 2 + b); };
+  // A stage is filled and freed in two halves, dims 0..255 and the rest, so that the scores'
+  // product begins while the second half is on its way, and the next tile's first half is
+  // copied while the output's second half is computed.
+  const auto kfull = [&](int s, int half) { return bar(2 * s + half); };
+  const auto kempty = [&](int s, int half) { return bar(2 * (kStages + s) + half); };
+  const uint32_t qfull = bar(4 * kStages), qempty = bar(4 * kStages + 1), pfull = bar(4 * kStages + 4),
+                 done = bar(4 * kStages + 5);
+  const auto sfull = [&](int b) { return bar(4 * kStages + 2 + b); };
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
-      ptx::mbar_init(kfull(s), 128);
-      ptx::mbar_init(kempty(s), 1);
+      for (int half = 0; half < 2; half++) {
+        ptx::mbar_init(kfull(s, half), 128);
+        ptx::mbar_init(kempty(s, half), 1);
+      }
     }
     ptx::mbar_init(qfull, 32);
     ptx::mbar_init(qempty, 1);
@@ -315,6 +384,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Seg seg;
   const bool any = first_seg(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
   Work wk = work_view(a.workspace);
@@ -409,7 +480,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       const int s = kcur % kStages;
       const uint16_t* src[4];
       uint32_t bytes[4];
-      if (!pipe::wait_warp(kempty(s), ((kcur / kStages) & 1) ^ 1, ctl)) break;
+      const uint32_t free = ((kcur / kStages) & 1) ^ 1;
+      if (!pipe::wait_warp(kempty(s, 0), free, ctl)) break;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         const bool in = page1[g] >= 0 && page1[g] < a.num_pages;
@@ -420,10 +492,16 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       }
       const uint32_t dst = sb + s * S::kStageBytes;
 #pragma unroll
-      for (int c = 0; c < kChunks; c++)
+      for (int c = 0; c < kChunks; c++) {
+        if (c == 4) {
+          mma::cp_async_commit();
+          if (!pipe::wait_warp(kempty(s, 1), free, ctl)) break;
+        }
 #pragma unroll
         for (int g = 0; g < 4; g++)
           mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
+      }
+      mma::cp_async_commit();
       have1 = have;
       const uint32_t kdone = kcur;
       kcur = kctr;
@@ -432,9 +510,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         advance(kStages);
         if (have) positions();
       }
-      mma::cp_async_wait_all();
+      mma::cp_async_wait_group<1>();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(kfull(kdone % kStages));
+      ptx::mbar_arrive(kfull(kdone % kStages, 0));
+      mma::cp_async_wait_group<0>();
+      ptx::fence_proxy_async_smem();
+      ptx::mbar_arrive(kfull(kdone % kStages, 1));
     }
     mma::cp_async_wait_all();
   } else if (any && warp == kQueryWarp) {
@@ -496,18 +577,27 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0), pd = mma::desc_lo(sb + S::kOffP, 0);
     uint32_t kctr = 0, ictr = 0;
     auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(kFull, ptx::mbar_test_wait(b, parity)) != 0; };
-    auto issue_s = [&](uint32_t k, bool last) {
+    // the scores' product of tile k over one half of the dims
+    auto issue_s = [&](uint32_t k, int half, bool last) {
       ptx::tc_fence_after();
       const uint32_t kd = mma::desc_lo(sb + (k % kStages) * S::kStageBytes, 0), d = tm_s + (k & 1) * kN;
       if (mma::elect_one()) {
+        if (half == 0) {
 #pragma unroll
-        for (int c = 0; c < kChunks; c++)
+          for (int c = 0; c < 4; c++)
 #pragma unroll
-          for (int i = 0; i < 4; i++)
-            mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS,
-                        (c | i) != 0);
-        ptx::mma_commit(sfull(k & 1));
-        if (last) ptx::mma_commit(qempty);
+            for (int i = 0; i < 4; i++)
+              mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS,
+                          (c | i) != 0);
+        } else {
+#pragma unroll
+          for (int c = 4; c < kChunks; c++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+              mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS, true);
+          ptx::mma_commit(sfull(k & 1));
+          if (last) ptx::mma_commit(qempty);
+        }
       }
       __syncwarp();
     };
@@ -515,44 +605,40 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     do {
       const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
       ok = pipe::wait_warp(qfull, ictr & 1, ctl);
-      uint32_t issued = 0;
+      uint32_t halves = 0;  // halves of scores issued in this segment
       for (uint32_t i = 0; ok && i < n; i++, kctr++) {
-        if (issued == i) {
-          ok = pipe::wait_warp(kfull(kctr % kStages), (kctr / kStages) & 1, ctl);
-          if (!ok) break;
-          issue_s(kctr, ++issued == n);
-        }
-        // until the weights are there, the next tile's scores are issued as soon as it is
-        if (issued < n && !ready(pfull, kctr & 1)) {
-          const uint64_t t0 = ptx::globaltimer();
-          const uint32_t k = kctr + 1;
-          for (uint32_t it = 1;; it++) {
-            if (ready(kfull(k % kStages), (k / kStages) & 1)) {
-              issue_s(k, ++issued == n);
-              break;
-            }
-            if (ready(pfull, kctr & 1)) break;
-            if ((it & 63u) == 0) {
-              if (*ctl.abort) ok = false;
-              else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
-              ok = __all_sync(kFull, ok);
-              if (!ok) break;
-            }
+        // This tile's scores, if they have not been issued; then, until its weights are there,
+        // the next tile's scores as their halves land.
+        const uint64_t t0 = ptx::globaltimer();
+        for (uint32_t it = 1;; it++) {
+          const uint32_t next = halves >> 1, k = kctr - i + next;
+          if (next > i && ready(pfull, kctr & 1)) break;
+          if (next < n && next <= i + 1 && ready(kfull(k % kStages, halves & 1), (k / kStages) & 1)) {
+            issue_s(k, halves & 1, next + 1 == n);
+            halves++;
+            continue;
           }
-          if (!ok) break;
+          if ((it & 63u) == 0) {
+            if (*ctl.abort) ok = false;
+            else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
+            ok = __all_sync(kFull, ok);
+            if (!ok) break;
+          }
         }
-        ok = pipe::wait_warp(pfull, kctr & 1, ctl);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t vd = mma::desc_lo(sb + (kctr % kStages) * S::kStageBytes, kTile * 128);
         if (mma::elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ks++)
+          for (int half = 0; half < 2; half++) {
 #pragma unroll
-            for (int b = 0; b < 4; b++)
-              mma::mma_ss(tmem + b * kN, vd + ((b * (2 * kTile * 128) + ks * 2048) >> 4), pd + ((ks * 32) >> 4), kIdO,
-                          ks > 0 || i > 0);
-          ptx::mma_commit(kempty(kctr % kStages));
+            for (int ks = 0; ks < 4; ks++)
+#pragma unroll
+              for (int b = 2 * half; b < 2 * half + 2; b++)
+                mma::mma_ss(tmem + b * kN, vd + ((b * (2 * kTile * 128) + ks * 2048) >> 4), pd + ((ks * 32) >> 4), kIdO,
+                            ks > 0 || i > 0);
+            ptx::mma_commit(kempty(kctr % kStages, half));
+          }
         }
         __syncwarp();
       }
@@ -586,7 +672,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       for (int i = 0; i < n; i++, kctr++) {
         const int st = kctr % kStages;
         // a warp whose wait ran out goes on to the next vote, so that all four leave together
-        ok = ok && pipe::wait_warp(kfull(st), (kctr / kStages) & 1, ctl) &&
+        ok = ok && pipe::wait_warp(kfull(st, 0), (kctr / kStages) & 1, ctl) &&
              pipe::wait_warp(sfull(kctr & 1), (kctr >> 1) & 1, ctl);
         if (threadIdx.x == 0) *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = kctr;
         ptx::tc_fence_after();
@@ -680,7 +766,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         // the last tile's product has read P^T, and the output may be rescaled
         if (kctr > 0) {
           const uint32_t last = kctr - 1;
-          ok = pipe::wait_warp(kempty(last % kStages), (last / kStages) & 1, ctl);
+          ok = pipe::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
           if (!ok) continue;
         }
         if (raise) {
@@ -739,7 +825,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (!whole && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
-      ok = pipe::wait_warp(kempty(last % kStages), (last / kStages) & 1, ctl);
+      ok = pipe::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
@@ -789,24 +875,31 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
 
 // ---------------------------------------------------------------- joining the pieces
 // Block (c, y): the unit whose first piece is CTA c's, columns 8 y .. 8 y + 7; its next pieces
-// are the first segments of the CTAs that follow.  Three groups of eight warps take the pieces
-// in turn, a warp one column; the groups' sums are added in order.
-constexpr int kJoinGroups = 3, kJoinThreads = kJoinGroups * 256;
-__global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p, int ctas) {
-  __shared__ float sh_o[kJoinGroups - 1][8][kValue];
+// are the first segments of the CTAs that follow.  kGroups groups of eight warps take the
+// pieces in turn, a warp one column; the groups' sums are added in order.  One group where
+// units have few pieces (then all blocks are resident at once), four where they have many.
+template <int kGroups>
+__global__ void __launch_bounds__(kGroups * 256) combine_kernel(const Params p, int ctas) {
+  __shared__ float sh_o[kGroups > 1 ? kGroups - 1 : 1][8][kGroups > 1 ? 256 : 1];
   __shared__ int sh_last;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const LatentArgs& a = p.a;
   const Work wk = work_view(a.workspace);
   const int c0 = blockIdx.x;
+  const int cx = c0 + 1 + (int)threadIdx.x;
+  // the unit's last piece: asked for by all threads at once, before the first is looked at
+  const int flags = cx < ctas ? wk.rec[2 * cx].flags : 0;
   int slot0 = 2 * c0 + 1;
   Record rec = wk.rec[slot0];
-  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) rec = wk.rec[--slot0];
+  const Record rec0 = wk.rec[slot0 - 1];
+  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) {
+    rec = rec0;
+    slot0--;
+  }
   if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) return;
   if (threadIdx.x == 0) sh_last = ctas;
   __syncthreads();
-  const int cx = c0 + 1 + (int)threadIdx.x;
-  if (cx < ctas && (wk.rec[2 * cx].flags & (kUsed | kBegins | kEnds)) == (kUsed | kEnds)) atomicMin(&sh_last, cx);
+  if ((flags & (kUsed | kBegins | kEnds)) == (kUsed | kEnds)) atomicMin(&sh_last, cx);
   __syncthreads();
   if (sh_last >= ctas) return;  // a run that gave up
   const int n = sh_last - c0 + 1;
@@ -829,7 +922,7 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p, i
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
 #pragma unroll 2
-    for (int i = grp; i < n; i += kJoinGroups) {
+    for (int i = grp; i < n; i += kGroups) {
       const int s = slot_of(i);
       const float f = mma::exp2_approx(wk.ml[s * 2 * kCols + col] - top);
       const float4* x = reinterpret_cast<const float4*>(wk.o + ((int64_t)s * kCols + col) * kValue) + lane;
@@ -843,30 +936,39 @@ __global__ void __launch_bounds__(kJoinThreads) combine_kernel(const Params p, i
       }
     }
   }
-  if (grp > 0) {
+  if constexpr (kGroups > 1) {
 #pragma unroll
-    for (int q = 0; q < 4; q++)
-      *reinterpret_cast<float4*>(&sh_o[grp - 1][cl][q * 128 + lane * 4]) =
-          make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+    for (int q = 0; q < 4; q += 2) {
+      if (grp > 0) {
+#pragma unroll
+        for (int e = 0; e < 2; e++)
+          *reinterpret_cast<float4*>(&sh_o[grp - 1][cl][e * 128 + lane * 4]) =
+              make_float4(o[4 * (q + e)], o[4 * (q + e) + 1], o[4 * (q + e) + 2], o[4 * (q + e) + 3]);
+      }
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int g = 0; g < kGroups - 1; g++)
+#pragma unroll
+          for (int e = 0; e < 2; e++) {
+            const float4 y = *reinterpret_cast<const float4*>(&sh_o[g][cl][e * 128 + lane * 4]);
+            o[4 * (q + e)] += y.x;
+            o[4 * (q + e) + 1] += y.y;
+            o[4 * (q + e) + 2] += y.z;
+            o[4 * (q + e) + 3] += y.w;
+          }
+      }
+      __syncthreads();
+    }
   }
-  __syncthreads();
   if (grp > 0 || !in) return;
   const float inv = total == 0.f ? 0.f : 1.f / total;
   const int64_t row = (int64_t)(rec.r0 + r) * a.heads + head;
 #pragma unroll
-  for (int q = 0; q < 4; q++) {
-#pragma unroll
-    for (int g = 0; g < kJoinGroups - 1; g++) {
-      const float4 y = *reinterpret_cast<const float4*>(&sh_o[g][cl][q * 128 + lane * 4]);
-      o[4 * q] += y.x;
-      o[4 * q + 1] += y.y;
-      o[4 * q + 2] += y.z;
-      o[4 * q + 3] += y.w;
-    }
+  for (int q = 0; q < 4; q++)
     *reinterpret_cast<uint2*>(a.out + row * kValue + q * 128 + lane * 4) =
         make_uint2(mma::pack_bf16(o[4 * q] * inv, o[4 * q + 1] * inv),
                    mma::pack_bf16(o[4 * q + 2] * inv, o[4 * q + 3] * inv));
-  }
   if (lane == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }
 
@@ -874,23 +976,30 @@ template <int kWidth, int kN>
 cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t stream) {
   using S = Shape<kWidth, kN>;
   static_assert(S::kBytes <= 232448, "shared memory of a CTA");
+  static_assert(S::kThreads <= kMaxWarps * 32, "");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN>);
   cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
   if (e != cudaSuccess) return e;
-  latent_attn_kernel<kWidth, kN><<<ctas, S::kThreads, S::kBytes, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || !may_split) return e;
+  // Both launches may begin while the one before them ends: each waits for it before its
+  // first access to global memory.
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, kN / 8, 1);
-  cfg.blockDim = dim3(kJoinThreads, 1, 1);
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, p, ctas);
+  cfg.stream = stream;
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(S::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kBytes;
+  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, p);
+  if (e != cudaSuccess || !may_split) return e;
+  const bool many = p.a.n_rows * p.hb * 8 <= ctas;  // pieces a unit
+  cfg.gridDim = dim3(ctas, kN / 8, 1);
+  cfg.blockDim = dim3(many ? 1024 : 256, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, many ? combine_kernel<4> : combine_kernel<1>, p, ctas);
 }
 
 }  // namespace
