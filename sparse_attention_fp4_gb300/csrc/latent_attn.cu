@@ -51,6 +51,7 @@ constexpr int kMmaRole = 0, kQueryRole = 1, kAheadRole = 2, kLoadRole = 3;
 constexpr uint32_t kAhead = 5;    // tiles that the prefetches are ahead of the softmax
 constexpr int kMaxGroup = 8;      // rows a unit
 constexpr float kRaise = 8.f;
+constexpr float kNoMax = -3.0e38f;
 
 struct Params {
   LatentArgs a;
@@ -315,6 +316,13 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   return true;
 }
 
+// One arrival for the warp's writes (each lane has fenced its own): an arrival of every lane
+// is an atomic on one word each.
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(bar);
+}
+
 // ---------------------------------------------------------------- shared memory
 template <int kWidth, int kN>
 struct Shape {
@@ -369,15 +377,15 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
       for (int half = 0; half < 2; half++) {
-        ptx::mbar_init(kfull(s, half), 128);
+        ptx::mbar_init(kfull(s, half), 4);
         ptx::mbar_init(kempty(s, half), 1);
       }
     }
-    ptx::mbar_init(qfull, 32);
+    ptx::mbar_init(qfull, 1);
     ptx::mbar_init(qempty, 1);
     ptx::mbar_init(sfull(0), 1);
     ptx::mbar_init(sfull(1), 1);
-    ptx::mbar_init(pfull, kSoft);
+    ptx::mbar_init(pfull, S::kSoftWarps);
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
     *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = 0;  // tiles that the softmax has begun
@@ -397,13 +405,14 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const Ctl ctl{abort_flag, a.status, p.wait_limit_ns};
+  const Ctl ctl{abort_flag, a.status, 2 * p.wait_limit_ns};  // in cycles: at most 2.07 a ns
   const uint32_t tm_s = tmem + 4 * kN;  // two S^T buffers behind the output
 
   if (any && warp >= kLoadWarp) {
     // ------------------------------------------------------------ loaders
     const int grp = (warp - kLoadWarp) >> 2, tid = threadIdx.x - (kLoadWarp + 4 * grp) * 32;
-    const int wrow = (tid >> 5) * 16 + (lane >> 3), piece = lane & 7;
+    const int wrow = (tid >> 5) * 16 + (lane >> 3), piece = lane & 7;  // of the copies
+    const int tok = (tid >> 5) * 16 + (lane & 15);  // the token that the lane looks up
     uint32_t kctr = 0;
     int t = seg.t0;
     bool have = !p.idle_producers;
@@ -420,57 +429,44 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         t = seg.t0 + n;
       }
     };
-    // A tile's tokens are looked up two steps ahead: positions, then page ids; each value is
-    // used an iteration after its load was issued.
-    int pos1[4], pos2[4];        // of the group's next tile, and of the one after it
-    uint32_t rows1[4], rows2[4];  // rows of the unit that see the token, if its position is valid
-    int32_t page1[4];
-    int seq2 = 0;
-    bool have1 = false;
+    // A tile's tokens are looked up two steps ahead, positions and then page ids, one token a
+    // lane; each value is used an iteration after its load was issued.
+    int pos1 = 0, pos2 = 0;        // of the group's next tile, and of the one after it
+    uint32_t rows1 = 0, rows2 = 0;  // rows of the unit that see the token, if its position is valid
+    int32_t page1 = -1;
+    const int32_t* table2 = a.page_table;
     auto positions = [&]() {  // of the walker's tile
-      seq2 = seg.u.seq;
-#pragma unroll
-      for (int g = 0; g < 4; g++) {
-        int pos = t * kTile + wrow + g * 4;
-        uint32_t rows = 0;
-        if (a.idx) {
-          if (pos < seg.u.min_len) {
-            pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
-            rows = 1;
-          }
-        } else if (pos < seg.u.min_len) {
-          rows = (1u << seg.u.rows) - 1;
-        } else {
-          for (int r = 0; r < seg.u.rows; r++) {
-            int len, end, err;
-            row_span(a, seg.u.r0 + r, len, end, err);
-            rows |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos) << r;
-          }
+      table2 = a.page_table + (int64_t)seg.u.seq * a.max_pages;
+      pos2 = t * kTile + tok;
+      rows2 = 0;
+      if (pos2 < seg.u.min_len) {
+        rows2 = (1u << seg.u.rows) - 1;
+        if (a.idx) pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
+      } else if (!a.idx) {
+        for (int r = 0; r < seg.u.rows; r++) {
+          int len, end, err;
+          row_span(a, seg.u.r0 + r, len, end, err);
+          rows2 |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos2) << r;
         }
-        pos2[g] = pos;
-        rows2[g] = rows;
       }
     };
     auto pages = [&]() {
-#pragma unroll
-      for (int g = 0; g < 4; g++) {
-        pos1[g] = pos2[g];
-        rows1[g] = rows2[g] && pos2[g] >= 0 ? rows2[g] : 0;
-        page1[g] = -1;
-        if (rows1[g]) {
-          if (pos1[g] / kPage < a.max_pages) {
-            page1[g] = a.page_table[(int64_t)seq2 * a.max_pages + pos1[g] / kPage];
-          } else {
-            record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-            rows1[g] = 0;
-          }
+      pos1 = pos2;
+      rows1 = pos2 >= 0 ? rows2 : 0;
+      page1 = -1;
+      if (rows1) {
+        if (pos1 / kPage < a.max_pages) {
+          page1 = table2[pos1 / kPage];
+        } else {
+          record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+          rows1 = 0;
         }
       }
     };
     if (have && grp > 0) advance(grp);
     uint32_t kcur = kctr;
+    bool have1 = have;
     if (have) {
-      have1 = true;
       positions();
       pages();
       advance(kStages);
@@ -478,24 +474,26 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     }
     while (have1) {
       const int s = kcur % kStages;
+      const uint32_t free = ((kcur / kStages) & 1) ^ 1;
+      if (!mma::wait_warp(kempty(s, 0), free, ctl)) break;
+      const bool in = (uint32_t)page1 < (uint32_t)a.num_pages;
+      if (!in && rows1) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+      const int slot = in ? page1 * kPage + (pos1 & (kPage - 1)) : -1;
+      if (lane < 16) smem[S::kOffSeen + s * kTile + tok] = (uint8_t)(in ? rows1 : 0);
       const uint16_t* src[4];
       uint32_t bytes[4];
-      const uint32_t free = ((kcur / kStages) & 1) ^ 1;
-      if (!pipe::wait_warp(kempty(s, 0), free, ctl)) break;
 #pragma unroll
       for (int g = 0; g < 4; g++) {
-        const bool in = page1[g] >= 0 && page1[g] < a.num_pages;
-        if (!in && rows1[g]) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-        src[g] = in ? a.cache + ((int64_t)page1[g] * kPage + pos1[g] % kPage) * kWidth + piece * 8 : a.cache;
-        bytes[g] = in ? 16 : 0;
-        if (piece == 0) smem[S::kOffSeen + s * kTile + wrow + g * 4] = (uint8_t)(in ? rows1[g] : 0);
+        const int of = __shfl_sync(kFull, slot, g * 4 + (lane >> 3));
+        src[g] = a.cache + (int64_t)max(of, 0) * kWidth + piece * 8;
+        bytes[g] = of >= 0 ? 16 : 0;
       }
       const uint32_t dst = sb + s * S::kStageBytes;
 #pragma unroll
       for (int c = 0; c < kChunks; c++) {
         if (c == 4) {
           mma::cp_async_commit();
-          if (!pipe::wait_warp(kempty(s, 1), free, ctl)) break;
+          if (!mma::wait_warp(kempty(s, 1), free, ctl)) break;
         }
 #pragma unroll
         for (int g = 0; g < 4; g++)
@@ -512,17 +510,17 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       }
       mma::cp_async_wait_group<1>();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(kfull(kdone % kStages, 0));
+      arrive_warp(kfull(kdone % kStages, 0), lane);
       mma::cp_async_wait_group<0>();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(kfull(kdone % kStages, 1));
+      arrive_warp(kfull(kdone % kStages, 1), lane);
     }
     mma::cp_async_wait_all();
   } else if (any && warp == kQueryWarp) {
     // ------------------------------------------------------------ queries
     uint32_t ictr = 0;
     do {
-      if (!pipe::wait_warp(qempty, (ictr & 1) ^ 1, ctl)) break;
+      if (!mma::wait_warp(qempty, (ictr & 1) ^ 1, ctl)) break;
       const int r0 = lane >> 3, pc = lane & 7;
       for (int col = r0; col < kN; col += 4) {
         const int r = col / p.hp, h = col % p.hp, head = seg.hb * p.hs + h;
@@ -534,7 +532,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       }
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(qfull);
+      arrive_warp(qfull, lane);
       ictr++;
     } while (next_seg(p, seg));
   } else if (any && warp == kAheadWarp) {
@@ -545,10 +543,10 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     do {
       for (int t = seg.t0; on && t < seg.t1; t++, kctr++) {
         if (kctr < kStages) continue;  // the loaders are at these already
-        const uint64_t t0 = ptx::globaltimer();
+        const int64_t t0 = clock64();
         while ((int32_t)(kctr - __shfl_sync(kFull, *progress, 0)) > (int32_t)kAhead) {
           __nanosleep(100);
-          const int stop = *ctl.abort || ptx::globaltimer() - t0 > ctl.timeout_ns;  // only a hint: no error
+          const int stop = *ctl.abort || clock64() - t0 > (int64_t)ctl.timeout_ns;  // only a hint: no error
           if (__shfl_sync(kFull, stop, 0)) {
             on = false;
             break;
@@ -575,59 +573,71 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
     constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
     const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0), pd = mma::desc_lo(sb + S::kOffP, 0);
-    uint32_t kctr = 0, ictr = 0;
     auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(kFull, ptx::mbar_test_wait(b, parity)) != 0; };
-    // the scores' product of tile k over one half of the dims
-    auto issue_s = [&](uint32_t k, int half, bool last) {
-      ptx::tc_fence_after();
-      const uint32_t kd = mma::desc_lo(sb + (k % kStages) * S::kStageBytes, 0), d = tm_s + (k & 1) * kN;
-      if (mma::elect_one()) {
-        if (half == 0) {
-#pragma unroll
-          for (int c = 0; c < 4; c++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS,
-                          (c | i) != 0);
-        } else {
-#pragma unroll
-          for (int c = 4; c < kChunks; c++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-              mma::mma_ss(d, kd + ((c * (kTile * 128) + i * 32) >> 4), qd + ((c * S::kQChunk + i * 32) >> 4), kIdS, true);
-          ptx::mma_commit(sfull(k & 1));
-          if (last) ptx::mma_commit(qempty);
-        }
-      }
-      __syncwarp();
-    };
+    const uint32_t kd0 = mma::desc_lo(sb, 0), vd0 = mma::desc_lo(sb, kTile * 128);
+    constexpr uint32_t kStageLo = S::kStageBytes >> 4;
+    // the next half of scores to issue: stage, phase and half; the next tile's weights
+    uint32_t s_stage = 0, s_phase = 0, s_half = 0, s_buf = 0;
+    uint32_t o_stage = 0, p_phase = 0, q_phase = 0;
     bool ok = true;
     do {
       const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
-      ok = pipe::wait_warp(qfull, ictr & 1, ctl);
-      uint32_t halves = 0;  // halves of scores issued in this segment
-      for (uint32_t i = 0; ok && i < n; i++, kctr++) {
+      ok = mma::wait_warp(qfull, q_phase, ctl);
+      q_phase ^= 1;
+      uint32_t left = 2 * n;  // halves of scores of this segment not issued yet
+      for (uint32_t i = 0; ok && i < n; i++) {
         // This tile's scores, if they have not been issued; then, until its weights are there,
         // the next tile's scores as their halves land.
-        const uint64_t t0 = ptx::globaltimer();
+        const uint32_t behind = 2 * (n - 1 - i);  // halves left once this tile's are issued
+        const int64_t t0 = clock64();
         for (uint32_t it = 1;; it++) {
-          const uint32_t next = halves >> 1, k = kctr - i + next;
-          if (next > i && ready(pfull, kctr & 1)) break;
-          if (next < n && next <= i + 1 && ready(kfull(k % kStages, halves & 1), (k / kStages) & 1)) {
-            issue_s(k, halves & 1, next + 1 == n);
-            halves++;
+          if (left <= behind && ready(pfull, p_phase)) break;
+          if (left && left + 2 > behind && ready(kfull(s_stage, s_half), s_phase)) {
+            ptx::tc_fence_after();
+            const uint32_t kd = kd0 + s_stage * kStageLo, d = tm_s + s_buf * kN;
+            left--;
+            if (s_half == 0) {
+              if (mma::elect_one()) {
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+#pragma unroll
+                  for (int e = 0; e < 4; e++)
+                    mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS,
+                                (c | e) != 0);
+              }
+              s_half = 1;
+            } else {
+              if (mma::elect_one()) {
+#pragma unroll
+                for (int c = 4; c < kChunks; c++)
+#pragma unroll
+                  for (int e = 0; e < 4; e++)
+                    mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS,
+                                true);
+                ptx::mma_commit(sfull(s_buf));
+                if (left == 0) ptx::mma_commit(qempty);
+              }
+              s_half = 0;
+              s_buf ^= 1;
+              if (++s_stage == kStages) {
+                s_stage = 0;
+                s_phase ^= 1;
+              }
+            }
+            __syncwarp();
             continue;
           }
           if ((it & 63u) == 0) {
             if (*ctl.abort) ok = false;
-            else if (ptx::globaltimer() - t0 > ctl.timeout_ns) ok = pipe::give_up(ctl);
+            else if (clock64() - t0 > (int64_t)ctl.timeout_ns) ok = pipe::give_up(ctl);
             ok = __all_sync(kFull, ok);
             if (!ok) break;
           }
         }
         if (!ok) break;
+        p_phase ^= 1;
         ptx::tc_fence_after();
-        const uint32_t vd = mma::desc_lo(sb + (kctr % kStages) * S::kStageBytes, kTile * 128);
+        const uint32_t vd = vd0 + o_stage * kStageLo;
         if (mma::elect_one()) {
 #pragma unroll
           for (int half = 0; half < 2; half++) {
@@ -637,17 +647,17 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
               for (int b = 2 * half; b < 2 * half + 2; b++)
                 mma::mma_ss(tmem + b * kN, vd + ((b * (2 * kTile * 128) + ks * 2048) >> 4), pd + ((ks * 32) >> 4), kIdO,
                             ks > 0 || i > 0);
-            ptx::mma_commit(kempty(kctr % kStages, half));
+            ptx::mma_commit(kempty(o_stage, half));
           }
         }
         __syncwarp();
+        if (++o_stage == kStages) o_stage = 0;
       }
-      ictr++;
     } while (ok && next_seg(p, seg));
     // nothing of this CTA's may be under way in the tensor cores when it ends
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
-    pipe::wait_warp(done, 0, ctl, false);
+    mma::wait_warp(done, 0, ctl, false);
   } else if (any && warp < S::kSoftWarps) {
     // ------------------------------------------------------------ softmax and output
     const float cs = a.scale * 1.4426950408889634f;
@@ -663,40 +673,55 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     do {
       const int n = seg.t1 - seg.t0;
       const uint32_t everyone = (1u << seg.u.rows) - 1;
-      float m[2 * kJ], l[2 * kJ];  // of the thread's columns 8 j + 2 quad + {0, 1}
+      // of the thread's columns 8 j + 2 quad + {0, 1}; m starts low enough that any score raises it
+      float2 m[kJ], l[kJ];
 #pragma unroll
-      for (int j = 0; j < 2 * kJ; j++) {
-        m[j] = -INFINITY;
-        l[j] = 0.f;
+      for (int j = 0; j < kJ; j++) {
+        m[j] = make_float2(kNoMax, kNoMax);
+        l[j] = make_float2(0.f, 0.f);
       }
       for (int i = 0; i < n; i++, kctr++) {
         const int st = kctr % kStages;
         // a warp whose wait ran out goes on to the next vote, so that all four leave together
-        ok = ok && pipe::wait_warp(kfull(st, 0), (kctr / kStages) & 1, ctl) &&
-             pipe::wait_warp(sfull(kctr & 1), (kctr >> 1) & 1, ctl);
-        if (threadIdx.x == 0) *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = kctr;
-        ptx::tc_fence_after();
-        float v[4 * kJ];
-        mma::ld_16x256b<kJ>(tm_s + (kctr & 1) * kN + col0 + lanes, v);
+        ok = ok && mma::wait_warp(kfull(st, 0), (kctr / kStages) & 1, ctl);
         const uint32_t see0 = smem[S::kOffSeen + st * kTile + tok], see1 = smem[S::kOffSeen + st * kTile + tok + 8];
-        if (!__all_sync(kFull, see0 == everyone && see1 == everyone)) {
+        const bool all_seen = __all_sync(kFull, (see0 & see1) == everyone);
+        if (threadIdx.x == 0) *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = kctr;
+        ok = ok && mma::wait_warp(sfull(kctr & 1), (kctr >> 1) & 1, ctl);
+        ptx::tc_fence_after();
+        // scores: v[2 j] of token tok, v[2 j + 1] of token tok + 8
+        float2 v[2 * kJ];
+        mma::ld_16x256b<kJ>(tm_s + (kctr & 1) * kN + col0 + lanes, reinterpret_cast<float*>(v));
+        float mul = cs;
+        bool zero0 = false, zero1 = false;
+        if (!all_seen) {
           if (seg.u.rows > 1) {
             // A token that some rows see and others do not stays in the second product.  If
-            // it is not finite (then no score of it is), its value row is zeroed and the
-            // columns that see it get a NaN weight: NaN for those, nothing for the others.
+            // its value is not finite (then no score is), the value row is zeroed below and
+            // the columns that see it get a NaN weight: NaN for those, nothing for the others.
 #pragma unroll
             for (int half = 0; half < 2; half++) {
               const uint32_t see = half ? see1 : see0;
               bool odd = see != 0 && see != everyone;
 #pragma unroll
-              for (int j = 0; j < kJ; j++) odd = odd && !(fabsf(v[4 * j + 2 * half]) < INFINITY) && !(fabsf(v[4 * j + 2 * half + 1]) < INFINITY);
-              const uint32_t all = __ballot_sync(kFull, odd) >> (lane & 28) & 15u;
-              if (all == 15u) {
-                for (int c = quad; c < kValue / 8; c += 4)
-                  *reinterpret_cast<uint4*>(smem + st * S::kStageBytes + (c >> 3) * (kTile * 128) +
-                                            mma::sw128(tok + 8 * half, c & 7)) = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < kJ; j++)
+                odd = odd && !(fabsf(v[2 * j + half].x) < INFINITY) && !(fabsf(v[2 * j + half].y) < INFINITY);
+              if (__any_sync(kFull, odd)) {
+                bool bad = false;
+                for (int c = quad; c < kValue / 8; c += 4) {
+                  const uint4 u = *reinterpret_cast<const uint4*>(smem + st * S::kStageBytes + (c >> 3) * (kTile * 128) +
+                                                                  mma::sw128(tok + 8 * half, c & 7));
+                  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < kJ; j++) v[4 * j + 2 * half] = v[4 * j + 2 * half + 1] = NAN;
+                  for (int e = 0; e < 4; e++)
+                    bad = bad || (w[e] & 0x7F80u) == 0x7F80u || (w[e] & 0x7F800000u) == 0x7F800000u;
+                }
+                bad = (__ballot_sync(kFull, bad) >> (lane & 28) & 15u) != 0 && see != 0 && see != everyone;
+                (half ? zero1 : zero0) = bad;
+                if (bad) {
+#pragma unroll
+                  for (int j = 0; j < kJ; j++) v[2 * j + half] = make_float2(NAN, NAN);
+                }
               }
             }
           }
@@ -704,22 +729,28 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           for (int j = 0; j < kJ; j++) {
             const int r = (col0 + 8 * j) / p.hp;
             const bool in0 = (see0 >> r) & 1, in1 = (see1 >> r) & 1;
-            v[4 * j] = in0 ? v[4 * j] * cs : -INFINITY;
-            v[4 * j + 1] = in0 ? v[4 * j + 1] * cs : -INFINITY;
-            v[4 * j + 2] = in1 ? v[4 * j + 2] * cs : -INFINITY;
-            v[4 * j + 3] = in1 ? v[4 * j + 3] * cs : -INFINITY;
+            v[2 * j] = in0 ? make_float2(v[2 * j].x * cs, v[2 * j].y * cs) : make_float2(-INFINITY, -INFINITY);
+            v[2 * j + 1] = in1 ? make_float2(v[2 * j + 1].x * cs, v[2 * j + 1].y * cs) : make_float2(-INFINITY, -INFINITY);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4 * kJ; j++) v[j] *= cs;
+          mul = 1.f;
         }
-        bool above = !ok;
+        // v[] becomes the exponents: scores, in powers of two, above the reference
+        const float2 mul2 = make_float2(mul, mul);
+        float most = -INFINITY;
+        float2 x[2 * kJ];
 #pragma unroll
-        for (int j = 0; j < kJ; j++) {
-          above = above || fmaxf(v[4 * j], v[4 * j + 2]) > m[2 * j] + kRaise ||
-                  fmaxf(v[4 * j + 1], v[4 * j + 3]) > m[2 * j + 1] + kRaise;
+        for (int j = 0; j < 2 * kJ; j++) {
+          x[j] = mma::fma2(v[j], mul2, make_float2(-m[j >> 1].x, -m[j >> 1].y));
+          most = fmaxf(most, fmaxf(x[j].x, x[j].y));
         }
-        const bool raise = mma::bar_any(1, kSoft, above);
+        const bool raise = mma::bar_any(1, kSoft, most > kRaise || !ok);
+        if (zero0 || zero1) {
+          for (int c = quad; c < kValue / 8; c += 4) {
+            uint8_t* row = smem + st * S::kStageBytes + (c >> 3) * (kTile * 128);
+            if (zero0) *reinterpret_cast<uint4*>(row + mma::sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
+            if (zero1) *reinterpret_cast<uint4*>(row + mma::sw128(tok + 8, c & 7)) = make_uint4(0, 0, 0, 0);
+          }
+        }
         if (raise) {
           if (mma::bar_any(1, kSoft, !ok)) {
             ok = false;
@@ -727,46 +758,47 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           }
 #pragma unroll
           for (int j = 0; j < kJ; j++) {
+            float2 t = make_float2(fmaxf(v[2 * j].x * mul, v[2 * j + 1].x * mul), fmaxf(v[2 * j].y * mul, v[2 * j + 1].y * mul));
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-              float x = fmaxf(v[4 * j + e], v[4 * j + 2 + e]);
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-              if (r8 == 0) red[qw * kN + col0 + 8 * j + 2 * quad + e] = x;
+            for (int d = 4; d <= 16; d <<= 1) {
+              t.x = fmaxf(t.x, __shfl_xor_sync(kFull, t.x, d));
+              t.y = fmaxf(t.y, __shfl_xor_sync(kFull, t.y, d));
             }
+            if (r8 == 0) *reinterpret_cast<float2*>(red + qw * kN + col0 + 8 * j + 2 * quad) = t;
           }
           ptx::named_bar_sync(1, kSoft);
 #pragma unroll
           for (int j = 0; j < kJ; j++) {
+            const int c = col0 + 8 * j + 2 * quad;
+            float2 m1 = m[j];
 #pragma unroll
-            for (int e = 0; e < 2; e++) {
-              const int c = col0 + 8 * j + 2 * quad + e;
-              const float x = fmaxf(fmaxf(red[c], red[kN + c]), fmaxf(red[2 * kN + c], red[3 * kN + c]));
-              const float m1 = fmaxf(m[2 * j + e], x);
-              const float f = m1 == m[2 * j + e] ? 1.f : mma::exp2_approx(m[2 * j + e] - m1);
-              if (qw == 0 && r8 == 0) sm_f[c] = f;
-              l[2 * j + e] *= f;
-              m[2 * j + e] = m1;
+            for (int q = 0; q < 4; q++) {
+              const float2 t = *reinterpret_cast<const float2*>(red + q * kN + c);
+              m1 = make_float2(fmaxf(m1.x, t.x), fmaxf(m1.y, t.y));
             }
+            const float2 f = make_float2(m1.x == m[j].x ? 1.f : mma::exp2_approx(m[j].x - m1.x),
+                                         m1.y == m[j].y ? 1.f : mma::exp2_approx(m[j].y - m1.y));
+            if (qw == 0 && r8 == 0) *reinterpret_cast<float2*>(sm_f + c) = f;
+            l[j] = make_float2(l[j].x * f.x, l[j].y * f.y);
+            m[j] = m1;
+            x[2 * j] = mma::fma2(v[2 * j], mul2, make_float2(-m1.x, -m1.y));
+            x[2 * j + 1] = mma::fma2(v[2 * j + 1], mul2, make_float2(-m1.x, -m1.y));
           }
           ptx::named_bar_sync(1, kSoft);  // red is read, sm_f is written
         }
         uint32_t pk[2 * kJ];
 #pragma unroll
         for (int j = 0; j < kJ; j++) {
-          const float m0 = m[2 * j] == -INFINITY ? 0.f : m[2 * j], m1 = m[2 * j + 1] == -INFINITY ? 0.f : m[2 * j + 1];
-          const float p0 = mma::exp2_approx(v[4 * j] - m0), p1 = mma::exp2_approx(v[4 * j + 1] - m1);
-          const float p2 = mma::exp2_approx(v[4 * j + 2] - m0), p3 = mma::exp2_approx(v[4 * j + 3] - m1);
-          l[2 * j] += p0 + p2;
-          l[2 * j + 1] += p1 + p3;
-          pk[2 * j] = mma::pack_bf16(p0, p1);
-          pk[2 * j + 1] = mma::pack_bf16(p2, p3);
+          const float2 p0 = make_float2(mma::exp2_approx(x[2 * j].x), mma::exp2_approx(x[2 * j].y));
+          const float2 p1 = make_float2(mma::exp2_approx(x[2 * j + 1].x), mma::exp2_approx(x[2 * j + 1].y));
+          l[j] = mma::add2(l[j], mma::add2(p0, p1));
+          pk[2 * j] = mma::pack_bf16(p0.x, p0.y);
+          pk[2 * j + 1] = mma::pack_bf16(p1.x, p1.y);
         }
         // the last tile's product has read P^T, and the output may be rescaled
         if (kctr > 0) {
           const uint32_t last = kctr - 1;
-          ok = pipe::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
+          ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
           if (!ok) continue;
         }
         if (raise) {
@@ -791,19 +823,21 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(pfull);
+        arrive_warp(pfull, lane);
       }
       if (mma::bar_any(1, kSoft, !ok)) break;
       // ---- the segment's output
       const bool begins = seg.t0 == 0, ends = seg.t1 == seg.u.tiles, whole = begins && ends;
 #pragma unroll
-      for (int j = 0; j < 2 * kJ; j++) {
-        l[j] += __shfl_xor_sync(kFull, l[j], 4);
-        l[j] += __shfl_xor_sync(kFull, l[j], 8);
-        l[j] += __shfl_xor_sync(kFull, l[j], 16);
-        const int c = col0 + 8 * (j >> 1) + 2 * quad + (j & 1);
-        if (r8 == 0) red[qw * kN + c] = l[j];
-        if (r8 == 0 && qw == 0) sm_m[c] = m[j];
+      for (int j = 0; j < kJ; j++) {
+#pragma unroll
+        for (int d = 4; d <= 16; d <<= 1) {
+          l[j].x += __shfl_xor_sync(kFull, l[j].x, d);
+          l[j].y += __shfl_xor_sync(kFull, l[j].y, d);
+        }
+        const int c = col0 + 8 * j + 2 * quad;
+        if (r8 == 0) *reinterpret_cast<float2*>(red + qw * kN + c) = l[j];
+        if (r8 == 0 && qw == 0) *reinterpret_cast<float2*>(sm_m + c) = m[j];
       }
       ptx::named_bar_sync(1, kSoft);
       const int slot = 2 * blockIdx.x + (first_of_cta ? 0 : 1);
@@ -825,7 +859,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (!whole && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
-      ok = pipe::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
+      ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
@@ -914,7 +948,6 @@ __global__ void __launch_bounds__(kGroups * 256) combine_kernel(const Params p, 
     for (int i = lane; i < n; i += 32) top = fmaxf(top, wk.ml[slot_of(i) * 2 * kCols + col]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, d));
-    if (top == -INFINITY) top = 0.f;
     for (int i = lane; i < n; i += 32) {
       const float* ml = wk.ml + slot_of(i) * 2 * kCols + col;
       total += mma::exp2_approx(ml[0] - top) * ml[kCols];

@@ -2,10 +2,33 @@
 // the bf16 MMA, tensor-memory loads and stores, cp.async and stmatrix.
 #pragma once
 
+#include "pipeline.cuh"
 #include "ptx.cuh"
 
 namespace fp4idx {
 namespace mma {
+
+// Bounded wait of the warp for an mbarrier phase, as pipe::wait_warp, but timed by the SM's
+// clock (ctl.timeout_ns holds cycles): reading the global timer takes longer than most
+// waits here last.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const pipe::Ctl& c, bool honor_abort = true) {
+  bool ok = ptx::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const int64_t t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+      ok = ptx::mbar_try_wait(bar, parity);
+      if (ok) break;
+      if ((it & 15u) == 0) {
+        if (honor_abort && *c.abort) break;
+        if (clock64() - t0 > (int64_t)c.timeout_ns) {
+          pipe::give_up(c);
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(pipe::kFull, ok);
+}
 
 // Operands lie in shared memory as rows of 128 bytes (64 bf16), eight rows an atom of 1,024
 // bytes whose 16-byte pieces are stored at piece ^ (row & 7).  K-major: rows are M or N,
@@ -78,6 +101,26 @@ __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+
+// Packed pairs: a * b + c and a + b, each element rounded once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%6, %7};\n\t"
+      "fma.rn.f32x2 pc, pa, pb, pc;\n\tmov.b64 {%0, %1}, pc;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 pa, pb;\n\t"
+      "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\t"
+      "add.rn.f32x2 pa, pa, pb;\n\tmov.b64 {%0, %1}, pa;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 // Whether any of the `threads` threads at named barrier `id` has pred.
