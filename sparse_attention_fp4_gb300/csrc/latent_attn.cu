@@ -48,7 +48,7 @@ constexpr int kCols = 64;         // columns of a workspace slot
 constexpr int kValue = FP4IDX_LATENT_VALUE;
 // roles behind the softmax warps
 constexpr int kMmaRole = 0, kQueryRole = 1, kAheadRole = 2, kLoadRole = 3;
-constexpr uint32_t kAhead = 5;    // tiles that the prefetches are ahead of the softmax
+constexpr uint32_t kAhead = 3;    // tiles that the prefetches are ahead of the softmax
 constexpr int kMaxGroup = 8;      // rows a unit
 constexpr float kRaise = 8.f;
 constexpr float kNoMax = -3.0e38f;
@@ -56,6 +56,7 @@ constexpr float kNoMax = -3.0e38f;
 struct Params {
   LatentArgs a;
   int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
+  int32_t columns;            // selected rows: CTA c takes units c, c + grid, ... whole
   uint64_t wait_limit_ns;
   int32_t idle_producers;
 };
@@ -142,10 +143,15 @@ struct Seg {
   int hb, t0, t1;
   int64_t left;  // tiles of the CTA from t0 on
 };
-__device__ __forceinline__ bool next_seg(const Params& p, Seg& s) {
+__device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = false) {
   s.left -= s.t1 - s.t0;
   if (s.left <= 0) return false;
-  if (++s.hb == p.hb) {
+  if (p.columns) {
+    const int64_t u = (int64_t)s.u.r0 * p.hb + s.hb + gridDim.x;
+    if (u >= (int64_t)p.a.n_rows * p.hb) return false;
+    s.hb = (int)(u % p.hb);
+    load_unit(p, (int)(u / p.hb), s.u, report);
+  } else if (++s.hb == p.hb) {
     s.hb = 0;
     load_unit(p, s.u.r0 + s.u.rows, s.u, false);
   }
@@ -162,6 +168,10 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s) {
 // 32 tiles make 128 pieces for the joining kernel instead of the 304 of an even cut over 152
 // CTAs (a piece's end costs as much as two tiles, and its 128 KB are written and read again).
 // Taken when `most` is at most an even share plus 1/16 and three tiles.
+// More units, of rows with a selection each, where whole rounds of units waste at most a
+// twentieth: CTA c takes units c, c + grid, ... whole.  No pieces, and the rows of one
+// sequence, whose selections overlap, are read at the same time (L2 then holds what they
+// share; one CTA taking them one after the other read all of it from HBM again).
 // Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
 // edge moves to the edge (no piece then, for 1/20 more work).
 constexpr int kMaxWarps = 20;
@@ -229,6 +239,15 @@ __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& ru
 }
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
+  if (p.columns) {
+    const int u = blockIdx.x;
+    load_unit(p, u / p.hb, s.u, threadIdx.x == 0);
+    s.hb = u % p.hb;
+    s.t0 = 0;
+    s.t1 = s.u.tiles;
+    s.left = INT64_MAX;
+    return true;
+  }
   const bool report = blockIdx.x == 0;
   int64_t all = 0, incl = 0, total;
   int run = -1;
@@ -329,23 +348,31 @@ struct Shape {
   static constexpr int kChunks = kWidth / 64;
   static constexpr uint32_t kStageBytes = kChunks * kTile * 128;
   static constexpr uint32_t kQChunk = kN * 128;
+  // The weights have a buffer a stage, so that a tile's softmax does not wait for the last
+  // tile's second product.  At width 576 it is the stage's last block of keys, which only the
+  // first product reads; at width 512 it lies behind the queries.
+  static constexpr bool kOwnP = kChunks == 8;
   // a third stage where it fits (width 512 with at most 16 columns)
-  static constexpr int kStages = 3 * kStageBytes + (kChunks + 1) * kQChunk <= 225 * 1024 ? 3 : 2;
+  static constexpr int kStages = 3 * (kStageBytes + kQChunk) + kChunks * kQChunk <= 225 * 1024 && kOwnP ? 3 : 2;
   static constexpr int kSoftWarps = kN == 64 ? 8 : 4;
   static constexpr int kMmaWarp = kSoftWarps + kMmaRole, kQueryWarp = kSoftWarps + kQueryRole;
   static constexpr int kAheadWarp = kSoftWarps + kAheadRole, kLoadWarp = kSoftWarps + kLoadRole;
   static constexpr int kThreads = (kLoadWarp + 4 * kStages) * 32;
   static constexpr uint32_t kOffQ = kStages * kStageBytes;
   static constexpr uint32_t kOffP = kOffQ + kChunks * kQChunk;
-  static constexpr uint32_t kOffSeen = kOffP + kN * 128;          // [stage][64] rows that see the token
+  static constexpr uint32_t kOffSeen = kOffP + (kOwnP ? kStages * kQChunk : 0);          // [stage][64] rows that see the token
   static constexpr uint32_t kOffRed = kOffSeen + kStages * kTile;  // [4][kN] floats
   static constexpr uint32_t kOffM = kOffRed + 4 * kN * 4;          // [kN]
   static constexpr uint32_t kOffF = kOffM + kN * 4;                // [kN]
   static constexpr uint32_t kOffBar = kOffF + kN * 4;
-  // kfull[stages][2], kempty[stages][2], qfull, qempty, sfull[2], pfull, done
-  static constexpr int kBars = 4 * kStages + 6;
+  // kfull[stages][2], kempty[stages][2], qfull, qempty, sfull[2], pfull[2], done
+  static constexpr int kBars = 4 * kStages + 7;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
   static constexpr uint32_t kBytes = kOffMisc + 16 + 1024;  // and the base's alignment
+  static_assert(kQChunk <= kTile * 128, "the weights fit a block of keys");
+  static __device__ __forceinline__ uint32_t off_p(int stage) {
+    return kOwnP ? kOffP + stage * kQChunk : stage * kStageBytes + 8 * kTile * 128;
+  }
   static constexpr uint32_t kTmemCols = kN == 64 ? 512 : kN == 32 ? 256 : 128;
 };
 // The scan's scratch lies in the query buffer, which is not in use yet.
@@ -371,9 +398,9 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   // copied while the output's second half is computed.
   const auto kfull = [&](int s, int half) { return bar(2 * s + half); };
   const auto kempty = [&](int s, int half) { return bar(2 * (kStages + s) + half); };
-  const uint32_t qfull = bar(4 * kStages), qempty = bar(4 * kStages + 1), pfull = bar(4 * kStages + 4),
-                 done = bar(4 * kStages + 5);
+  const uint32_t qfull = bar(4 * kStages), qempty = bar(4 * kStages + 1), done = bar(4 * kStages + 6);
   const auto sfull = [&](int b) { return bar(4 * kStages + 2 + b); };
+  const auto pfull = [&](int b) { return bar(4 * kStages + 4 + b); };  // by the tile's parity, as sfull
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; s++) {
       for (int half = 0; half < 2; half++) {
@@ -385,13 +412,22 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::mbar_init(qempty, 1);
     ptx::mbar_init(sfull(0), 1);
     ptx::mbar_init(sfull(1), 1);
-    ptx::mbar_init(pfull, S::kSoftWarps);
+    ptx::mbar_init(pfull(0), S::kSoftWarps);
+    ptx::mbar_init(pfull(1), S::kSoftWarps);
     ptx::mbar_init(done, 1);
     *abort_flag = 0;
     *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = 0;  // tiles that the softmax has begun
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+  // Lists, page table and queries into L2, a line a thread of the whole grid, while the run is
+  // being found: three dependent reads lie between the lengths and the first tile.
+  {
+    const int64_t at = ((int64_t)blockIdx.x * S::kThreads + threadIdx.x) * 128;
+    if (a.idx && at < (int64_t)a.n_rows * a.k * 4) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.idx) + at);
+    if (at < (int64_t)a.num_seqs * a.max_pages * 4) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.page_table) + at);
+    if (at < (int64_t)a.n_rows * a.heads * (kWidth * 2)) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.q) + at);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Seg seg;
@@ -534,7 +570,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
       ictr++;
-    } while (next_seg(p, seg));
+    } while (next_seg(p, seg, lane == 0));
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)
     uint32_t kctr = 0;
@@ -572,13 +608,13 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     // ------------------------------------------------------------ MMA issue (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
     constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
-    const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0), pd = mma::desc_lo(sb + S::kOffP, 0);
+    const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0);
     auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(kFull, ptx::mbar_test_wait(b, parity)) != 0; };
     const uint32_t kd0 = mma::desc_lo(sb, 0), vd0 = mma::desc_lo(sb, kTile * 128);
     constexpr uint32_t kStageLo = S::kStageBytes >> 4;
     // the next half of scores to issue: stage, phase and half; the next tile's weights
     uint32_t s_stage = 0, s_phase = 0, s_half = 0, s_buf = 0;
-    uint32_t o_stage = 0, p_phase = 0, q_phase = 0;
+    uint32_t o_stage = 0, o_tile = 0, q_phase = 0;
     bool ok = true;
     do {
       const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
@@ -591,7 +627,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         const uint32_t behind = 2 * (n - 1 - i);  // halves left once this tile's are issued
         const int64_t t0 = clock64();
         for (uint32_t it = 1;; it++) {
-          if (left <= behind && ready(pfull, p_phase)) break;
+          if (left <= behind && ready(pfull(o_tile & 1), (o_tile >> 1) & 1)) break;
           if (left && left + 2 > behind && ready(kfull(s_stage, s_half), s_phase)) {
             ptx::tc_fence_after();
             const uint32_t kd = kd0 + s_stage * kStageLo, d = tm_s + s_buf * kN;
@@ -635,9 +671,9 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           }
         }
         if (!ok) break;
-        p_phase ^= 1;
+        o_tile++;
         ptx::tc_fence_after();
-        const uint32_t vd = vd0 + o_stage * kStageLo;
+        const uint32_t vd = vd0 + o_stage * kStageLo, pd = mma::desc_lo(sb + S::off_p(o_stage), 0);
         if (mma::elect_one()) {
 #pragma unroll
           for (int half = 0; half < 2; half++) {
@@ -795,35 +831,31 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           pk[2 * j] = mma::pack_bf16(p0.x, p0.y);
           pk[2 * j + 1] = mma::pack_bf16(p1.x, p1.y);
         }
-        // the last tile's product has read P^T, and the output may be rescaled
-        if (kctr > 0) {
+        if (raise && i > 0) {
+          // the output is rescaled once the last tile's product is in it
           const uint32_t last = kctr - 1;
           ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
           if (!ok) continue;
-        }
-        if (raise) {
-          if (i > 0) {
-            ptx::tc_fence_after();
+          ptx::tc_fence_after();
 #pragma unroll 1
-            for (int b = 0; b < 4 * kMyCols; b += 16) {
-              const int c = col0 + b % kMyCols, at = b / kMyCols * kN + c;
-              float o[16];
-              mma::ld_32x16(tmem + at + lanes, o);
+          for (int b = 0; b < 4 * kMyCols; b += 16) {
+            const int c = col0 + b % kMyCols, at = b / kMyCols * kN + c;
+            float o[16];
+            mma::ld_32x16(tmem + at + lanes, o);
 #pragma unroll
-              for (int e = 0; e < 16; e++) o[e] *= sm_f[c + e];
-              mma::st_32x16(tmem + at + lanes, o);
-            }
-            ptx::tmem_wait_st();
+            for (int e = 0; e < 16; e++) o[e] *= sm_f[c + e];
+            mma::st_32x16(tmem + at + lanes, o);
           }
+          ptx::tmem_wait_st();
         }
 #pragma unroll
         for (int j = 0; j < kJ; j += 2) {
           const int col = col0 + 8 * (j + (lane >> 4)) + (lane & 7), tb = 2 * qw + ((lane >> 3) & 1);
-          mma::stmatrix_x4_trans(sb + S::kOffP + mma::sw128(col, tb), pk[2 * j], pk[2 * j + 1], pk[2 * j + 2], pk[2 * j + 3]);
+          mma::stmatrix_x4_trans(sb + S::off_p(st) + mma::sw128(col, tb), pk[2 * j], pk[2 * j + 1], pk[2 * j + 2], pk[2 * j + 3]);
         }
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
-        arrive_warp(pfull, lane);
+        arrive_warp(pfull(kctr & 1), lane);
       }
       if (mma::bar_any(1, kSoft, !ok)) break;
       // ---- the segment's output
@@ -908,37 +940,59 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
 }
 
 // ---------------------------------------------------------------- joining the pieces
-// Block (c, y): the unit whose first piece is CTA c's, columns 8 y .. 8 y + 7; its next pieces
-// are the first segments of the CTAs that follow.  kGroups groups of eight warps take the
-// pieces in turn, a warp one column; the groups' sums are added in order.  One group where
-// units have few pieces (then all blocks are resident at once), four where they have many.
-template <int kGroups>
-__global__ void __launch_bounds__(kGroups * 256) combine_kernel(const Params p, int ctas) {
-  __shared__ float sh_o[kGroups > 1 ? kGroups - 1 : 1][8][kGroups > 1 ? 256 : 1];
-  __shared__ int sh_last;
+// Block (u, y): the u-th unit that is in pieces, kBlockCols columns from kBlockCols * y on.  Its
+// first piece is some CTA's last segment, the others are the first segments of the CTAs that
+// follow.  A warp takes one column and every kGroups-th piece; the groups' sums are added in
+// order.  Units have few pieces or many: one group of warps a column (all blocks are then
+// resident at once), or 16.
+template <int kBlockCols, int kGroups>
+__global__ void __launch_bounds__(kBlockCols * kGroups * 32) combine_kernel(const Params p, int ctas) {
+  __shared__ float sh_o[kGroups][kBlockCols][kGroups > 1 ? 128 : 1];
+  __shared__ uint32_t sh_starts[kMaxCtas / 32], sh_ends[kMaxCtas / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const LatentArgs& a = p.a;
   const Work wk = work_view(a.workspace);
-  const int c0 = blockIdx.x;
-  const int cx = c0 + 1 + (int)threadIdx.x;
-  // the unit's last piece: asked for by all threads at once, before the first is looked at
-  const int flags = cx < ctas ? wk.rec[2 * cx].flags : 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const auto starts = [](const Record& r) { return (r.flags & (kUsed | kBegins | kEnds)) == (kUsed | kBegins); };
+  if (warp < kMaxCtas / 32) {
+    const int c = threadIdx.x;
+    bool first = false, last = false;
+    if (c < ctas) {
+      const Record r0 = wk.rec[2 * c], r1 = wk.rec[2 * c + 1];
+      first = starts(r0) || starts(r1);
+      last = (r0.flags & (kUsed | kBegins | kEnds)) == (kUsed | kEnds);
+    }
+    const uint32_t f = __ballot_sync(kFull, first), l = __ballot_sync(kFull, last);
+    if (lane == 0) {
+      sh_starts[warp] = f;
+      sh_ends[warp] = l;
+    }
+  }
+  __syncthreads();
+  int c0 = -1, left = blockIdx.x;
+#pragma unroll
+  for (int w = 0; w < kMaxCtas / 32; w++) {
+    const uint32_t f = sh_starts[w];
+    const int n = __popc(f);
+    if (c0 < 0 && left < n) c0 = 32 * w + __fns(f, 0, left + 1);
+    left -= n;
+  }
+  if (c0 < 0) return;
+  int c1 = ctas;
+#pragma unroll
+  for (int w = kMaxCtas / 32 - 1; w >= 0; w--) {
+    uint32_t l = sh_ends[w];
+    if (32 * w + 31 <= c0) l = 0;
+    else if (32 * w <= c0) l &= ~0u << (c0 + 1 - 32 * w);
+    if (l) c1 = 32 * w + __ffs(l) - 1;
+  }
+  if (c1 >= ctas) return;  // a run that gave up
   int slot0 = 2 * c0 + 1;
   Record rec = wk.rec[slot0];
-  const Record rec0 = wk.rec[slot0 - 1];
-  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) {
-    rec = rec0;
-    slot0--;
-  }
-  if ((rec.flags & (kUsed | kBegins | kEnds)) != (kUsed | kBegins)) return;
-  if (threadIdx.x == 0) sh_last = ctas;
-  __syncthreads();
-  if ((flags & (kUsed | kBegins | kEnds)) == (kUsed | kEnds)) atomicMin(&sh_last, cx);
-  __syncthreads();
-  if (sh_last >= ctas) return;  // a run that gave up
-  const int n = sh_last - c0 + 1;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp >> 3, cl = warp & 7;
-  const int col = blockIdx.y * 8 + cl;
+  if (!starts(rec)) rec = wk.rec[--slot0];
+  const int n = c1 - c0 + 1;
+  const int grp = warp / kBlockCols, cl = warp % kBlockCols;
+  const int col = blockIdx.y * kBlockCols + cl;
   const int r = col / p.hp, h = col % p.hp, head = rec.hb * p.hs + h;
   const bool in = r < rec.rows && h < p.hs && head < a.heads;
   auto slot_of = [&](int i) { return i == 0 ? slot0 : 2 * (c0 + i); };
@@ -971,25 +1025,18 @@ __global__ void __launch_bounds__(kGroups * 256) combine_kernel(const Params p, 
   }
   if constexpr (kGroups > 1) {
 #pragma unroll
-    for (int q = 0; q < 4; q += 2) {
-      if (grp > 0) {
-#pragma unroll
-        for (int e = 0; e < 2; e++)
-          *reinterpret_cast<float4*>(&sh_o[grp - 1][cl][e * 128 + lane * 4]) =
-              make_float4(o[4 * (q + e)], o[4 * (q + e) + 1], o[4 * (q + e) + 2], o[4 * (q + e) + 3]);
-      }
+    for (int q = 0; q < 4; q++) {
+      *reinterpret_cast<float4*>(&sh_o[grp][cl][lane * 4]) = make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
       __syncthreads();
       if (grp == 0) {
 #pragma unroll
-        for (int g = 0; g < kGroups - 1; g++)
-#pragma unroll
-          for (int e = 0; e < 2; e++) {
-            const float4 y = *reinterpret_cast<const float4*>(&sh_o[g][cl][e * 128 + lane * 4]);
-            o[4 * (q + e)] += y.x;
-            o[4 * (q + e) + 1] += y.y;
-            o[4 * (q + e) + 2] += y.z;
-            o[4 * (q + e) + 3] += y.w;
-          }
+        for (int g = 1; g < kGroups; g++) {
+          const float4 y = *reinterpret_cast<const float4*>(&sh_o[g][cl][lane * 4]);
+          o[4 * q] += y.x;
+          o[4 * q + 1] += y.y;
+          o[4 * q + 2] += y.z;
+          o[4 * q + 3] += y.w;
+        }
       }
       __syncthreads();
     }
@@ -1028,11 +1075,12 @@ cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t strea
   cfg.dynamicSmemBytes = S::kBytes;
   e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, p);
   if (e != cudaSuccess || !may_split) return e;
-  const bool many = p.a.n_rows * p.hb * 8 <= ctas;  // pieces a unit
-  cfg.gridDim = dim3(ctas, kN / 8, 1);
+  const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most
+  const bool many = units * 8 <= ctas;  // eight pieces a unit or more
+  cfg.gridDim = dim3(units, many ? kN / 2 : kN / 8, 1);
   cfg.blockDim = dim3(many ? 1024 : 256, 1, 1);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, many ? combine_kernel<4> : combine_kernel<1>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, many ? combine_kernel<2, 16> : combine_kernel<8, 1>, p, ctas);
 }
 
 }  // namespace
@@ -1058,7 +1106,9 @@ cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool selected
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sms, kMaxCtas);
-  const bool may_split = (selected ? a.k : a.max_context) > kTile;
+  const int units = a.n_rows * p.hb, rounds = (units + ctas - 1) / ctas;
+  p.columns = selected && units > ctas && (int64_t)rounds * ctas * 20 <= (int64_t)units * 21;
+  const bool may_split = !p.columns && (selected ? a.k : a.max_context) > kTile;
   const int cols = p.group * p.hp;
   if (width == 576) {
     if (cols <= 16) return launch<576, 16>(p, ctas, may_split, stream);
