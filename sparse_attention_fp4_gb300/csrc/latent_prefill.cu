@@ -1,66 +1,398 @@
-// Expanded latent attention: causal attention over packed prompts, per-head keys (128 own
-// dims and 64 rotated ones that the heads share) and values (128 dims).
+// Expanded latent attention on the tensor cores: causal attention over packed prompts,
+// per-head keys (128 own dims and 64 rotated ones that the heads share) and values (128 dims).
 //
-// A warp per (query row, head); a lane holds six dims of the query and four of the output.
+// A CTA takes 256 consecutive query rows of one (sequence, head), as two tiles of 128 that
+// share the key and value tiles (128 tokens) in shared memory:
+//   S = Q K^T          M = 128 rows, N = 128 tokens, K = 192     (Q, K in shared memory)
+//   P = exp2(c S - m)  in place of S in tensor memory, bf16
+//   O += P V           M = 128 rows, N = 128 dims, K = 128       (P in tensor memory)
+// The issuer alternates the tiles (PV0, S0 of the next tokens, PV1, S1), so that one tile's
+// softmax runs while the other's products do.  Bound: 1,280 tensor cycles for a 128 x 128
+// tile against ~1,000 for its exponentials.
+//   warps 0-3, 4-7  softmax and output of tile 0, 1: a thread a row
+//   warp 8          issues the MMAs
+//   warp 9          one thread issues the TMA loads into a ring of eight 16 KB blocks (128
+//                   tokens x 64 dims): three a key tile, two a value tile
+// m is raised only when a score passes it by more than 8 (powers of two), so O is hardly ever
+// rescaled; the result does not depend on it.
+// Queries of longer contexts have smaller block indices: the longest work starts first.
 #include <algorithm>
 
 #include "launchers.cuh"
+#include "mma_bf16.cuh"
 
 namespace fp4idx {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kKey = FP4IDX_PREFILL_KEY, kVal = FP4IDX_PREFILL_VALUE;
+using pipe::Ctl;
+using pipe::kFull;
 
-__device__ __forceinline__ float2 two(const uint16_t* p) {
-  const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+constexpr int kKey = FP4IDX_PREFILL_KEY, kVal = FP4IDX_PREFILL_VALUE;
+constexpr int kRows = 128, kTokens = 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
+constexpr int kRing = 8;
+constexpr uint32_t kBlock = 128 * 128;  // bytes: 128 rows of 64 bf16
+constexpr uint32_t kOffRing = 6 * kBlock;  // behind the two query tiles
+constexpr uint32_t kOffBar = kOffRing + kRing * kBlock;
+// full[8], empty[8], qfull[2], sfull[2], pfull[2], ofull[2], done
+constexpr int kBars = 2 * kRing + 9;
+constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
+constexpr uint32_t kBytes = kOffMisc + 8 + 1024;
+static_assert(kBytes <= 232448, "shared memory of a CTA");
+constexpr uint32_t kTmO = 256;  // tensor memory: S0, S1 at 0 and 128, O0, O1 behind them
+constexpr float kRaise = 8.f, kNoMax = -3.0e38f;
+
+struct Params {
+  PrefillArgs a;
+  uint64_t wait_limit_ns;
+  int32_t idle_producers;
+};
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 
-__global__ void __launch_bounds__(kWarps * 32) latent_prefill_kernel(const PrefillArgs a) {
-  const int seq = blockIdx.z, h = blockIdx.y, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
+                                                                    const __grid_constant__ CUtensorMap kv_map,
+                                                                    const __grid_constant__ CUtensorMap r_map,
+                                                                    const __grid_constant__ Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  const PrefillArgs& a = p.a;
+  const int seq = blockIdx.z, head = blockIdx.y;
   const int64_t q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_kv[seq], k1 = a.cu_kv[seq + 1];
   if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_kv || q1 - q0 > a.max_q || k1 - k0 > a.max_kv) {
     if (threadIdx.x == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
     return;
   }
-  const int i = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (i >= q1 - q0) return;
-  const int64_t row = (q0 + i) * a.heads + h;
-  const uint16_t* q = a.q + row * kKey;
-  const float2 qa = two(q + lane * 4), qb = two(q + lane * 4 + 2), qc = two(q + 128 + lane * 2);
-  const int64_t n = (k1 - k0) - (q1 - q0) + i + 1;
-  float m = -INFINITY, l = 0.f, o[4] = {};
-  for (int64_t j = k0; j < k0 + n; j++) {
-    const uint16_t* kv = a.kv + (j * a.heads + h) * 256;
-    const float2 ka = two(kv + lane * 4), kb = two(kv + lane * 4 + 2), kc = two(a.k_rope + j * 64 + lane * 2);
-    const float2 va = two(kv + 128 + lane * 4), vb = two(kv + 128 + lane * 4 + 2);
-    float s = qa.x * ka.x + qa.y * ka.y + qb.x * kb.x + qb.y * kb.y + qc.x * kc.x + qc.y * kc.y;
+  const int nq = (int)(q1 - q0), nk = (int)(k1 - k0);
+  const int i0 = (int)(gridDim.x - 1 - blockIdx.x) * 2 * kRows;
+  if (i0 >= nq) return;
+  // key tiles of the two query tiles: row i sees the keys before nk - nq + i + 1
+  int tiles[2];
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    s *= a.scale;
-    const float m1 = fmaxf(m, s), keep = m1 == -INFINITY ? 1.f : expf(m - m1);
-    const float p = m1 == -INFINITY ? 0.f : expf(s - m1);
-    m = m1;
-    l = l * keep + p;
-    o[0] = o[0] * keep + p * va.x;
-    o[1] = o[1] * keep + p * va.y;
-    o[2] = o[2] * keep + p * vb.x;
-    o[3] = o[3] * keep + p * vb.y;
+  for (int t = 0; t < 2; t++) {
+    const int last = min(nq, i0 + (t + 1) * kRows);  // rows before this one
+    const int see = min(nk, nk - nq + last);
+    tiles[t] = i0 + t * kRows < nq && see > 0 ? (see + kTokens - 1) / kTokens : 0;
   }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  uint2 u;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o[1] * r), "f"(o[0] * r));
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o[3] * r), "f"(o[2] * r));
-  *reinterpret_cast<uint2*>(a.out + row * kVal + lane * 4) = u;
-  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
+  const int n0 = tiles[0], n1 = tiles[1], n = max(n0, n1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t raw = ptx::smem_addr(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
+  const uint32_t sb = ptx::smem_addr(smem);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 4);
+  const auto bar = [&](int i) { return sb + kOffBar + i * 8; };
+  const auto full = [&](int i) { return bar(i); };
+  const auto empty = [&](int i) { return bar(kRing + i); };
+  const auto qfull = [&](int t) { return bar(2 * kRing + t); };
+  const auto sfull = [&](int t) { return bar(2 * kRing + 2 + t); };
+  const auto pfull = [&](int t) { return bar(2 * kRing + 4 + t); };
+  const auto ofull = [&](int t) { return bar(2 * kRing + 6 + t); };
+  const uint32_t done = bar(2 * kRing + 8);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRing; i++) {
+      ptx::mbar_init(full(i), 1);
+      ptx::mbar_init(empty(i), 1);
+    }
+    for (int t = 0; t < 2; t++) {
+      ptx::mbar_init(qfull(t), 1);
+      ptx::mbar_init(sfull(t), 1);
+      ptx::mbar_init(pfull(t), 4);
+      ptx::mbar_init(ofull(t), 1);
+    }
+    ptx::mbar_init(done, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctl ctl{abort_flag, a.status, 2 * p.wait_limit_ns};  // in cycles
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------ loads
+    // block b of the stream: key tile j is blocks 5 j .. 5 j + 2, value tile j 5 j + 3, 5 j + 4
+    const int blocks = p.idle_producers ? 0 : 5 * n;
+    bool ok = true;
+    int b = 0;
+    if (!p.idle_producers) {
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        if (tiles[t] > 0 && mma::elect_one()) {
+          ptx::mbar_arrive_expect_tx(qfull(t), 3 * kBlock);
+#pragma unroll
+          for (int c = 0; c < 3; c++)
+            tma_3d(sb + (3 * t + c) * kBlock, &q_map, c * 64, head, (int)q0 + i0 + t * kRows, qfull(t));
+        }
+        __syncwarp();
+      }
+    }
+    for (; b < blocks; b++) {
+      const int s = b % kRing, j = b / 5, c = b % 5;
+      ok = mma::wait_warp(empty(s), ((b / kRing) & 1) ^ 1, ctl);
+      if (!ok) break;
+      if (mma::elect_one()) {
+        ptx::mbar_arrive_expect_tx(full(s), kBlock);
+        const int row = (int)k0 + j * kTokens;
+        const uint32_t dst = sb + kOffRing + s * kBlock;
+        if (c == 2) tma_2d(dst, &r_map, 0, row, full(s));
+        else tma_3d(dst, &kv_map, c < 2 ? c * 64 : (c - 1) * 64, head, row, full(s));
+      }
+      __syncwarp();
+    }
+    // every copy lands before the CTA ends
+    for (int x = max(0, b - kRing); x < b; x++) mma::wait_warp(full(x % kRing), (x / kRing) & 1, ctl, false);
+    if (!p.idle_producers) {
+      for (int t = 0; t < 2; t++)
+        if (tiles[t] > 0) mma::wait_warp(qfull(t), 0, ctl, false);
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------ MMA issue (the warp as one)
+    constexpr uint32_t kIdS = mma::idesc_bf16(128, kTokens, false, false);
+    constexpr uint32_t kIdO = mma::idesc_bf16(128, 64, false, true);
+    const uint32_t qd = mma::desc_lo(sb, 0), kd = mma::desc_lo(sb + kOffRing, 0), vd = mma::desc_lo(sb + kOffRing, kBlock);
+    bool ok = true;
+    const auto wait_block = [&](int b) { return mma::wait_warp(full(b % kRing), (b / kRing) & 1, ctl); };
+    // scores of tile t and key tile j; the last user of the key tile frees its blocks
+    const auto scores = [&](int t, int j, bool frees) {
+#pragma unroll
+      for (int c = 0; c < 3; c++) {
+        const int b = 5 * j + c;
+        ok = ok && wait_block(b);
+        if (!ok) return;
+        ptx::tc_fence_after();
+        const uint32_t kb = kd + (b % kRing) * (kBlock >> 4);
+        if (mma::elect_one()) {
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            mma::mma_ss(tmem + t * 128, qd + (((3 * t + c) * kBlock + e * 32) >> 4), kb + ((e * 32) >> 4), kIdS, (c | e) != 0);
+          if (frees) ptx::mma_commit(empty(b % kRing));
+          if (c == 2) ptx::mma_commit(sfull(t));
+        }
+        __syncwarp();
+      }
+    };
+    const auto output = [&](int t, int j, bool frees, bool last) {
+      ok = ok && mma::wait_warp(pfull(t), j & 1, ctl);
+      if (!ok) return;
+      ptx::tc_fence_after();
+      // the two value blocks may lie on either side of the ring's end: one descriptor each
+#pragma unroll
+      for (int c = 0; c < 2; c++) {
+        const int b = 5 * j + 3 + c;
+        const uint32_t vb = vd + (b % kRing) * (kBlock >> 4);
+        if (mma::elect_one()) {
+#pragma unroll
+          for (int e = 0; e < 8; e++)
+            mma::mma_ts(tmem + kTmO + t * 128 + c * 64, tmem + t * 128 + e * 8, vb + ((e * 2048) >> 4),
+                        kIdO, j > 0 || e > 0);
+          if (frees) ptx::mma_commit(empty(b % kRing));
+          if (last && c == 1) ptx::mma_commit(ofull(t));
+        }
+        __syncwarp();
+      }
+    };
+    // a value tile that ends behind the sequence: its rows there (another sequence's, or
+    // anything) become zero, since a weight of zero does not hide a NaN
+    const auto values = [&](int j) {
+      for (int c = 3; c < 5; c++) ok = ok && wait_block(5 * j + c);
+      const int rows = nk - j * kTokens;
+      if (!ok || rows >= kTokens) return;
+      for (int c = 3; c < 5; c++) {
+        uint8_t* v = smem + kOffRing + ((5 * j + c) % kRing) * kBlock;
+        for (int i = rows * 8 + lane; i < kTokens * 8; i += 32) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+    };
+    // key tile j is last used by tile 1 if that reaches it, else by tile 0
+    if (n0 > 0) ok = mma::wait_warp(qfull(0), 0, ctl);
+    if (ok && n0 > 0) scores(0, 0, n1 == 0);
+    if (ok && n1 > 0) ok = mma::wait_warp(qfull(1), 0, ctl);
+    if (ok && n1 > 0) scores(1, 0, true);
+    for (int j = 0; ok && j < n; j++) {
+      values(j);
+      if (j < n0) {
+        output(0, j, j >= n1, j + 1 == n0);
+        if (j + 1 < n0) scores(0, j + 1, j + 1 >= n1);
+      }
+      if (j < n1) {
+        output(1, j, true, j + 1 == n1);
+        if (j + 1 < n1) scores(1, j + 1, true);
+      }
+    }
+    if (mma::elect_one()) ptx::mma_commit(done);
+    __syncwarp();
+    mma::wait_warp(done, 0, ctl, false);
+  } else if (warp < 8) {
+    // ------------------------------------------------------------ softmax and output
+    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int i = i0 + t * kRows + row;  // the thread's query row in its sequence
+    const int nt = t ? n1 : n0;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + t * 128 + lanes, to = tmem + kTmO + t * 128 + lanes;
+    const float cs = a.scale * 1.4426950408889634f;
+    const float2 cs2 = make_float2(cs, cs);
+    const int limit = min(nk, nk - nq + i + 1);       // keys before this one are seen
+    const int least = nk - nq + i0 + t * kRows + 1;   // ... by the tile's first row
+    float m = kNoMax, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < nt; j++) {
+      ok = mma::wait_warp(sfull(t), j & 1, ctl);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const int seen = limit - j * kTokens;  // columns before this one are seen
+      const bool masked = min(least, nk) < (j + 1) * kTokens;
+      uint32_t pk[64];
+      float sum = 0.f;
+      // one pass with the present reference; again, with a raised one, if a score passes it by far
+      for (bool again = j == 0;; again = true) {
+        if (again) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; c++) {
+            float v[32];
+            mma::ld_32x32(ts + c * 32, v);
+#pragma unroll
+            for (int e = 0; e < 32; e++) top = fmaxf(top, !masked || c * 32 + e < seen ? v[e] * cs : -INFINITY);
+          }
+          const float m1 = fmaxf(m, top);
+          if (j > 0) {
+            const float f = m1 == m ? 1.f : mma::exp2_approx(m - m1);
+            l *= f;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {
+              float o[16];
+              mma::ld_32x16(to + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; e++) o[e] *= f;
+              mma::st_32x16(to + c, o);
+            }
+            ptx::tmem_wait_st();
+          }
+          m = m1;
+        }
+        const float2 nm = make_float2(-m, -m);
+        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
+        float most = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          float2 v[16];
+          mma::ld_32x32(ts + c * 32, reinterpret_cast<float*>(v));
+#pragma unroll
+          for (int e = 0; e < 16; e++) {
+            float2 x = mma::fma2(v[e], cs2, nm);
+            if (masked) {
+              if (c * 32 + 2 * e >= seen) x.x = -INFINITY;
+              if (c * 32 + 2 * e + 1 >= seen) x.y = -INFINITY;
+            }
+            most = fmaxf(most, fmaxf(x.x, x.y));
+            const float2 w = make_float2(mma::exp2_approx(x.x), mma::exp2_approx(x.y));
+            if (e & 1) acc1 = mma::add2(acc1, w); else acc0 = mma::add2(acc0, w);
+            pk[c * 16 + e] = mma::pack_bf16(w.x, w.y);
+          }
+        }
+        sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
+        if (again || !__any_sync(kFull, most > kRaise)) break;
+      }
+      l += sum;
+#pragma unroll
+      for (int c = 0; c < 4; c++) mma::st_32x16(ts + c * 16, reinterpret_cast<float*>(pk + c * 16));
+      ptx::tmem_wait_st();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(pfull(t));
+    }
+    if (ok && nt > 0) ok = mma::wait_warp(ofull(t), 0, ctl);
+    const bool in = i < nq;
+    if (ok) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // through the tile's query blocks, which are free: a warp's 32 rows of 256 bytes
+      uint8_t* st = smem + t * 3 * kBlock + (warp & 3) * 8192;
+      if (nt > 0) {
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          float o[32];
+          mma::ld_32x32(to + c * 32, o);
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const float* x = o + 8 * e;
+            const uint4 u = make_uint4(mma::pack_bf16(x[0] * inv, x[1] * inv), mma::pack_bf16(x[2] * inv, x[3] * inv),
+                                       mma::pack_bf16(x[4] * inv, x[5] * inv), mma::pack_bf16(x[6] * inv, x[7] * inv));
+            *reinterpret_cast<uint4*>(st + lane * 256 + (((c * 4 + e) ^ (lane & 15)) << 4)) = u;
+          }
+        }
+      }
+      __syncwarp();
+      const int64_t r0 = q0 + i0 + t * kRows + (warp & 3) * 32;
+      const int rows = min(32, nq - (i0 + t * kRows + (warp & 3) * 32));
+      for (int r = lane >> 4; r < rows; r += 2) {
+        const int pc = lane & 15;
+        const uint4 u = nt > 0 ? *reinterpret_cast<const uint4*>(st + r * 256 + ((pc ^ (r & 15)) << 4)) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(a.out + ((r0 + r) * a.heads + head) * kVal + pc * 8) = u;
+      }
+      if (in && a.lse)
+        a.lse[(q0 + i) * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
+}
+
+// [rows, heads, width] bf16, in boxes of 128 rows of one head x 64 dims, 128-byte swizzle.
+bool encode_heads(CUtensorMap* map, const void* base, int64_t rows, int32_t heads, int32_t width) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * heads};
+  cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_rope(CUtensorMap* map, const void* base, int64_t rows) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {64, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {64, 128}, es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
 cudaError_t launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream) {
-  const dim3 grid((a.max_q + kWarps - 1) / kWarps, a.heads, a.n_seqs);
-  latent_prefill_kernel<<<grid, kWarps * 32, 0, stream>>>(a);
+  Params p{a, pipeline_wait_limit_ns(), pipeline_idle_producers() ? 1 : 0};
+  CUtensorMap q_map, kv_map, r_map;
+  // without any key the maps are never used: they then describe the queries' memory
+  const bool keys = a.n_kv > 0;
+  if (!encode_heads(&q_map, a.q, a.n_q, a.heads, kKey) ||
+      !encode_heads(&kv_map, keys ? a.kv : a.q, keys ? a.n_kv : 1, keys ? a.heads : 1, keys ? 256 : 64) ||
+      !encode_rope(&r_map, keys ? a.k_rope : a.q, keys ? a.n_kv : 1))
+    return cudaErrorInvalidValue;
+  const void* kernel = reinterpret_cast<const void*>(latent_prefill_kernel);
+  cudaError_t e = set_smem_attr_once(kernel, kBytes);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((a.max_q + 2 * kRows - 1) / (2 * kRows), a.heads, a.n_seqs);
+  latent_prefill_kernel<<<grid, kThreads, kBytes, stream>>>(q_map, kv_map, r_map, p);
   return cudaGetLastError();
 }
 
