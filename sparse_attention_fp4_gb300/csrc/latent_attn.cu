@@ -14,12 +14,13 @@
 // One persistent CTA an SM:
 //   warps 0-3   (0-7 with 64 columns, half of them each) softmax: S^T from tensor memory, masks, exp2, P^T to shared memory; at the end
 //               of a segment the output
-//   then a warp that issues the MMAs,
+//   then two warps that issue the MMAs of either product,
 //   a warp      that copies a segment's queries,
 //   a warp      that walks kAhead tiles ahead of the softmax and prefetches their tokens into L2, so
 //               that two stages in shared memory suffice to stream from HBM
-//   the others  groups of four warps, one per stage, copy tiles with 16-byte cp.async (rows of
-//               listed tokens or of a page; tokens that no row sees become zero rows)
+//   the others  groups of four warps, one per stage, copy tiles: whole pages by TMA, listed
+//               tokens and partial pages with 16-byte cp.async (tokens that no row sees become
+//               zero rows)
 // The work is the list of all units' tiles (a unit: one row, or adjacent rows of a sequence,
 // and up to 64 columns), cut into runs of tiles, one a CTA, whatever the lengths are.
 // A unit cut between CTAs leaves each piece's unnormalised output, maximum and sum in the
@@ -47,7 +48,7 @@ constexpr int kMaxCtas = 160;     // slots of the workspace
 constexpr int kCols = 64;         // columns of a workspace slot
 constexpr int kValue = FP4IDX_LATENT_VALUE;
 // roles behind the softmax warps
-constexpr int kMmaRole = 0, kQueryRole = 1, kAheadRole = 2, kLoadRole = 3;
+constexpr int kScoreRole = 0, kOutRole = 1, kQueryRole = 2, kAheadRole = 3, kLoadRole = 4;
 constexpr uint32_t kAhead = 3;    // tiles that the prefetches are ahead of the softmax
 constexpr int kMaxGroup = 8;      // rows a unit
 constexpr float kRaise = 8.f;
@@ -355,7 +356,8 @@ struct Shape {
   // a third stage where it fits (width 512 with at most 16 columns)
   static constexpr int kStages = 3 * (kStageBytes + kQChunk) + kChunks * kQChunk <= 225 * 1024 && kOwnP ? 3 : 2;
   static constexpr int kSoftWarps = kN == 64 ? 8 : 4;
-  static constexpr int kMmaWarp = kSoftWarps + kMmaRole, kQueryWarp = kSoftWarps + kQueryRole;
+  static constexpr int kScoreWarp = kSoftWarps + kScoreRole, kOutWarp = kSoftWarps + kOutRole;
+  static constexpr int kQueryWarp = kSoftWarps + kQueryRole;
   static constexpr int kAheadWarp = kSoftWarps + kAheadRole, kLoadWarp = kSoftWarps + kLoadRole;
   static constexpr int kThreads = (kLoadWarp + 4 * kStages) * 32;
   static constexpr uint32_t kOffQ = kStages * kStageBytes;
@@ -378,10 +380,11 @@ struct Shape {
 // The scan's scratch lies in the query buffer, which is not in use yet.
 
 template <int kWidth, int kN>
-__global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ CUtensorMap cache_map,
+                                                                                   const __grid_constant__ Params p) {
   using S = Shape<kWidth, kN>;
   constexpr int kStages = S::kStages, kChunks = S::kChunks, kSoft = S::kSoftWarps * 32;
-  constexpr int kMmaWarp = S::kMmaWarp, kQueryWarp = S::kQueryWarp, kAheadWarp = S::kAheadWarp, kLoadWarp = S::kLoadWarp;
+  constexpr int kScoreWarp = S::kScoreWarp, kOutWarp = S::kOutWarp, kQueryWarp = S::kQueryWarp, kAheadWarp = S::kAheadWarp, kLoadWarp = S::kLoadWarp;
   constexpr int kMyCols = kN * 4 / S::kSoftWarps, kJ = kMyCols / 8;  // columns of a softmax warp
   extern __shared__ uint8_t smem_raw[];
   const LatentArgs& a = p.a;
@@ -414,12 +417,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::mbar_init(sfull(1), 1);
     ptx::mbar_init(pfull(0), S::kSoftWarps);
     ptx::mbar_init(pfull(1), S::kSoftWarps);
-    ptx::mbar_init(done, 1);
+    ptx::mbar_init(done, 2);
     *abort_flag = 0;
     *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = 0;  // tiles that the softmax has begun
     ptx::fence_mbar_init();
   }
-  if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
+  if (warp == kScoreWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
   // Lists, page table and queries into L2, a line a thread of the whole grid, while the run is
   // being found: three dependent reads lie between the lengths and the first tile.
   {
@@ -467,6 +470,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     };
     // A tile's tokens are looked up two steps ahead, positions and then page ids, one token a
     // lane; each value is used an iteration after its load was issued.
+    bool whole1 = false, whole2 = false;  // every row sees all of the tile, which is one page
     int pos1 = 0, pos2 = 0;        // of the group's next tile, and of the one after it
     uint32_t rows1 = 0, rows2 = 0;  // rows of the unit that see the token, if its position is valid
     int32_t page1 = -1;
@@ -475,6 +479,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       table2 = a.page_table + (int64_t)seg.u.seq * a.max_pages;
       pos2 = t * kTile + tok;
       rows2 = 0;
+      whole2 = !a.idx && (t + 1) * kTile <= seg.u.min_len;
       if (pos2 < seg.u.min_len) {
         rows2 = (1u << seg.u.rows) - 1;
         if (a.idx) pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
@@ -488,6 +493,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     };
     auto pages = [&]() {
       pos1 = pos2;
+      whole1 = whole2;
       rows1 = pos2 >= 0 ? rows2 : 0;
       page1 = -1;
       if (rows1) {
@@ -501,7 +507,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     };
     if (have && grp > 0) advance(grp);
     uint32_t kcur = kctr;
-    bool have1 = have;
+    bool have1 = have, tma = false;
+    uint32_t last = 0;
     if (have) {
       positions();
       pages();
@@ -516,6 +523,35 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (!in && rows1) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
       const int slot = in ? page1 * kPage + (pos1 & (kPage - 1)) : -1;
       if (lane < 16) smem[S::kOffSeen + s * kTile + tok] = (uint8_t)(in ? rows1 : 0);
+      const uint32_t dst = sb + s * S::kStageBytes;
+      last = kcur;
+      have1 = have;
+      // (a page outside the cache takes the other path: its rows become zero)
+      tma = __all_sync(kFull, whole1 && in);
+      if (tma) {
+        // a whole page: one box of 64 tokens x 64 dims a block, issued by the first warp
+        const int row = __shfl_sync(kFull, page1, 0) * kPage;
+        __syncwarp();
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+          if (half && !mma::wait_warp(kempty(s, 1), free, ctl)) break;
+          if (tid >= 32) {
+            arrive_warp(kfull(s, half), lane);
+          } else if (mma::elect_one()) {
+            const int c0 = half ? 4 : 0, c1 = half ? kChunks : 4;
+            ptx::mbar_arrive_expect_tx(kfull(s, half), (c1 - c0) * kTile * 128);
+            for (int c = c0; c < c1; c++) mma::tma_2d(dst + c * (kTile * 128), &cache_map, c * 64, row, kfull(s, half));
+          }
+          __syncwarp();
+        }
+        kcur = kctr;
+        if (have) {
+          pages();
+          advance(kStages);
+          if (have) positions();
+        }
+        continue;
+      }
       const uint16_t* src[4];
       uint32_t bytes[4];
 #pragma unroll
@@ -524,7 +560,6 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         src[g] = a.cache + (int64_t)max(of, 0) * kWidth + piece * 8;
         bytes[g] = of >= 0 ? 16 : 0;
       }
-      const uint32_t dst = sb + s * S::kStageBytes;
 #pragma unroll
       for (int c = 0; c < kChunks; c++) {
         if (c == 4) {
@@ -536,7 +571,6 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
       }
       mma::cp_async_commit();
-      have1 = have;
       const uint32_t kdone = kcur;
       kcur = kctr;
       if (have) {
@@ -552,6 +586,11 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       arrive_warp(kfull(kdone % kStages, 1), lane);
     }
     mma::cp_async_wait_all();
+    // every copy lands before the CTA ends
+    if (tma && tid < 32) {
+      mma::wait_warp(kfull(last % kStages, 0), (last / kStages) & 1, ctl, false);
+      mma::wait_warp(kfull(last % kStages, 1), (last / kStages) & 1, ctl, false);
+    }
   } else if (any && warp == kQueryWarp) {
     // ------------------------------------------------------------ queries
     uint32_t ictr = 0;
@@ -604,76 +643,72 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         }
       }
     } while (on && next_seg(p, seg));
-  } else if (any && warp == kMmaWarp) {
-    // ------------------------------------------------------------ MMA issue (the warp as one)
+  } else if (any && warp == kScoreWarp) {
+    // ------------------------------------------------------------ the first product (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
-    constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
-    const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0);
-    auto ready = [&](uint32_t b, uint32_t parity) { return __all_sync(kFull, ptx::mbar_test_wait(b, parity)) != 0; };
-    const uint32_t kd0 = mma::desc_lo(sb, 0), vd0 = mma::desc_lo(sb, kTile * 128);
-    constexpr uint32_t kStageLo = S::kStageBytes >> 4;
-    // the next half of scores to issue: stage, phase and half; the next tile's weights
-    uint32_t s_stage = 0, s_phase = 0, s_half = 0, s_buf = 0;
-    uint32_t o_stage = 0, o_tile = 0, q_phase = 0;
+    const uint32_t qd = mma::desc_lo(sb + S::kOffQ, 0), kd0 = mma::desc_lo(sb, 0);
+    uint32_t stage = 0, phase = 0, buf = 0, q_phase = 0;
     bool ok = true;
     do {
       const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
       ok = mma::wait_warp(qfull, q_phase, ctl);
       q_phase ^= 1;
-      uint32_t left = 2 * n;  // halves of scores of this segment not issued yet
       for (uint32_t i = 0; ok && i < n; i++) {
-        // This tile's scores, if they have not been issued; then, until its weights are there,
-        // the next tile's scores as their halves land.
-        const uint32_t behind = 2 * (n - 1 - i);  // halves left once this tile's are issued
-        const int64_t t0 = clock64();
-        for (uint32_t it = 1;; it++) {
-          if (left <= behind && ready(pfull(o_tile & 1), (o_tile >> 1) & 1)) break;
-          if (left && left + 2 > behind && ready(kfull(s_stage, s_half), s_phase)) {
-            ptx::tc_fence_after();
-            const uint32_t kd = kd0 + s_stage * kStageLo, d = tm_s + s_buf * kN;
-            left--;
-            if (s_half == 0) {
-              if (mma::elect_one()) {
-#pragma unroll
-                for (int c = 0; c < 4; c++)
-#pragma unroll
-                  for (int e = 0; e < 4; e++)
-                    mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS,
-                                (c | e) != 0);
-              }
-              s_half = 1;
-            } else {
-              if (mma::elect_one()) {
-#pragma unroll
-                for (int c = 4; c < kChunks; c++)
-#pragma unroll
-                  for (int e = 0; e < 4; e++)
-                    mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS,
-                                true);
-                ptx::mma_commit(sfull(s_buf));
-                if (left == 0) ptx::mma_commit(qempty);
-              }
-              s_half = 0;
-              s_buf ^= 1;
-              if (++s_stage == kStages) {
-                s_stage = 0;
-                s_phase ^= 1;
-              }
-            }
-            __syncwarp();
-            continue;
-          }
-          if ((it & 63u) == 0) {
-            if (*ctl.abort) ok = false;
-            else if (clock64() - t0 > (int64_t)ctl.timeout_ns) ok = pipe::give_up(ctl);
-            ok = __all_sync(kFull, ok);
-            if (!ok) break;
-          }
+        // The scores' buffer was last used two tiles ago.  Its reader is done once that
+        // tile's second product has begun, which with two stages the loads wait for too.
+        if (kStages > 2) {
+          const uint32_t at = stage >= 2 ? stage - 2 : stage + kStages - 2;
+          ok = mma::wait_warp(kempty(at, 0), (stage >= 2 ? phase : phase ^ 1), ctl);
+          if (!ok) break;
         }
+        const uint32_t kd = kd0 + stage * (S::kStageBytes >> 4), d = tm_s + buf * kN;
+        ok = mma::wait_warp(kfull(stage, 0), phase, ctl);
         if (!ok) break;
-        o_tile++;
         ptx::tc_fence_after();
-        const uint32_t vd = vd0 + o_stage * kStageLo, pd = mma::desc_lo(sb + S::off_p(o_stage), 0);
+        if (mma::elect_one()) {
+#pragma unroll
+          for (int c = 0; c < 4; c++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS, (c | e) != 0);
+        }
+        __syncwarp();
+        ok = mma::wait_warp(kfull(stage, 1), phase, ctl);
+        if (!ok) break;
+        if (mma::elect_one()) {
+#pragma unroll
+          for (int c = 4; c < kChunks; c++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              mma::mma_ss(d, kd + ((c * (kTile * 128) + e * 32) >> 4), qd + ((c * S::kQChunk + e * 32) >> 4), kIdS, true);
+          ptx::mma_commit(sfull(buf));
+          if (i + 1 == n) ptx::mma_commit(qempty);
+        }
+        __syncwarp();
+        buf ^= 1;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    } while (ok && next_seg(p, seg));
+    // nothing of this CTA's may be under way in the tensor cores when it ends
+    if (mma::elect_one()) ptx::mma_commit(done);
+    __syncwarp();
+    mma::wait_warp(done, 0, ctl, false);
+  } else if (any && warp == kOutWarp) {
+    // ------------------------------------------------------------ the second product
+    constexpr uint32_t kIdO = mma::idesc_bf16(128, kN, true, false);
+    const uint32_t vd0 = mma::desc_lo(sb, kTile * 128);
+    uint32_t stage = 0, tile = 0;
+    bool ok = true;
+    do {
+      const uint32_t n = __shfl_sync(kFull, (uint32_t)(seg.t1 - seg.t0), 0);
+      for (uint32_t i = 0; ok && i < n; i++, tile++) {
+        ok = mma::wait_warp(pfull(tile & 1), (tile >> 1) & 1, ctl);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t vd = vd0 + stage * (S::kStageBytes >> 4), pd = mma::desc_lo(sb + S::off_p(stage), 0);
         if (mma::elect_one()) {
 #pragma unroll
           for (int half = 0; half < 2; half++) {
@@ -683,14 +718,13 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
               for (int b = 2 * half; b < 2 * half + 2; b++)
                 mma::mma_ss(tmem + b * kN, vd + ((b * (2 * kTile * 128) + ks * 2048) >> 4), pd + ((ks * 32) >> 4), kIdO,
                             ks > 0 || i > 0);
-            ptx::mma_commit(kempty(o_stage, half));
+            ptx::mma_commit(kempty(stage, half));
           }
         }
         __syncwarp();
-        if (++o_stage == kStages) o_stage = 0;
+        if (++stage == kStages) stage = 0;
       }
     } while (ok && next_seg(p, seg));
-    // nothing of this CTA's may be under way in the tensor cores when it ends
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
     mma::wait_warp(done, 0, ctl, false);
@@ -936,7 +970,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
+  if (warp == kScoreWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
 // ---------------------------------------------------------------- joining the pieces
@@ -1052,6 +1086,18 @@ __global__ void __launch_bounds__(kBlockCols * kGroups * 32) combine_kernel(cons
   if (lane == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }
 
+// [rows, width] bf16, in boxes of 64 rows x 64 dims, 128-byte swizzle.
+bool encode_cache(CUtensorMap* map, const void* base, int64_t rows, int32_t width) {
+  EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)width * 2};
+  cuuint32_t box[2] = {64, kTile}, es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kWidth, int kN>
 cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t stream) {
   using S = Shape<kWidth, kN>;
@@ -1059,6 +1105,8 @@ cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t strea
   static_assert(S::kThreads <= kMaxWarps * 32, "");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN>);
+  CUtensorMap cache_map;
+  if (!encode_cache(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth)) return cudaErrorInvalidValue;
   cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
   if (e != cudaSuccess) return e;
   // Both launches may begin while the one before them ends: each waits for it before its
@@ -1073,7 +1121,7 @@ cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t strea
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kBytes;
-  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, p);
+  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, cache_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most
   const bool many = units * 8 <= ctas;  // eight pieces a unit or more

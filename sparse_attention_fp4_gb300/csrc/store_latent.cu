@@ -29,12 +29,7 @@ __device__ __forceinline__ uint4 pack(const float* v) {
 }
 // The eight lanes of a rotated run of 64 dims: lane r of the run holds dims 8r..8r+7, its
 // pair's other half four lanes away.  Every lane of the warp takes part in the shuffles.
-__device__ __forceinline__ void rope(float* v, int r, const uint16_t* __restrict__ cs, bool rotate) {
-  uint4 uc = make_uint4(0, 0, 0, 0), us = uc;
-  if (rotate) {
-    uc = *reinterpret_cast<const uint4*>(cs + (r & 3) * 8);
-    us = *reinterpret_cast<const uint4*>(cs + 32 + (r & 3) * 8);
-  }
+__device__ __forceinline__ void rope(float* v, int r, const uint4& uc, const uint4& us, bool rotate) {
   float c[8], s[8];
   unpack(uc, c);
   unpack(us, s);
@@ -45,6 +40,8 @@ __device__ __forceinline__ void rope(float* v, int r, const uint16_t* __restrict
   }
 }
 
+// A warp walks rows `step` apart.  The row's values and its cos/sin are loaded a row ahead,
+// its slot and position two rows ahead, so that no load waits for another.
 template <int kWidth>
 __global__ void __launch_bounds__(kWarps * 32) store_latent_kernel(
     const uint16_t* __restrict__ kv, int64_t n_rows, const int32_t* __restrict__ positions,
@@ -52,42 +49,69 @@ __global__ void __launch_bounds__(kWarps * 32) store_latent_kernel(
     const uint16_t* __restrict__ cos_sin, int32_t max_pos, uint16_t* __restrict__ cache, int64_t num_pages,
     int32_t* status) {
   const int lane = threadIdx.x & 31;
+  const bool rotates = kWidth == 576 ? lane < 8 : lane >= 24;
   float w0[8], w1[8];
   unpack(*reinterpret_cast<const uint4*>(norm_w + lane * 8), w0);
   unpack(*reinterpret_cast<const uint4*>(norm_w + 256 + lane * 8), w1);
-  for (int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); n < n_rows; n += (int64_t)gridDim.x * kWarps) {
-    const int32_t slot = slots[n], pos = positions[n];
-    if (slot < 0) continue;
-    if (slot >= num_pages * kPage || pos < 0 || pos >= max_pos) {
-      if (lane == 0) record_error(status, slot >= num_pages * kPage ? FP4IDX_ERR_BAD_PAGE : FP4IDX_ERR_BAD_POSITION);
-      continue;
-    }
+  struct Meta {
+    int32_t slot, pos;
+  };
+  struct Data {
+    uint4 a, b, t, c, s;
+  };
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  const auto meta = [&](int64_t n) {
+    return n < n_rows ? Meta{__ldg(slots + n), __ldg(positions + n)} : Meta{-1, 0};
+  };
+  const auto data = [&](int64_t n, const Meta& m) {
+    Data d{none, none, none, none, none};
+    if (m.slot < 0) return d;
     const uint16_t* x = kv + n * kWidth;
-    const uint16_t* cs = cos_sin + (int64_t)pos * kRope;
-    float a[8], b[8], t[8];
-    unpack(*reinterpret_cast<const uint4*>(x + lane * 8), a);
-    unpack(*reinterpret_cast<const uint4*>(x + 256 + lane * 8), b);
-    if (kWidth == 576) unpack(lane < 8 ? *reinterpret_cast<const uint4*>(x + 512 + lane * 8) : make_uint4(0, 0, 0, 0), t);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; i++) ss += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) ss += __shfl_xor_sync(~0u, ss, d);
-    const float r = __fdiv_rn(1.f, __fsqrt_rn(ss * (1.f / kValue) + eps));
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-      a[i] = a[i] * r * w0[i];
-      b[i] = b[i] * r * w1[i];
+    d.a = __ldcs(reinterpret_cast<const uint4*>(x + lane * 8));
+    d.b = __ldcs(reinterpret_cast<const uint4*>(x + 256 + lane * 8));
+    if (kWidth == 576 && rotates) d.t = __ldcs(reinterpret_cast<const uint4*>(x + 512 + lane * 8));
+    if (rotates && m.pos >= 0 && m.pos < max_pos) {
+      const uint16_t* cs = cos_sin + (int64_t)m.pos * kRope + (lane & 3) * 8;
+      d.c = __ldg(reinterpret_cast<const uint4*>(cs));
+      d.s = __ldg(reinterpret_cast<const uint4*>(cs + 32));
     }
-    uint16_t* y = cache + (int64_t)slot * kWidth;
-    if (kWidth == 576) {
-      rope(t, lane & 7, cs, lane < 8);
-      if (lane < 8) *reinterpret_cast<uint4*>(y + 512 + lane * 8) = pack(t);
-    } else {
-      rope(b, lane & 7, cs, lane >= 24);
+    return d;
+  };
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t n = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  Meta m = meta(n), m1 = meta(n + step);
+  Data d = data(n, m);
+  for (; n < n_rows; n += step) {
+    const Data d1 = data(n + step, m1);
+    const Meta m2 = meta(n + 2 * step);
+    const bool bad_slot = m.slot >= num_pages * kPage, bad_pos = m.pos < 0 || m.pos >= max_pos;
+    if (m.slot >= 0 && (bad_slot || bad_pos)) {
+      if (lane == 0) record_error(status, bad_slot ? FP4IDX_ERR_BAD_PAGE : FP4IDX_ERR_BAD_POSITION);
+    } else if (m.slot >= 0) {
+      float a[8], b[8], t[8];
+      unpack(d.a, a);
+      unpack(d.b, b);
+      if (kWidth == 576) unpack(d.t, t);
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; i++) ss += a[i] * a[i] + b[i] * b[i];
+#pragma unroll
+      for (int x = 16; x > 0; x >>= 1) ss += __shfl_xor_sync(~0u, ss, x);
+      const float r = __fdiv_rn(1.f, __fsqrt_rn(ss * (1.f / kValue) + eps));
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        a[i] = a[i] * r * w0[i];
+        b[i] = b[i] * r * w1[i];
+      }
+      uint16_t* y = cache + (int64_t)m.slot * kWidth;
+      rope(kWidth == 576 ? t : b, lane & 7, d.c, d.s, rotates);
+      if (kWidth == 576 && rotates) *reinterpret_cast<uint4*>(y + 512 + lane * 8) = pack(t);
+      *reinterpret_cast<uint4*>(y + lane * 8) = pack(a);
+      *reinterpret_cast<uint4*>(y + 256 + lane * 8) = pack(b);
     }
-    *reinterpret_cast<uint4*>(y + lane * 8) = pack(a);
-    *reinterpret_cast<uint4*>(y + 256 + lane * 8) = pack(b);
+    d = d1;
+    m = m1;
+    m1 = m2;
   }
 }
 

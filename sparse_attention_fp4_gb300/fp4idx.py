@@ -433,15 +433,16 @@ class _Args:
         self.stream = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
 
     def __call__(self, t, name, dtypes, numel):
+        if (isinstance(t, torch.Tensor) and t.get_device() == self.device and t.dtype in dtypes and t.is_contiguous()
+                and (numel == 0 or t.numel() >= numel)):
+            return t.data_ptr()
         if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
             raise ValueError("%s must be a CUDA tensor on the current device" % name)
         if t.dtype not in dtypes:
             raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
         if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
-        if t.numel() < numel:
-            raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
-        return t.data_ptr()
+        raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
 
     def optional(self, t, name, dtypes, numel):
         return None if t is None else self(t, name, dtypes, numel)
