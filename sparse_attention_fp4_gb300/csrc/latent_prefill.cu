@@ -20,6 +20,7 @@
 // ever rescaled and no maximum is taken after the first tile; the result does not depend on m.
 // Queries of longer contexts have smaller block indices: the longest work starts first.
 #include <algorithm>
+#include <type_traits>
 
 #include "launchers.cuh"
 #include "mma_bf16.cuh"
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       const bool masked = min(least, nk) < (j + 1) * kTokens;
       uint32_t pk[32];
       float sum;
-      const auto weights = [&]() {
+      const auto weights = [&](auto mask) {  // mask: whether some columns are not seen
         float2 v[32];
         mma::ld_32x64(ts + half * 64, reinterpret_cast<float*>(v));
         const float2 nm = make_float2(-m, -m);
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 32; e++) {
           float2 x = mma::fma2(v[e], cs2, nm);
-          if (masked) {
+          if (decltype(mask)::value) {
             if (2 * e >= seen) x.x = -INFINITY;
             if (2 * e + 1 >= seen) x.y = -INFINITY;
           }
@@ -314,7 +315,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         }
         sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
       };
-      if (j > 0) weights();
+      const auto all_weights = [&]() {
+        if (masked) weights(std::true_type{});
+        else weights(std::false_type{});
+      };
+      if (j > 0) all_weights();
       if (mma::bar_any(pair, 64, j == 0 || sum > kRaise || !ok)) {
         if (mma::bar_any(pair, 64, !ok)) {
           ok = false;
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
           ptx::tmem_wait_st();
         }
         m = m1;
-        weights();
+        all_weights();
         ptx::named_bar_sync(pair, 64);  // red is read
       }
       l += sum;
