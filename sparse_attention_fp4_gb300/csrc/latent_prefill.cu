@@ -2,20 +2,22 @@
 // per-head keys (128 own dims and 64 rotated ones that the heads share) and values (128 dims).
 //
 // A CTA takes 256 consecutive query rows of one (sequence, head), as two tiles of 128 that
-// share the key and value tiles (128 tokens) in shared memory:
-//   S = Q K^T          M = 128 rows, N = 128 tokens, K = 192     (Q, K in shared memory)
+// share the key and value tiles (112 tokens) in shared memory:
+//   S = Q K^T          M = 128 rows, N = 112 tokens, K = 192     (Q, K in shared memory)
 //   P = exp2(c S - m)  in place of S in tensor memory, bf16
-//   O += P V           M = 128 rows, N = 128 dims, K = 128       (P in tensor memory)
+//   O += P V           M = 128 rows, N = 128 dims, K = 112       (P in tensor memory)
 // Each tile has a warp that issues its products in bursts (PV, then S of the next tokens); the
 // warps take turns, so that one tile's softmax, and the few hundred cycles from a barrier to
 // the next issue, pass while the other's burst runs.  (Without turns their MMAs interleave,
 // both tiles' scores are done at once, and the tensor cores then wait for both softmaxes:
 // 1.06 ms instead of 0.80 for the long prompts below.)  Bound: 1,280 tensor cycles for a
 // 128 x 128 tile.
-//   warps 0-7, 8-15 softmax and output of tile 0, 1: two threads a row, 64 columns each
+//   warps 0-7, 8-15 softmax and output of tile 0, 1: two threads a row, 56 columns each
 //   warps 16, 17    issue the MMAs of tile 0, 1
-//   warp 18         issues the TMA loads into a ring of eight 16 KB blocks (128 tokens x 64
-//                   dims): three a key tile, two a value tile
+//   warp 18         issues the TMA loads into a ring of nine 14 KB blocks (112 tokens x 64
+//                   dims): three a key tile, two a value tile.  Tiles of 128 tokens leave
+//                   room for eight: two of a step's five blocks then come when they are
+//                   needed, not before (800 us)
 // m is raised only when the weights of a row's half tile sum to more than 2^16, so O is hardly
 // ever rescaled and no maximum is taken after the first tile; the result does not depend on m.
 // Queries of longer contexts have smaller block indices: the longest work starts first.
@@ -32,11 +34,11 @@ using pipe::Ctl;
 using pipe::kFull;
 
 constexpr int kKey = FP4IDX_PREFILL_KEY, kVal = FP4IDX_PREFILL_VALUE;
-constexpr int kRows = 128, kTokens = 128;
+constexpr int kRows = 128, kTokens = 112, kHalf = kTokens / 2;
 constexpr int kMmaWarp = 16, kLoadWarp = 18, kThreads = 608;
-constexpr int kRing = 8;
-constexpr uint32_t kBlock = 128 * 128;  // bytes: 128 rows of 64 bf16
-constexpr uint32_t kOffRing = 6 * kBlock;  // behind the two query tiles
+constexpr int kRing = 9;
+constexpr uint32_t kQBlock = kRows * 128, kBlock = kTokens * 128;  // bytes: rows of 64 bf16
+constexpr uint32_t kOffRing = 6 * kQBlock;  // behind the two query tiles
 constexpr uint32_t kOffBar = kOffRing + kRing * kBlock;
 // full[8], empty[8], qfull[2], sfull[2], pfull[2], ofull[2], done, tail, issued[2]
 constexpr int kBars = 2 * kRing + 12;
@@ -131,10 +133,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
 #pragma unroll
       for (int t = 0; t < 2; t++) {
         if (tiles[t] > 0 && mma::elect_one()) {
-          ptx::mbar_arrive_expect_tx(qfull(t), 3 * kBlock);
+          ptx::mbar_arrive_expect_tx(qfull(t), 3 * kQBlock);
 #pragma unroll
           for (int c = 0; c < 3; c++)
-            tma_3d(sb + (3 * t + c) * kBlock, &q_map, c * 64, head, (int)q0 + i0 + t * kRows, qfull(t));
+            tma_3d(sb + (3 * t + c) * kQBlock, &q_map, c * 64, head, (int)q0 + i0 + t * kRows, qfull(t));
         }
         __syncwarp();
       }
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     constexpr uint32_t kIdS = mma::idesc_bf16(128, kTokens, false, false);
     constexpr uint32_t kIdO = mma::idesc_bf16(128, 64, false, true);
     const int t = __shfl_sync(kFull, warp - kMmaWarp, 0), nt = t ? n1 : n0;
-    const uint32_t qd = mma::desc_lo(sb + t * 3 * kBlock, 0), kd = mma::desc_lo(sb + kOffRing, 0);
+    const uint32_t qd = mma::desc_lo(sb + t * 3 * kQBlock, 0), kd = mma::desc_lo(sb + kOffRing, 0);
     const uint32_t vd = mma::desc_lo(sb + kOffRing, kBlock);
     const uint32_t ts = tmem + t * 128, to = tmem + kTmO + t * 128;
     uint32_t slot = 0, phase = 0;  // of the stream's next block
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         const uint32_t kb = kd + k_slot[c] * (kBlock >> 4);
 #pragma unroll
         for (int e = 0; e < 4; e++)
-          mma::mma_ss(ts, qd + ((c * kBlock + e * 32) >> 4), kb + ((e * 32) >> 4), kIdS, (c | e) != 0);
+          mma::mma_ss(ts, qd + ((c * kQBlock + e * 32) >> 4), kb + ((e * 32) >> 4), kIdS, (c | e) != 0);
         ptx::mma_commit(empty(k_slot[c]));
       }
       ptx::mma_commit(sfull(t));
@@ -247,10 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       const uint32_t vb0 = vd + v_slot[0] * (kBlock >> 4), vb1 = vd + v_slot[1] * (kBlock >> 4);
       if (mma::elect_one()) {
 #pragma unroll
-        for (int e = 0; e < 8; e++) mma::mma_ts(to, ts + e * 8, vb0 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
+        for (int e = 0; e < kTokens / 16; e++) mma::mma_ts(to, ts + e * 8, vb0 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
         ptx::mma_commit(empty(v_slot[0]));
 #pragma unroll
-        for (int e = 0; e < 8; e++) mma::mma_ts(to + 64, ts + e * 8, vb1 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
+        for (int e = 0; e < kTokens / 16; e++) mma::mma_ts(to + 64, ts + e * 8, vb1 + ((e * 2048) >> 4), kIdO, j > 0 || e > 0);
         ptx::mma_commit(empty(v_slot[1]));
         if (j + 1 == nt) ptx::mma_commit(ofull(t));
         else scores();
@@ -293,17 +295,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       // a warp whose wait ran out goes on to the next vote, so that the pair leaves together
       ok = ok && mma::wait_warp(sfull(t), j & 1, ctl);
       ptx::tc_fence_after();
-      const int seen = limit - j * kTokens - half * 64;  // columns before this one are seen
+      const int seen = limit - j * kTokens - half * kHalf;  // columns before this one are seen
       const bool masked = min(least, nk) < (j + 1) * kTokens;
-      uint32_t pk[32];
+      uint32_t pk[kHalf / 2];
       float sum;
       const auto weights = [&](auto mask) {  // mask: whether some columns are not seen
-        float2 v[32];
-        mma::ld_32x64(ts + half * 64, reinterpret_cast<float*>(v));
+        float2 v[kHalf / 2];
+        mma::ld_32x56(ts + half * kHalf, reinterpret_cast<float*>(v));
         const float2 nm = make_float2(-m, -m);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int e = 0; e < 32; e++) {
+        for (int e = 0; e < kHalf / 2; e++) {
           float2 x = mma::fma2(v[e], cs2, nm);
           if (decltype(mask)::value) {
             if (2 * e >= seen) x.x = -INFINITY;
@@ -328,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         // the scores are still there: no weight is stored before both warps have voted
         float top = -INFINITY;
         {
-          float v[64];
-          mma::ld_32x64(ts + half * 64, v);
+          float v[kHalf];
+          mma::ld_32x56(ts + half * kHalf, v);
 #pragma unroll
-          for (int e = 0; e < 64; e++)
+          for (int e = 0; e < kHalf; e++)
             if (!masked || e < seen) top = fmaxf(top, v[e] * cs);
         }
         red[half * kRows] = top;
@@ -356,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
         ptx::named_bar_sync(pair, 64);  // red is read
       }
       l += sum;
-#pragma unroll
-      for (int c = 0; c < 2; c++) mma::st_32x16(ts + half * 32 + c * 16, reinterpret_cast<float*>(pk + c * 16));
+      mma::st_32x28(ts + half * (kHalf / 2), pk);
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
       __syncwarp();
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
       l = red[0] + red[kRows];
       const float inv = l == 0.f ? 0.f : 1.f / l;
       // through the tile's query blocks, which are free: a warp's 32 rows of 128 bytes
-      uint8_t* st = smem + t * 3 * kBlock + (warp & 7) * 4096;
+      uint8_t* st = smem + t * 3 * kQBlock + (warp & 7) * 4096;
       if (nt > 0) {
         ptx::tc_fence_after();
 #pragma unroll
@@ -404,13 +405,13 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   if (warp == kMmaWarp) ptx::tmem_dealloc(tmem, 512);
 }
 
-// [rows, heads, width] bf16, in boxes of 128 rows of one head x 64 dims, 128-byte swizzle.
-bool encode_heads(CUtensorMap* map, const void* base, int64_t rows, int32_t heads, int32_t width) {
+// [rows, heads, width] bf16, in boxes of box_rows rows of one head x 64 dims, 128-byte swizzle.
+bool encode_heads(CUtensorMap* map, const void* base, int64_t rows, int32_t heads, int32_t width, int box_rows) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)heads, (cuuint64_t)rows};
   cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * heads};
-  cuuint32_t box[3] = {64, 1, 128}, es[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -420,7 +421,7 @@ bool encode_rope(CUtensorMap* map, const void* base, int64_t rows) {
   if (!fn) return false;
   cuuint64_t dims[2] = {64, (cuuint64_t)rows};
   cuuint64_t strides[1] = {128};
-  cuuint32_t box[2] = {64, 128}, es[2] = {1, 1};
+  cuuint32_t box[2] = {64, kTokens}, es[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -433,8 +434,8 @@ cudaError_t launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream) {
   CUtensorMap q_map, kv_map, r_map;
   // without any key the maps are never used: they then describe the queries' memory
   const bool keys = a.n_kv > 0;
-  if (!encode_heads(&q_map, a.q, a.n_q, a.heads, kKey) ||
-      !encode_heads(&kv_map, keys ? a.kv : a.q, keys ? a.n_kv : 1, keys ? a.heads : 1, keys ? 256 : 64) ||
+  if (!encode_heads(&q_map, a.q, a.n_q, a.heads, kKey, kRows) ||
+      !encode_heads(&kv_map, keys ? a.kv : a.q, keys ? a.n_kv : 1, keys ? a.heads : 1, keys ? 256 : 64, kTokens) ||
       !encode_rope(&r_map, keys ? a.k_rope : a.q, keys ? a.n_kv : 1))
     return cudaErrorInvalidValue;
   const void* kernel = reinterpret_cast<const void*>(latent_prefill_kernel);

@@ -212,19 +212,20 @@ __device__ __forceinline__ void ld_32x32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
-// 32 lanes x 64 columns.
-__device__ __forceinline__ void ld_32x64(uint32_t taddr, float* v) {
-  uint32_t r[64];
+// 32 lanes x 56 columns: three loads in flight together, one wait.
+__device__ __forceinline__ void ld_32x56(uint32_t taddr, float* v) {
+  uint32_t r[56];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\ttcgen05.wait::ld.sync.aligned;"
-      : FP4IDX_R8(0), FP4IDX_R8(8), FP4IDX_R8(16), FP4IDX_R8(24), FP4IDX_R8(32), FP4IDX_R8(40), FP4IDX_R8(48),
-        FP4IDX_R8(56)
-      : "r"(taddr)
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%56];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%57];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%48,%49,%50,%51,%52,%53,%54,%55}, [%58];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : FP4IDX_R8(0), FP4IDX_R8(8), FP4IDX_R8(16), FP4IDX_R8(24), FP4IDX_R8(32), FP4IDX_R8(40), FP4IDX_R8(48)
+      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 48)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 64; i++) v[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < 56; i++) v[i] = __uint_as_float(r[i]);
 }
 // 32 lanes x 8 columns.
 __device__ __forceinline__ void ld_32x8(uint32_t taddr, float* v) {
@@ -248,6 +249,17 @@ __device__ __forceinline__ void st_32x16(uint32_t taddr, const float* v) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// 32 lanes x 28 columns.
+__device__ __forceinline__ void st_32x28(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+  ptx::tmem_st8(taddr + 16, v + 16);
+  ptx::tmem_st4(taddr + 24, v[24], v[25], v[26], v[27]);
 }
 
 }  // namespace mma
