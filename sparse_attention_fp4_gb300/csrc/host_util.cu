@@ -6,6 +6,7 @@
 #include <map>
 #include <mutex>
 #include <set>
+#include <tuple>
 #include <utility>
 
 #include "launchers.cuh"
@@ -71,6 +72,37 @@ cudaError_t resident_ctas(const void* kernel, int threads, size_t smem, int* out
   if (e != cudaSuccess) return e;
   *out = std::max(1, per_sm) * sms;
   known[{kernel, dev}] = *out;
+  return cudaSuccess;
+}
+
+cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t smem, int* out) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int>, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = known.find({kernel, size, dev});
+  if (it != known.end()) {
+    *out = it->second;
+    return cudaSuccess;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(size, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e != cudaSuccess) return e;
+  *out = n;
+  known[{kernel, size, dev}] = n;
   return cudaSuccess;
 }
 

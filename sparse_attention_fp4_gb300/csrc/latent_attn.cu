@@ -32,6 +32,7 @@
 // depend on m; weights stay below 2^8.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "launchers.cuh"
 #include "mma_bf16.cuh"
@@ -58,6 +59,7 @@ struct Params {
   LatentArgs a;
   int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
   int32_t columns;            // selected rows: CTA c takes units c, c + grid, ... whole
+  int32_t cluster;            // CTAs of a cluster that share one unit; 0: the list is cut
   uint64_t wait_limit_ns;
   int32_t idle_producers;
 };
@@ -169,6 +171,9 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = 
 // 32 tiles make 128 pieces for the joining kernel instead of the 304 of an even cut over 152
 // CTAs (a piece's end costs as much as two tiles, and its 128 KB are written and read again).
 // Taken when `most` is at most an even share plus 1/16 and three tiles.
+// Few units, of rows with a selection each: a cluster of two, four or eight CTAs shares a unit and
+// adds its pieces up through distributed shared memory (no scan, no workspace, no second
+// launch, which together cost what three tiles do).
 // More units, of rows with a selection each, where whole rounds of units waste at most a
 // twentieth: CTA c takes units c, c + grid, ... whole.  No pieces, and the rows of one
 // sequence, whose selections overlap, are read at the same time (L2 then holds what they
@@ -240,6 +245,15 @@ __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& ru
 }
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
+  if (p.cluster) {
+    const int u = blockIdx.x / p.cluster, j = blockIdx.x % p.cluster;
+    load_unit(p, u / p.hb, s.u, threadIdx.x == 0 && j == 0);
+    s.hb = u % p.hb;
+    s.t0 = (int)((int64_t)s.u.tiles * j / p.cluster);
+    s.t1 = (int)((int64_t)s.u.tiles * (j + 1) / p.cluster);
+    s.left = s.t1 - s.t0;
+    return s.left > 0;
+  }
   if (p.columns) {
     const int u = blockIdx.x;
     load_unit(p, u / p.hb, s.u, threadIdx.x == 0);
@@ -436,7 +450,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   Seg seg;
   const bool any = first_seg(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
   Work wk = work_view(a.workspace);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && !p.cluster) {
     wk.rec[2 * blockIdx.x] = Record{0, 0, 0, 0};
     wk.rec[2 * blockIdx.x + 1] = Record{0, 0, 0, 0};
   }
@@ -553,23 +567,32 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         continue;
       }
       const uint16_t* src[4];
+      bool every = true;
       uint32_t bytes[4];
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         const int of = __shfl_sync(kFull, slot, g * 4 + (lane >> 3));
         src[g] = a.cache + (int64_t)max(of, 0) * kWidth + piece * 8;
         bytes[g] = of >= 0 ? 16 : 0;
+        every = every && of >= 0;
       }
+      const auto copy = [&](int c0, int c1, auto all) {
 #pragma unroll
-      for (int c = 0; c < kChunks; c++) {
-        if (c == 4) {
-          mma::cp_async_commit();
-          if (!mma::wait_warp(kempty(s, 1), free, ctl)) break;
-        }
+        for (int c = c0; c < c1; c++)
 #pragma unroll
-        for (int g = 0; g < 4; g++)
-          mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
-      }
+          for (int g = 0; g < 4; g++) {
+            const uint32_t to = dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece);
+            if (decltype(all)::value) mma::cp_async16(to, src[g] + c * 64);
+            else mma::cp_async16(to, src[g] + c * 64, bytes[g]);
+          }
+      };
+      every = __all_sync(kFull, every);
+      if (every) copy(0, 4, std::true_type{});
+      else copy(0, 4, std::false_type{});
+      mma::cp_async_commit();
+      if (!mma::wait_warp(kempty(s, 1), free, ctl)) break;
+      if (every) copy(4, kChunks, std::true_type{});
+      else copy(4, kChunks, std::false_type{});
       mma::cp_async_commit();
       const uint32_t kdone = kcur;
       kcur = kctr;
@@ -911,7 +934,9 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (threadIdx.x < kN) {
         const int c = threadIdx.x;
         const float total = red[c] + red[kN + c] + red[2 * kN + c] + red[3 * kN + c];
-        if (whole) {
+        if (p.cluster) {
+          sm_f[c] = total;
+        } else if (whole) {
           sm_f[c] = total == 0.f ? 0.f : 1.f / total;
           const int r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
           if (a.lse && r < seg.u.rows && h < p.hs && head < a.heads)
@@ -922,11 +947,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           wk.ml[slot * 2 * kCols + kCols + c] = total;
         }
       }
-      if (!whole && threadIdx.x == 0)
+      if (!whole && !p.cluster && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
       ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
+      if (p.cluster) break;  // the one piece: joined below
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
       if (whole) {
@@ -970,6 +996,71 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  if (p.cluster) {
+    // ---- the cluster's pieces are joined: each CTA for its share of the columns
+    // All main loops are over, so shared memory is free: pieces of the CTA's columns at 0,
+    // [piece][column][512] fp32, every piece's m and l in the query buffer.
+    const int ctas = p.cluster, mine = blockIdx.x % ctas, share = kN / ctas;
+    float* gather = reinterpret_cast<float*>(smem + S::kOffQ);  // [piece][2][kN]
+    float* sm_m = reinterpret_cast<float*>(smem + S::kOffM);
+    float* sm_l = reinterpret_cast<float*>(smem + S::kOffF);
+    mma::cluster_sync();
+    for (int i = threadIdx.x; i < ctas * kN; i += S::kThreads) {
+      const int c = i % kN, to = i / kN;
+      mma::st_cluster(mma::map_shared(ptx::smem_addr(gather + (mine * 2) * kN + c), to), any ? sm_m[c] : kNoMax);
+      mma::st_cluster(mma::map_shared(ptx::smem_addr(gather + (mine * 2 + 1) * kN + c), to), any ? sm_l[c] : 0.f);
+    }
+    if (any && warp < S::kSoftWarps) {
+      const int qw = warp & 3;
+      const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+#pragma unroll 1
+      for (int c = (warp >> 2) * kMyCols; c < ((warp >> 2) + 1) * kMyCols; c += 8) {
+#pragma unroll
+        for (int b = 0; b < 4; b++) {
+          float o[8];
+          mma::ld_32x8(tmem + b * kN + c + lanes, o);
+#pragma unroll
+          for (int e = 0; e < 8; e++) {
+            const int to = (c + e) / share, col = (c + e) % share;
+            mma::st_cluster(mma::map_shared(sb + ((mine * share + col) * kValue + b * 128 + qw * 32 + lane) * 4, to), o[e]);
+          }
+        }
+      }
+    }
+    mma::cluster_sync();
+    for (int col = warp; col < share; col += S::kThreads / 32) {
+      const int c = mine * share + col, h = c % p.hp, head = seg.hb * p.hs + h;
+      if (c >= p.hp || h >= p.hs || head >= a.heads) continue;  // one row a unit
+      float top = kNoMax, total = 0.f, o[16] = {};
+      for (int i = 0; i < ctas; i++) top = fmaxf(top, gather[(i * 2) * kN + c]);
+      for (int i = 0; i < ctas; i++) {
+        const float l = gather[(i * 2 + 1) * kN + c];
+        if (l == 0.f) continue;  // no token, and nothing in the piece
+        const float f = mma::exp2_approx(gather[(i * 2) * kN + c] - top);
+        total += f * l;
+        const float4* x = reinterpret_cast<const float4*>(smem) + ((i * share + col) * kValue) / 4 + lane;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+          const float4 y = x[32 * q];
+          o[4 * q] += f * y.x;
+          o[4 * q + 1] += f * y.y;
+          o[4 * q + 2] += f * y.z;
+          o[4 * q + 3] += f * y.w;
+        }
+      }
+      const float inv = total == 0.f ? 0.f : 1.f / total;
+      const int64_t row = (int64_t)seg.u.r0 * a.heads + head;
+#pragma unroll
+      for (int q = 0; q < 4; q++)
+        *reinterpret_cast<uint2*>(a.out + row * kValue + q * 128 + lane * 4) =
+            make_uint2(mma::pack_bf16(o[4 * q] * inv, o[4 * q + 1] * inv),
+                       mma::pack_bf16(o[4 * q + 2] * inv, o[4 * q + 3] * inv));
+      if (lane == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+  }
   if (warp == kScoreWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
 
@@ -1099,10 +1190,11 @@ bool encode_cache(CUtensorMap* map, const void* base, int64_t rows, int32_t widt
 }
 
 template <int kWidth, int kN>
-cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t stream) {
+cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   using S = Shape<kWidth, kN>;
   static_assert(S::kBytes <= 232448, "shared memory of a CTA");
   static_assert(S::kThreads <= kMaxWarps * 32, "");
+  static_assert(kN * kValue * 4 <= S::kOffQ, "a cluster's pieces fit the stages");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN>);
   CUtensorMap cache_map;
@@ -1112,7 +1204,7 @@ cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t strea
   // Both launches may begin while the one before them ends: each waits for it before its
   // first access to global memory.
   cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
@@ -1121,6 +1213,24 @@ cudaError_t launch(const Params& p, int ctas, bool may_split, cudaStream_t strea
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kBytes;
+  // A cluster a unit, of the largest size of which the device holds that many, if its CTAs get
+  // at most three tiles more than an even cut would give them.
+  const int units_all = p.a.n_rows * p.hb, tiles = p.a.idx ? (p.a.k + kTile - 1) / kTile : 0;
+  for (int c = 8; c >= 2 && may_split && p.a.idx; c /= 2) {
+    if ((int64_t)units_all * c > ctas || (tiles + c - 1) / c > ((int64_t)tiles * units_all + ctas - 1) / ctas + 3) continue;
+    int fit = 0;
+    e = resident_clusters(kernel, c, S::kThreads, S::kBytes, &fit);
+    if (e != cudaSuccess) return e;
+    if (fit < units_all) continue;
+    p.cluster = c;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(units_all * c, 1, 1);
+    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, cache_map, p);
+  }
   e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, cache_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most

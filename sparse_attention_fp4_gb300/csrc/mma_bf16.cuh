@@ -43,7 +43,10 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const p
 // from a branch of one lane, an MMA takes 46 cycles whatever its size, since the operands
 // then go through per-thread registers.  Measured for K = 16 and M x N on one SM: 64x16 24
 // cycles, 64x64 33, 128x64 48, 64x128 and 128x128 63, 128x256 123.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+// (In a cluster the addresses of shared memory have the CTA's rank in their upper bits.)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
 constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // sbo 1,024, version, 128-byte swizzle
 // kind::f16: D f32, A and B bf16; a_m_major: A is stored with M contiguous.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_m_major, bool b_n_major) {
@@ -94,12 +97,29 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const void* map, int32_t x,
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int kLeft>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Distributed shared memory: the address of `addr` in CTA `cta` of the cluster, a store to such
+// an address, and a barrier of all the cluster's threads that orders those stores.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, uint32_t cta) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(cta));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 // Four 8x8 b16 matrices, each stored transposed: lane l gives the address of row l % 8 of
 // matrix l / 8; register i of lane l holds elements (row l / 4, cols 2 (l % 4) + {0, 1}) of
