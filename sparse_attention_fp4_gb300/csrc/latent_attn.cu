@@ -32,7 +32,6 @@
 // depend on m; weights stay below 2^8.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "launchers.cuh"
 #include "mma_bf16.cuh"
@@ -87,6 +86,7 @@ constexpr size_t kWorkBytes =
 
 // ---------------------------------------------------------------- the list of tiles
 // Tokens that row t sees: its plain length, and the end of what it sees (0, 0: nothing).
+template <bool kSelected>
 __device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& len, int& end, int& err) {
   const int seq = a.row_seq[t];
   len = end = 0;
@@ -94,7 +94,7 @@ __device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& len, i
     err = FP4IDX_ERR_BAD_PAGE;
     return;
   }
-  if (a.idx) {
+  if (kSelected) {
     len = end = a.context_lens ? max(0, min(a.k, a.context_lens[t])) : a.k;
     return;
   }
@@ -123,6 +123,7 @@ struct Unit {
   int r0, rows, seq, tiles;
   int min_len;  // every row sees the tokens before it
 };
+template <bool kSelected>
 __device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool report) {
   u.r0 = r0;
   u.rows = 0;
@@ -131,12 +132,12 @@ __device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool
   int most = 0;
   do {
     int len, end, err = 0;
-    row_span(p.a, r0 + u.rows, len, end, err);
+    row_span<kSelected>(p.a, r0 + u.rows, len, end, err);
     if (err && report) record_error(p.a.status, err);
     u.min_len = min(u.min_len, len);
     most = max(most, end);
     u.rows++;
-  } while (u.rows < p.group && r0 + u.rows < p.a.n_rows && p.a.row_seq[r0 + u.rows] == u.seq);
+  } while (!kSelected && u.rows < p.group && r0 + u.rows < p.a.n_rows && p.a.row_seq[r0 + u.rows] == u.seq);
   u.tiles = max(1, (most + kTile - 1) / kTile);  // an empty unit still writes its zeros
 }
 
@@ -146,17 +147,18 @@ struct Seg {
   int hb, t0, t1;
   int64_t left;  // tiles of the CTA from t0 on
 };
+template <bool kSelected>
 __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = false) {
   s.left -= s.t1 - s.t0;
   if (s.left <= 0) return false;
-  if (p.columns) {
+  if (kSelected && p.columns) {
     const int64_t u = (int64_t)s.u.r0 * p.hb + s.hb + gridDim.x;
     if (u >= (int64_t)p.a.n_rows * p.hb) return false;
     s.hb = (int)(u % p.hb);
-    load_unit(p, (int)(u / p.hb), s.u, report);
+    load_unit<kSelected>(p, (int)(u / p.hb), s.u, report);
   } else if (++s.hb == p.hb) {
     s.hb = 0;
-    load_unit(p, s.u.r0 + s.u.rows, s.u, false);
+    load_unit<kSelected>(p, s.u.r0 + s.u.rows, s.u, false);
   }
   s.t0 = 0;
   s.t1 = (int)min((int64_t)s.u.tiles, s.left);
@@ -214,11 +216,12 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, ScanShared& sh, int64_t
   return (warp ? before : 0) + v;
 }
 // `run` carries the first row of the last run of one sequence from chunk to chunk.
+template <bool kSelected>
 __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& run, ScanShared& sh, bool report) {
   const int t = base + (int)threadIdx.x;
   const bool in = t < p.a.n_rows;
   bool starts = in;
-  if (p.group > 1) {
+  if (!kSelected && p.group > 1) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     int first = in && (t == 0 || p.a.row_seq[t] != p.a.row_seq[t - 1]) ? t : -1;
 #pragma unroll
@@ -240,23 +243,24 @@ __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& ru
   }
   if (!starts) return Weight{0, 0};
   Unit u;
-  load_unit(p, t, u, report);
+  load_unit<kSelected>(p, t, u, report);
   return Weight{u.tiles, u.rows};
 }
+template <bool kSelected>
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
-  if (p.cluster) {
+  if (kSelected && p.cluster) {
     const int u = blockIdx.x / p.cluster, j = blockIdx.x % p.cluster;
-    load_unit(p, u / p.hb, s.u, threadIdx.x == 0 && j == 0);
+    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x == 0 && j == 0);
     s.hb = u % p.hb;
     s.t0 = (int)((int64_t)s.u.tiles * j / p.cluster);
     s.t1 = (int)((int64_t)s.u.tiles * (j + 1) / p.cluster);
     s.left = s.t1 - s.t0;
     return s.left > 0;
   }
-  if (p.columns) {
+  if (kSelected && p.columns) {
     const int u = blockIdx.x;
-    load_unit(p, u / p.hb, s.u, threadIdx.x == 0);
+    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x == 0);
     s.hb = u % p.hb;
     s.t0 = 0;
     s.t1 = s.u.tiles;
@@ -268,7 +272,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   int run = -1;
   Weight w{0, 0};
   for (int base = 0; base < n; base += step) {
-    w = unit_weight(p, base, run, sh, report);
+    w = unit_weight<kSelected>(p, base, run, sh, report);
     incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
     all += total;
   }
@@ -295,7 +299,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
         if (cta >= total) return false;
         if (cta >= begin && cta < end) {
           const int k = cta - (int)begin, j = k % per;
-          load_unit(p, threadIdx.x, sh.unit, false);
+          load_unit<kSelected>(p, threadIdx.x, sh.unit, false);
           sh.found_hb = k / per;
           sh.found_t0 = (int)((int64_t)w.tiles * j / per);
           sh.found_left = (int)((int64_t)w.tiles * (j + 1) / per) - sh.found_t0;
@@ -317,7 +321,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   __syncthreads();
   for (int base = 0; base < n; base += step) {
     if (n > step) {
-      w = unit_weight(p, base, run, sh, false);
+      w = unit_weight<kSelected>(p, base, run, sh, false);
       incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
     }
     const int64_t end = carry + incl, begin = end - (int64_t)w.tiles * p.hb;
@@ -343,7 +347,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   __syncthreads();
   s.left = sh.cut[1] - sh.cut[0];
   if (s.left <= 0) return false;
-  load_unit(p, sh.found_row, s.u, false);
+  load_unit<kSelected>(p, sh.found_row, s.u, false);
   s.hb = sh.found_hb;
   s.t0 = sh.found_t0;
   s.t1 = (int)min((int64_t)s.u.tiles, s.t0 + s.left);
@@ -393,7 +397,7 @@ struct Shape {
 };
 // The scan's scratch lies in the query buffer, which is not in use yet.
 
-template <int kWidth, int kN>
+template <int kWidth, int kN, bool kSelected>
 __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ CUtensorMap cache_map,
                                                                                    const __grid_constant__ Params p) {
   using S = Shape<kWidth, kN>;
@@ -441,16 +445,16 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   // being found: three dependent reads lie between the lengths and the first tile.
   {
     const int64_t at = ((int64_t)blockIdx.x * S::kThreads + threadIdx.x) * 128;
-    if (a.idx && at < (int64_t)a.n_rows * a.k * 4) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.idx) + at);
+    if (kSelected && at < (int64_t)a.n_rows * a.k * 4) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.idx) + at);
     if (at < (int64_t)a.num_seqs * a.max_pages * 4) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.page_table) + at);
     if (at < (int64_t)a.n_rows * a.heads * (kWidth * 2)) pipe::prefetch_l2(reinterpret_cast<const uint8_t*>(a.q) + at);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Seg seg;
-  const bool any = first_seg(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
+  const bool any = first_seg<kSelected>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
   Work wk = work_view(a.workspace);
-  if (threadIdx.x == 0 && !p.cluster) {
+  if (threadIdx.x == 0 && !(kSelected && p.cluster)) {
     wk.rec[2 * blockIdx.x] = Record{0, 0, 0, 0};
     wk.rec[2 * blockIdx.x + 1] = Record{0, 0, 0, 0};
   }
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       t += n;
       while (t >= seg.t1) {
         n = t - seg.t1;
-        if (!next_seg(p, seg)) {
+        if (!next_seg<kSelected>(p, seg)) {
           have = false;
           return;
         }
@@ -493,14 +497,14 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       table2 = a.page_table + (int64_t)seg.u.seq * a.max_pages;
       pos2 = t * kTile + tok;
       rows2 = 0;
-      whole2 = !a.idx && (t + 1) * kTile <= seg.u.min_len;
+      whole2 = !kSelected && (t + 1) * kTile <= seg.u.min_len;
       if (pos2 < seg.u.min_len) {
         rows2 = (1u << seg.u.rows) - 1;
-        if (a.idx) pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
-      } else if (!a.idx) {
+        if (kSelected) pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
+      } else if (!kSelected) {
         for (int r = 0; r < seg.u.rows; r++) {
           int len, end, err;
-          row_span(a, seg.u.r0 + r, len, end, err);
+          row_span<kSelected>(a, seg.u.r0 + r, len, end, err);
           rows2 |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos2) << r;
         }
       }
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       last = kcur;
       have1 = have;
       // (a page outside the cache takes the other path: its rows become zero)
-      tma = __all_sync(kFull, whole1 && in);
+      tma = !kSelected && __all_sync(kFull, whole1 && in);
       if (tma) {
         // a whole page: one box of 64 tokens x 64 dims a block, issued by the first warp
         const int row = __shfl_sync(kFull, page1, 0) * kPage;
@@ -567,32 +571,23 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         continue;
       }
       const uint16_t* src[4];
-      bool every = true;
       uint32_t bytes[4];
 #pragma unroll
       for (int g = 0; g < 4; g++) {
         const int of = __shfl_sync(kFull, slot, g * 4 + (lane >> 3));
         src[g] = a.cache + (int64_t)max(of, 0) * kWidth + piece * 8;
         bytes[g] = of >= 0 ? 16 : 0;
-        every = every && of >= 0;
       }
-      const auto copy = [&](int c0, int c1, auto all) {
 #pragma unroll
-        for (int c = c0; c < c1; c++)
+      for (int c = 0; c < kChunks; c++) {
+        if (c == 4) {
+          mma::cp_async_commit();
+          if (!mma::wait_warp(kempty(s, 1), free, ctl)) break;
+        }
 #pragma unroll
-          for (int g = 0; g < 4; g++) {
-            const uint32_t to = dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece);
-            if (decltype(all)::value) mma::cp_async16(to, src[g] + c * 64);
-            else mma::cp_async16(to, src[g] + c * 64, bytes[g]);
-          }
-      };
-      every = __all_sync(kFull, every);
-      if (every) copy(0, 4, std::true_type{});
-      else copy(0, 4, std::false_type{});
-      mma::cp_async_commit();
-      if (!mma::wait_warp(kempty(s, 1), free, ctl)) break;
-      if (every) copy(4, kChunks, std::true_type{});
-      else copy(4, kChunks, std::false_type{});
+        for (int g = 0; g < 4; g++)
+          mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
+      }
       mma::cp_async_commit();
       const uint32_t kdone = kcur;
       kcur = kctr;
@@ -632,7 +627,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
       ictr++;
-    } while (next_seg(p, seg, lane == 0));
+    } while (next_seg<kSelected>(p, seg, lane == 0));
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)
     uint32_t kctr = 0;
@@ -653,8 +648,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
 #pragma unroll
         for (int g = 0; g < 2; g++) {
           int pos = t * kTile + lane + 32 * g;
-          bool some = pos < (a.idx ? seg.u.min_len : seg.u.tiles * kTile) && seg.u.seq >= 0 && seg.u.seq < a.num_seqs;
-          if (some && a.idx) pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
+          bool some = pos < (kSelected ? seg.u.min_len : seg.u.tiles * kTile) && seg.u.seq >= 0 && seg.u.seq < a.num_seqs;
+          if (some && kSelected) pos = a.idx[(int64_t)seg.u.r0 * a.k + pos];
           if (some && pos >= 0 && pos / kPage < a.max_pages) {
             const int32_t page = a.page_table[(int64_t)seg.u.seq * a.max_pages + pos / kPage];
             if (page >= 0 && page < a.num_pages) {
@@ -665,7 +660,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           }
         }
       }
-    } while (on && next_seg(p, seg));
+    } while (on && next_seg<kSelected>(p, seg));
   } else if (any && warp == kScoreWarp) {
     // ------------------------------------------------------------ the first product (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
@@ -714,7 +709,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           phase ^= 1;
         }
       }
-    } while (ok && next_seg(p, seg));
+    } while (ok && next_seg<kSelected>(p, seg));
     // nothing of this CTA's may be under way in the tensor cores when it ends
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
@@ -747,7 +742,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         __syncwarp();
         if (++stage == kStages) stage = 0;
       }
-    } while (ok && next_seg(p, seg));
+    } while (ok && next_seg<kSelected>(p, seg));
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
     mma::wait_warp(done, 0, ctl, false);
@@ -788,7 +783,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         float mul = cs;
         bool zero0 = false, zero1 = false;
         if (!all_seen) {
-          if (seg.u.rows > 1) {
+          if (!kSelected && seg.u.rows > 1) {
             // A token that some rows see and others do not stays in the second product.  If
             // its value is not finite (then no score is), the value row is zeroed below and
             // the columns that see it get a NaN weight: NaN for those, nothing for the others.
@@ -820,7 +815,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           }
 #pragma unroll
           for (int j = 0; j < kJ; j++) {
-            const int r = (col0 + 8 * j) / p.hp;
+            const int r = kSelected ? 0 : (col0 + 8 * j) / p.hp;
             const bool in0 = (see0 >> r) & 1, in1 = (see1 >> r) & 1;
             v[2 * j] = in0 ? make_float2(v[2 * j].x * cs, v[2 * j].y * cs) : make_float2(-INFINITY, -INFINITY);
             v[2 * j + 1] = in1 ? make_float2(v[2 * j + 1].x * cs, v[2 * j + 1].y * cs) : make_float2(-INFINITY, -INFINITY);
@@ -837,7 +832,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           most = fmaxf(most, fmaxf(x[j].x, x[j].y));
         }
         const bool raise = mma::bar_any(1, kSoft, most > kRaise || !ok);
-        if (zero0 || zero1) {
+        if (!kSelected && (zero0 || zero1)) {
           for (int c = quad; c < kValue / 8; c += 4) {
             uint8_t* row = smem + st * S::kStageBytes + (c >> 3) * (kTile * 128);
             if (zero0) *reinterpret_cast<uint4*>(row + mma::sw128(tok, c & 7)) = make_uint4(0, 0, 0, 0);
@@ -934,7 +929,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (threadIdx.x < kN) {
         const int c = threadIdx.x;
         const float total = red[c] + red[kN + c] + red[2 * kN + c] + red[3 * kN + c];
-        if (p.cluster) {
+        if (kSelected && p.cluster) {
           sm_f[c] = total;
         } else if (whole) {
           sm_f[c] = total == 0.f ? 0.f : 1.f / total;
@@ -947,12 +942,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           wk.ml[slot * 2 * kCols + kCols + c] = total;
         }
       }
-      if (!whole && !p.cluster && threadIdx.x == 0)
+      if (!whole && !(kSelected && p.cluster) && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
       ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
-      if (p.cluster) break;  // the one piece: joined below
+      if (kSelected && p.cluster) break;  // the one piece: joined below
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
       if (whole) {
@@ -991,12 +986,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       }
       ptx::tc_fence_before();
       ptx::named_bar_sync(1, kSoft);  // red, sm_m and sm_f are free again
-    } while (next_seg(p, seg));
+    } while (next_seg<kSelected>(p, seg));
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (p.cluster) {
+  if (kSelected && p.cluster) {
     // ---- the cluster's pieces are joined: each CTA for its share of the columns
     // All main loops are over, so shared memory is free: pieces of the CTA's columns at 0,
     // [piece][column][512] fp32, every piece's m and l in the query buffer.
@@ -1189,14 +1184,14 @@ bool encode_cache(CUtensorMap* map, const void* base, int64_t rows, int32_t widt
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kWidth, int kN>
+template <int kWidth, int kN, bool kSelected>
 cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   using S = Shape<kWidth, kN>;
   static_assert(S::kBytes <= 232448, "shared memory of a CTA");
   static_assert(S::kThreads <= kMaxWarps * 32, "");
   static_assert(kN * kValue * 4 <= S::kOffQ, "a cluster's pieces fit the stages");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
-  const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN>);
+  const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN, kSelected>);
   CUtensorMap cache_map;
   if (!encode_cache(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth)) return cudaErrorInvalidValue;
   cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
@@ -1215,8 +1210,8 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   cfg.dynamicSmemBytes = S::kBytes;
   // A cluster a unit, of the largest size of which the device holds that many, if its CTAs get
   // at most three tiles more than an even cut would give them.
-  const int units_all = p.a.n_rows * p.hb, tiles = p.a.idx ? (p.a.k + kTile - 1) / kTile : 0;
-  for (int c = 8; c >= 2 && may_split && p.a.idx; c /= 2) {
+  const int units_all = p.a.n_rows * p.hb, tiles = (p.a.k + kTile - 1) / kTile;
+  for (int c = 8; kSelected && c >= 2 && may_split; c /= 2) {
     if ((int64_t)units_all * c > ctas || (tiles + c - 1) / c > ((int64_t)tiles * units_all + ctas - 1) / ctas + 3) continue;
     int fit = 0;
     e = resident_clusters(kernel, c, S::kThreads, S::kBytes, &fit);
@@ -1229,9 +1224,9 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(units_all * c, 1, 1);
-    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, cache_map, p);
+    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, p);
   }
-  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN>, cache_map, p);
+  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most
   const bool many = units * 8 <= ctas;  // eight pieces a unit or more
@@ -1239,6 +1234,18 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   cfg.blockDim = dim3(many ? 1024 : 256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, many ? combine_kernel<2, 16> : combine_kernel<8, 1>, p, ctas);
+}
+
+template <bool kSelected>
+cudaError_t launch_shape(const Params& p, int32_t width, int cols, int ctas, bool may_split, cudaStream_t stream) {
+  if (width == 576) {
+    if (cols <= 16) return launch<576, 16, kSelected>(p, ctas, may_split, stream);
+    if (cols <= 32) return launch<576, 32, kSelected>(p, ctas, may_split, stream);
+    return launch<576, 64, kSelected>(p, ctas, may_split, stream);
+  }
+  if (cols <= 16) return launch<512, 16, kSelected>(p, ctas, may_split, stream);
+  if (cols <= 32) return launch<512, 32, kSelected>(p, ctas, may_split, stream);
+  return launch<512, 64, kSelected>(p, ctas, may_split, stream);
 }
 
 }  // namespace
@@ -1268,14 +1275,8 @@ cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool selected
   p.columns = selected && units > ctas && (int64_t)rounds * ctas * 20 <= (int64_t)units * 21;
   const bool may_split = !p.columns && (selected ? a.k : a.max_context) > kTile;
   const int cols = p.group * p.hp;
-  if (width == 576) {
-    if (cols <= 16) return launch<576, 16>(p, ctas, may_split, stream);
-    if (cols <= 32) return launch<576, 32>(p, ctas, may_split, stream);
-    return launch<576, 64>(p, ctas, may_split, stream);
-  }
-  if (cols <= 16) return launch<512, 16>(p, ctas, may_split, stream);
-  if (cols <= 32) return launch<512, 32>(p, ctas, may_split, stream);
-  return launch<512, 64>(p, ctas, may_split, stream);
+  return selected ? launch_shape<true>(p, width, cols, ctas, may_split, stream)
+                  : launch_shape<false>(p, width, cols, ctas, may_split, stream);
 }
 
 }  // namespace fp4idx

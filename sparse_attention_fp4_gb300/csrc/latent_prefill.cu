@@ -99,7 +99,17 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
   const auto ofull = [&](int t) { return bar(2 * kRing + 6 + t); };
   const uint32_t done = bar(2 * kRing + 8), tail = bar(2 * kRing + 9);
   const auto issued = [&](int t) { return bar(2 * kRing + 10 + t); };
-  if (threadIdx.x == 0) {
+  // The loading warp sets the barriers up, so that its first loads need not wait for the others.
+  const auto load = [&](int b) {  // block b of the stream, by one thread
+    const int s = b % kRing, j = b / 5, c = b % 5, row = (int)k0 + j * kTokens;
+    const uint32_t dst = sb + kOffRing + s * kBlock;
+    ptx::mbar_arrive_expect_tx(full(s), kBlock);
+    if (c == 2) mma::tma_2d(dst, &r_map, 0, row, full(s));
+    else tma_3d(dst, &kv_map, c < 2 ? c * 64 : (c - 1) * 64, head, row, full(s));
+  };
+  // block b of the stream: key tile j is blocks 5 j .. 5 j + 2, value tile j 5 j + 3, 5 j + 4
+  const int blocks = p.idle_producers ? 0 : 5 * n, early = min(blocks, kRing);
+  if (warp == kLoadWarp && mma::elect_one()) {
     for (int i = 0; i < kRing; i++) {
       ptx::mbar_init(full(i), 1);
       ptx::mbar_init(empty(i), 2);  // both tiles
@@ -115,6 +125,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
     ptx::mbar_init(tail, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
+    ptx::fence_proxy_async_smem();
+    for (int t = 0; t < 2; t++) {
+      if (tiles[t] == 0 || p.idle_producers) continue;
+      ptx::mbar_arrive_expect_tx(qfull(t), 3 * kQBlock);
+      for (int c = 0; c < 3; c++)
+        tma_3d(sb + (3 * t + c) * kQBlock, &q_map, c * 64, head, (int)q0 + i0 + t * kRows, qfull(t));
+      if (t == 0)
+        for (int b = 0; b < min(early, 3); b++) load(b);
+    }
+    for (int b = tiles[0] && !p.idle_producers ? min(early, 3) : 0; b < early; b++) load(b);
   }
   if (warp == kMmaWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), 512);
   ptx::tc_fence_before();
@@ -125,33 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
 
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------ loads
-    // block b of the stream: key tile j is blocks 5 j .. 5 j + 2, value tile j 5 j + 3, 5 j + 4
-    const int blocks = p.idle_producers ? 0 : 5 * n;
     bool ok = true;
-    int b = 0;
-    if (!p.idle_producers) {
-#pragma unroll
-      for (int t = 0; t < 2; t++) {
-        if (tiles[t] > 0 && mma::elect_one()) {
-          ptx::mbar_arrive_expect_tx(qfull(t), 3 * kQBlock);
-#pragma unroll
-          for (int c = 0; c < 3; c++)
-            tma_3d(sb + (3 * t + c) * kQBlock, &q_map, c * 64, head, (int)q0 + i0 + t * kRows, qfull(t));
-        }
-        __syncwarp();
-      }
-    }
+    int b = early;
     for (; b < blocks; b++) {
-      const int s = b % kRing, j = b / 5, c = b % 5;
-      ok = mma::wait_warp(empty(s), ((b / kRing) & 1) ^ 1, ctl);
+      ok = mma::wait_warp(empty(b % kRing), ((b / kRing) & 1) ^ 1, ctl);
       if (!ok) break;
-      if (mma::elect_one()) {
-        ptx::mbar_arrive_expect_tx(full(s), kBlock);
-        const int row = (int)k0 + j * kTokens;
-        const uint32_t dst = sb + kOffRing + s * kBlock;
-        if (c == 2) mma::tma_2d(dst, &r_map, 0, row, full(s));
-        else tma_3d(dst, &kv_map, c < 2 ? c * 64 : (c - 1) * 64, head, row, full(s));
-      }
+      if (mma::elect_one()) load(b);
       __syncwarp();
     }
     // A value tile that ends behind the sequence: its rows there (another sequence's, or
