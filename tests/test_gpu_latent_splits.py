@@ -1,0 +1,113 @@
+"""Row counts around every way the attention work is cut (clusters, CTAs of a unit's own,
+whole rounds, an even cut), and the bounded waits of the attention kernels."""
+import pytest
+import torch
+
+from tests.test_gpu_latent_attn import Batch, i32, selection, workspace
+from tests.test_gpu_latent_prefill import Prompts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("rows", [2, 19, 38, 39, 76, 77, 100, 151, 152, 153, 200, 304, 305, 460])
+@pytest.mark.parametrize("heads,k", [(8, 300), (70, 130)])
+def test_selected_rows(rows, heads, k):
+    from sparse_attention_fp4_gb300 import fp4idx
+    lens = [1 + (37 * i) % 500 for i in range(rows)]
+    b = Batch(rows, lens, 1, heads, 512)
+    idx, want = selection(b, k, 2, lens)
+    status = i32([0])
+    out, lse = b.buffers()
+    fp4idx.latent_attn_topk(b.q, b.cache, b.table, b.row_seq, idx, b.scale, workspace(b), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 0
+    b.check(out, lse, want, rows=range(0, rows, 1 + rows // 60))
+
+
+@pytest.mark.parametrize("seqs,n", [(1, 1), (3, 5), (40, 1), (40, 4), (152, 1), (153, 1), (200, 2), (64, 7)])
+@pytest.mark.parametrize("heads", [8, 24, 64])
+def test_whole_context_rows(seqs, n, heads):
+    from sparse_attention_fp4_gb300 import fp4idx
+    lens = [(i * i * 13) % 900 for i in range(seqs)]
+    lens[0] = 1500
+    b = Batch(seqs, lens, n, heads, 576)
+    L = [max(0, v - (n - 1 - i)) for v in lens for i in range(n)]
+    status = i32([0])
+    out, lse = b.buffers()
+    fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(L), 1500, b.scale, workspace(b), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 0
+    b.check(out, lse, [list(range(v)) for v in L], rows=range(0, b.T, 1 + b.T // 60))
+
+
+def test_rows_of_mixed_sequences():
+    """Runs of one sequence of every length up to more than a pass holds, sequences that come
+    back, and rows of a bad sequence between them."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    b = Batch(3, [200, 300, 70], 12, 8, 512)
+    seqs = [0] * 3 + [1] * 11 + [0] + [2] * 2 + [5] * 2 + [1] + [2] * 9 + [0] * 7
+    L = [(i * 53) % 70 + 1 for i in range(len(seqs))]
+    assert len(seqs) == b.T
+    b.row_seq = i32([s if s < 3 else 0 for s in seqs])
+    status = i32([0])
+    out, lse = b.buffers()
+    fp4idx.latent_attn(b.q, b.cache, b.table, i32(seqs), i32(L), 80, b.scale, workspace(b), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 5
+    b.check(out, lse, [list(range(v)) if s < 3 else [] for v, s in zip(L, seqs)])
+
+
+def test_same_bits_every_time():
+    """Pieces are joined in a fixed order, whatever runs beside them."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    b = Batch(7, [3000, 20, 700], 1, 40, 576)
+    idx, _ = selection(b, 700, 2, b.lens)
+    ws, ws2 = workspace(b), workspace(b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    first = None
+    for _ in range(6):
+        out, lse = b.buffers()
+        out2, lse2 = b.buffers()
+        torch.cuda.synchronize()
+        fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(b.lens), 3000, b.scale, ws, out, lse=lse)
+        fp4idx.latent_attn_topk(b.q, b.cache, b.table, b.row_seq, idx, b.scale, ws2, out2, lse=lse2, stream=side)
+        torch.cuda.synchronize()
+        got = [v.clone() for v in (out, lse, out2, lse2)]
+        first = first or got
+        assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+def test_waits_run_out():
+    """With loads that never come every call ends with a status, and the next calls are right."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    b = Batch(9, [500, 300], 1, 16, 576)
+    many = Batch(10, [400] * 90, 1, 64, 512)
+    p = Prompts(11, [200, 40], [300, 40], 2)
+    idx, want = selection(b, 200, 1, b.lens)
+    midx, mwant = selection(many, 200, 1, many.lens)
+
+    def calls(check):
+        for x, sel, w in ((b, idx, want), (many, midx, mwant)):  # a cluster a row; CTAs of a row's own
+            status = i32([0])
+            out, lse = x.buffers()
+            fp4idx.latent_attn_topk(x.q, x.cache, x.table, x.row_seq, sel, x.scale, workspace(x), out, lse=lse, status=status)
+            assert fp4idx.read_status(status) == (0 if check else 6)
+            if check:
+                x.check(out, lse, w, rows=range(0, x.T, 30))
+        status = i32([0])
+        out, lse = b.buffers()
+        fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(b.lens), 500, b.scale, workspace(b), out, lse=lse, status=status)
+        assert fp4idx.read_status(status) == (0 if check else 6)
+        if check:
+            b.check(out, lse, [list(range(v)) for v in b.lens])
+        status = i32([0])
+        out, lse = p.run(status)
+        assert fp4idx.read_status(status) == (0 if check else 6)
+        if check:
+            p.check(out, lse, every=23)
+
+    calls(True)
+    try:
+        fp4idx.test_pipeline_waits(True, 30_000_000)
+        calls(False)
+    finally:
+        fp4idx.test_pipeline_waits(False, 0)
+    calls(True)
