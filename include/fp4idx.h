@@ -12,6 +12,9 @@
  * tensor and a 4-byte scale tensor.  Read side: paged-MQA logits
  *   logits[t,s] = sum_h w[t,h] * ReLU(q_fp4[t,h] . k_fp4[s]),  s < context_lens[t],
  * then a per-row top-k of compressed-token indices, ascending.
+ * Around the indexer: the step's maps built on the device (fp4idx_plan_step), and the cache
+ * and attention that the selection is for (fp4idx_store_latent, fp4idx_latent_attn_topk,
+ * fp4idx_latent_attn, fp4idx_latent_prefill).
  *
  * Conventions for every entry point
  *   - Pointers are DEVICE pointers (cudaMalloc / torch CUDA memory on the current
@@ -544,12 +547,12 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
                           void* stream);
 
 /*
- * Test support for the logits kernels' bounded waits (failure detection), with no
- * counterpart on the pages.  Every wait of a logits pipeline gives up after
+ * Test support for the bounded waits of the logits and attention kernels (failure
+ * detection), with no counterpart on the pages.  Every wait of such a pipeline gives up after
  * wait_limit_ns (0 restores the default, 2 s): the CTA then records FP4IDX_ERR_TIMEOUT
  * in status_dev, lets the copies it issued land, frees its tensor memory and returns,
  * and the context stays usable.  idle_producers != 0 tells the producer warps of
- * later logits launches to issue nothing, so that every launch ends in that timeout;
+ * later launches to issue nothing, so that every launch ends in that timeout;
  * a test sets it with a short limit, checks the status, and calls
  * fp4idx_test_pipeline_waits(0, 0) to restore normal operation.  Process-wide; host
  * only (takes effect at the next launch).

@@ -2,7 +2,7 @@
 // the caller's stream.
 #include <cmath>
 
-#include "launchers.cuh"
+#include "latent.cuh"
 
 namespace {
 

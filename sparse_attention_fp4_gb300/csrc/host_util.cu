@@ -9,7 +9,7 @@
 #include <tuple>
 #include <utility>
 
-#include "launchers.cuh"
+#include "latent.cuh"
 
 namespace fp4idx {
 

@@ -33,7 +33,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "launchers.cuh"
+#include "latent.cuh"
 #include "mma_bf16.cuh"
 #include "pipeline.cuh"
 

@@ -11,7 +11,7 @@
 // what another writes: the table entries read are those of pages that exist already.
 #include <algorithm>
 
-#include "launchers.cuh"
+#include "latent.cuh"
 
 namespace fp4idx {
 namespace {

@@ -3,12 +3,13 @@
 // Bound by HBM (2,304 bytes a row of 576).  A warp walks rows `step` apart; rows and their
 // cos/sin come by bulk copies into a ring of four a warp, 82 KB in flight an SM: 65,536 rows
 // take 51 us with plain loads, 39 us with loads a row ahead in registers (16 warps an SM) and
-// 36 us with the ring (4.2 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds dims 8l..8l+7 and 256 + 8l.. of the 512, and at width 576
-// lanes 0..7 hold the last 64; the two halves of a RoPE pair (i, i + 32) are then four lanes
-// apart.
+// 32 us with the ring (4.8 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds
+// dims 8l..8l+7 and 256 + 8l.. of the 512; the rotated dims are taken from the ring again, a pair
+// (i, i + 32) a lane (pairs exchanged by shuffles, by eight lanes: 347 warp instructions a row and
+// 36 us).
 #include <algorithm>
 
-#include "launchers.cuh"
+#include "latent.cuh"
 #include "mma_bf16.cuh"
 
 namespace fp4idx {
@@ -32,17 +33,8 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ uint4 pack(const float* v) {
   return make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
-// The eight lanes of a rotated run of 64 dims: lane r of the run holds dims 8r..8r+7, its
-// pair's other half four lanes away.  Every lane of the warp takes part in the shuffles.
-__device__ __forceinline__ void rope(float* v, int r, const uint4& uc, const uint4& us, bool rotate) {
-  float c[8], s[8];
-  unpack(uc, c);
-  unpack(us, s);
-#pragma unroll
-  for (int i = 0; i < 8; i++) {
-    const float other = __shfl_xor_sync(~0u, v[i], 4);
-    if (rotate) v[i] = r < 4 ? v[i] * c[i] - other * s[i] : v[i] * c[i] + other * s[i];
-  }
+__device__ __forceinline__ float bf16_at(const uint8_t* p) {
+  return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
 
 template <int kWidth>
@@ -62,7 +54,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
   using R = Ring<kWidth>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool rotates = kWidth == 576 ? lane < 8 : lane >= 24;
+  constexpr int kRot = kWidth - kRope;  // the first rotated dim
   uint8_t* ring = smem + warp * kRing * R::kSlot;
   const uint32_t bars = ptx::smem_addr(smem) + R::kOffBar + warp * kRing * 8;
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + R::kOffAbort);
@@ -77,6 +69,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
   float w0[8], w1[8];
   unpack(*reinterpret_cast<const uint4*>(norm_w + lane * 8), w0);
   unpack(*reinterpret_cast<const uint4*>(norm_w + 256 + lane * 8), w1);
+  // the weights of the lane's rotated pair (width 512, where those dims are normalised)
+  float wp = 0.f, wq = 0.f;
+  if (kWidth == 512) {
+    wp = bf16_at(reinterpret_cast<const uint8_t*>(norm_w + kRot + lane));
+    wq = bf16_at(reinterpret_cast<const uint8_t*>(norm_w + kRot + 32 + lane));
+  }
   const int64_t step = (int64_t)gridDim.x * kWarps;
   uint32_t phases = 0;  // a bit a ring slot
   // 32 of the warp's rows at a time: lane i has the slot and position of the i-th
@@ -119,12 +117,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
       if (!mma::wait_warp(bars + s * 8, phases >> s & 1, ctl, false)) return;
       phases ^= 1u << s;
       const uint8_t* x = ring + s * R::kSlot;
-      float a[8], b[8], t[8];
+      float a[8], b[8];
       unpack(*reinterpret_cast<const uint4*>(x + lane * 16), a);
       unpack(*reinterpret_cast<const uint4*>(x + 512 + lane * 16), b);
-      if (kWidth == 576) unpack(*reinterpret_cast<const uint4*>(x + 1024 + (lane & 7) * 16), t);
-      const uint4 c = *reinterpret_cast<const uint4*>(x + R::kRow + (lane & 3) * 16);
-      const uint4 sn = *reinterpret_cast<const uint4*>(x + R::kRow + 64 + (lane & 3) * 16);
+      float p = bf16_at(x + (kRot + lane) * 2), q = bf16_at(x + (kRot + 32 + lane) * 2);
+      const float c = bf16_at(x + R::kRow + lane * 2), sn = bf16_at(x + R::kRow + 64 + lane * 2);
       __syncwarp();
       if (ahead) ask();  // into the place just read
       float ss = 0.f;
@@ -138,11 +135,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
         a[e] = a[e] * r * w0[e];
         b[e] = b[e] * r * w1[e];
       }
+      if (kWidth == 512) {
+        p = p * r * wp;
+        q = q * r * wq;
+      }
+      const uint32_t rotated = pack2(p * c - q * sn, q * c + p * sn);
       uint16_t* y = cache + (int64_t)__shfl_sync(~0u, slot, i) * kWidth;
-      rope(kWidth == 576 ? t : b, lane & 7, c, sn, rotates);
-      if (kWidth == 576 && rotates) *reinterpret_cast<uint4*>(y + 512 + lane * 8) = pack(t);
       *reinterpret_cast<uint4*>(y + lane * 8) = pack(a);
-      *reinterpret_cast<uint4*>(y + 256 + lane * 8) = pack(b);
+      if (kWidth == 576 || lane < 24) *reinterpret_cast<uint4*>(y + 256 + lane * 8) = pack(b);
+      y[kRot + lane] = (uint16_t)rotated;
+      y[kRot + 32 + lane] = (uint16_t)(rotated >> 16);
     }
   }
 }
