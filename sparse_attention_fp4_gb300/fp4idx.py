@@ -422,30 +422,28 @@ PREFILL_KEY = 192
 PREFILL_VALUE = 128
 
 
-class _Args:
-    """Argument checks of one call: every tensor on the current device, contiguous, of the
-    right type and at least the size that the call reads or writes; gives its address."""
+def _here(stream):
+    """The current device, and the stream to launch on."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
-    __slots__ = ("device", "stream")
 
-    def __init__(self, stream):
-        self.device = torch.cuda.current_device()
-        self.stream = torch._C._cuda_getCurrentRawStream(self.device) if stream is None else stream.cuda_stream
-
-    def __call__(self, t, name, dtypes, numel):
-        if (isinstance(t, torch.Tensor) and t.get_device() == self.device and t.dtype in dtypes and t.is_contiguous()
-                and (numel == 0 or t.numel() >= numel)):
+def _addr(t, name, dtypes, numel, dev):
+    """The address of a tensor that is on device `dev`, contiguous, of one of the types and of
+    at least `numel` elements.  (A plain function: a decode step's calls are short, and their
+    argument checks are most of the host's time.)"""
+    try:
+        if t.dtype in dtypes and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
             return t.data_ptr()
-        if not isinstance(t, torch.Tensor) or t.get_device() != self.device:
-            raise ValueError("%s must be a CUDA tensor on the current device" % name)
-        if t.dtype not in dtypes:
-            raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
-        raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
-
-    def optional(self, t, name, dtypes, numel):
-        return None if t is None else self(t, name, dtypes, numel)
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the current device" % name)
+    if t.dtype not in dtypes:
+        raise ValueError("%s has dtype %s, expected one of %s" % (name, t.dtype, dtypes))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    raise ValueError("%s has %d elements, needs %d" % (name, t.numel(), numel))
 
 
 def alloc_latent_cache(num_pages, width=576, device="cuda"):
@@ -457,34 +455,38 @@ def plan_step(cached_lens, new_lens, ratio, free_pages, page_table, q_positions,
               store_positions, store_slots, cu_rows, cu_context, counts, free_head=None, status=None, stream=None):
     """The maps of a step from its request lengths (fp4idx_plan_step): page_table is extended
     in place, the other outputs are written; their lengths are the call's capacities."""
-    arg = _Args(stream)
+    dev, on = _here(stream)
     B, rows, stores = cached_lens.numel(), q_positions.numel(), store_positions.numel()
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError("page_table must be [n_seqs, max_pages] with n_seqs = %d" % B)
     rc = _lib.fp4idx_plan_step(
-        arg(cached_lens, "cached_lens", _I32, B), arg(new_lens, "new_lens", _I32, B), B, ratio,
-        arg(free_pages, "free_pages", _I32, 0), free_pages.numel(), arg.optional(free_head, "free_head", _I32, 1),
-        arg(page_table, "page_table", _I32, 0), page_table.shape[1], arg(q_positions, "q_positions", _I32, 0),
-        arg(row_seq, "row_seq", _I32, rows), arg(context_lens, "context_lens", _I32, rows), rows,
-        arg(store_positions, "store_positions", _I32, 0), arg(store_slots, "store_slots", _I32, stores), stores,
-        arg(cu_rows, "cu_rows", _I32, B + 1), arg(cu_context, "cu_context", _I32, B + 1),
-        arg(counts, "counts", _I32, 4), arg.optional(status, "status", _I32, 1), arg.stream)
+        _addr(cached_lens, "cached_lens", _I32, B, dev), _addr(new_lens, "new_lens", _I32, B, dev), B, ratio,
+        _addr(free_pages, "free_pages", _I32, 0, dev), free_pages.numel(),
+        None if free_head is None else _addr(free_head, "free_head", _I32, 1, dev),
+        _addr(page_table, "page_table", _I32, 0, dev), page_table.shape[1],
+        _addr(q_positions, "q_positions", _I32, 0, dev), _addr(row_seq, "row_seq", _I32, rows, dev),
+        _addr(context_lens, "context_lens", _I32, rows, dev), rows,
+        _addr(store_positions, "store_positions", _I32, 0, dev),
+        _addr(store_slots, "store_slots", _I32, stores, dev), stores, _addr(cu_rows, "cu_rows", _I32, B + 1, dev),
+        _addr(cu_context, "cu_context", _I32, B + 1, dev), _addr(counts, "counts", _I32, 4, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_plan_step", rc)
 
 
 def store_latent(kv, positions, slots, norm_w, eps, cos_sin, cache, status=None, stream=None):
     """RMSNorm (dims 0..511), RoPE (last 64 dims) and the scatter of latent rows [n, width]
     into the paged cache [num_pages, 64, width]."""
-    arg = _Args(stream)
+    dev, on = _here(stream)
     if kv.dim() != 2 or cache.dim() != 3 or cache.shape[1] != PAGE_TOKENS or cache.shape[2] != kv.shape[1]:
         raise ValueError("kv must be [n_rows, width] and cache [num_pages, 64, width]")
     if cos_sin.dim() != 2 or cos_sin.shape[1] != 64:
         raise ValueError("cos_sin must be [max_pos, 64]")
     n, width = kv.shape
     rc = _lib.fp4idx_store_latent(
-        arg(kv, "kv", _BF16, 0), n, width, arg(positions, "positions", _I32, n), arg(slots, "slots", _I32, n),
-        arg(norm_w, "norm_w", _BF16, LATENT_VALUE), eps, arg(cos_sin, "cos_sin", _BF16, 0), cos_sin.shape[0],
-        arg(cache, "cache", _BF16, 0), cache.shape[0], arg.optional(status, "status", _I32, 1), arg.stream)
+        _addr(kv, "kv", _BF16, 0, dev), n, width, _addr(positions, "positions", _I32, n, dev),
+        _addr(slots, "slots", _I32, n, dev), _addr(norm_w, "norm_w", _BF16, LATENT_VALUE, dev), eps,
+        _addr(cos_sin, "cos_sin", _BF16, 0, dev), cos_sin.shape[0], _addr(cache, "cache", _BF16, 0, dev),
+        cache.shape[0], None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_store_latent", rc)
 
 
@@ -504,17 +506,19 @@ def latent_attn_topk(q, cache, page_table, row_seq, topk_idx, scale, workspace, 
                      status=None, stream=None):
     """Absorbed latent attention of q [T, H, width] over the tokens that topk_idx [T, k] lists:
     out [T, H, 512] bf16, lse [T, H] fp32 (workspace: latent_attn_workspace_bytes)."""
-    arg = _Args(stream)
+    dev, on = _here(stream)
     T, H, width = _latent_shapes(q, cache, page_table)
     if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
         raise ValueError("topk_idx must be [n_rows, k]")
     rc = _lib.fp4idx_latent_attn_topk(
-        arg(q, "q", _BF16, 0), T, H, width, arg(cache, "cache", _BF16, 0), cache.shape[0],
-        arg(page_table, "page_table", _I32, 0), page_table.shape[0], page_table.shape[1],
-        arg(row_seq, "row_seq", _I32, T), arg(topk_idx, "topk_idx", _I32, 0), topk_idx.shape[1],
-        arg.optional(context_lens, "context_lens", _I32, T), scale, arg(workspace, "workspace", _U8, 0),
-        workspace.numel(), arg(out, "out", _BF16, T * H * LATENT_VALUE), arg.optional(lse, "lse", _F32, T * H),
-        arg.optional(status, "status", _I32, 1), arg.stream)
+        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), cache.shape[0],
+        _addr(page_table, "page_table", _I32, 0, dev), page_table.shape[0], page_table.shape[1],
+        _addr(row_seq, "row_seq", _I32, T, dev), _addr(topk_idx, "topk_idx", _I32, 0, dev), topk_idx.shape[1],
+        None if context_lens is None else _addr(context_lens, "context_lens", _I32, T, dev), scale,
+        _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(),
+        _addr(out, "out", _BF16, T * H * LATENT_VALUE, dev),
+        None if lse is None else _addr(lse, "lse", _F32, T * H, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_latent_attn_topk", rc)
 
 
@@ -522,7 +526,7 @@ def latent_attn(q, cache, page_table, row_seq, context_lens, max_context, scale,
                 tree_mask=None, status=None, stream=None):
     """Absorbed latent attention of q [T, H, width] over each row's whole context and, with
     tree_mask [T, words] int32, the drafted tokens behind it whose bits are set."""
-    arg = _Args(stream)
+    dev, on = _here(stream)
     T, H, width = _latent_shapes(q, cache, page_table)
     words = 0
     if tree_mask is not None:
@@ -530,19 +534,21 @@ def latent_attn(q, cache, page_table, row_seq, context_lens, max_context, scale,
             raise ValueError("tree_mask must be [n_rows, words]")
         words = tree_mask.shape[1]
     rc = _lib.fp4idx_latent_attn(
-        arg(q, "q", _BF16, 0), T, H, width, arg(cache, "cache", _BF16, 0), cache.shape[0],
-        arg(page_table, "page_table", _I32, 0), page_table.shape[0], page_table.shape[1],
-        arg(row_seq, "row_seq", _I32, T), arg(context_lens, "context_lens", _I32, T), int(max_context),
-        arg.optional(tree_mask, "tree_mask", _I32, 0), words, scale, arg(workspace, "workspace", _U8, 0),
-        workspace.numel(), arg(out, "out", _BF16, T * H * LATENT_VALUE), arg.optional(lse, "lse", _F32, T * H),
-        arg.optional(status, "status", _I32, 1), arg.stream)
+        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), cache.shape[0],
+        _addr(page_table, "page_table", _I32, 0, dev), page_table.shape[0], page_table.shape[1],
+        _addr(row_seq, "row_seq", _I32, T, dev), _addr(context_lens, "context_lens", _I32, T, dev), int(max_context),
+        None if tree_mask is None else _addr(tree_mask, "tree_mask", _I32, 0, dev), words, scale,
+        _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(),
+        _addr(out, "out", _BF16, T * H * LATENT_VALUE, dev),
+        None if lse is None else _addr(lse, "lse", _F32, T * H, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_latent_attn", rc)
 
 
 def latent_prefill(q, kv, k_rope, cu_q, cu_kv, max_q, max_kv, scale, out, lse=None, status=None, stream=None):
     """Expanded causal latent attention over packed prompts: q [n_q, H, 192], kv [n_kv, H, 256]
     (128 key dims, 128 value dims), k_rope [n_kv, 64]; out [n_q, H, 128] bf16, lse [n_q, H]."""
-    arg = _Args(stream)
+    dev, on = _here(stream)
     if q.dim() != 3 or q.shape[2] != PREFILL_KEY:
         raise ValueError("q must be [n_q, heads, 192]")
     n_q, H, _ = q.shape
@@ -552,10 +558,12 @@ def latent_prefill(q, kv, k_rope, cu_q, cu_kv, max_q, max_kv, scale, out, lse=No
     if B < 0:
         raise ValueError("cu_q must be [n_seqs + 1]")
     rc = _lib.fp4idx_latent_prefill(
-        arg(q, "q", _BF16, 0), n_q, H, arg(kv, "kv", _BF16, 0), n_kv, arg(k_rope, "k_rope", _BF16, n_kv * 64),
-        arg(cu_q, "cu_q", _I32, B + 1), arg(cu_kv, "cu_kv", _I32, B + 1), B, int(max_q), int(max_kv), scale,
-        arg(out, "out", _BF16, n_q * H * PREFILL_VALUE), arg.optional(lse, "lse", _F32, n_q * H),
-        arg.optional(status, "status", _I32, 1), arg.stream)
+        _addr(q, "q", _BF16, 0, dev), n_q, H, _addr(kv, "kv", _BF16, 0, dev), n_kv,
+        _addr(k_rope, "k_rope", _BF16, n_kv * 64, dev), _addr(cu_q, "cu_q", _I32, B + 1, dev),
+        _addr(cu_kv, "cu_kv", _I32, B + 1, dev), B, int(max_q), int(max_kv), scale,
+        _addr(out, "out", _BF16, n_q * H * PREFILL_VALUE, dev),
+        None if lse is None else _addr(lse, "lse", _F32, n_q * H, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_latent_prefill", rc)
 
 
