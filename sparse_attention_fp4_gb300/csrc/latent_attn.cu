@@ -57,6 +57,7 @@ constexpr float kNoMax = -3.0e38f;
 struct Params {
   LatentArgs a;
   int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
+  int32_t q_boxes;            // a unit's columns are adjacent rows of q: copied as boxes
   int32_t columns;            // selected rows: CTA c takes units c, c + grid, ... whole
   int32_t cluster;            // CTAs of a cluster that share one unit; 0: the list is cut
   uint64_t wait_limit_ns;
@@ -250,7 +251,7 @@ template <bool kSelected>
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
   if (kSelected && p.cluster) {
-    const int u = blockIdx.x / p.cluster, j = blockIdx.x % p.cluster;
+    const int u = blockIdx.x >> (__ffs(p.cluster) - 1), j = blockIdx.x & (p.cluster - 1);
     load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x == 0 && j == 0);
     s.hb = u % p.hb;
     s.t0 = (int)((int64_t)s.u.tiles * j / p.cluster);
@@ -399,6 +400,7 @@ struct Shape {
 
 template <int kWidth, int kN, bool kSelected>
 __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ CUtensorMap cache_map,
+                                                                                   const __grid_constant__ CUtensorMap q_map,
                                                                                    const __grid_constant__ Params p) {
   using S = Shape<kWidth, kN>;
   constexpr int kStages = S::kStages, kChunks = S::kChunks, kSoft = S::kSoftWarps * 32;
@@ -614,6 +616,19 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     uint32_t ictr = 0;
     do {
       if (!mma::wait_warp(qempty, (ictr & 1) ^ 1, ctl)) break;
+      ictr++;
+      if (p.q_boxes) {
+        // (columns behind the unit's get other rows' queries, or zeros behind the last row: what
+        // comes of them is not stored)
+        if (mma::elect_one()) {
+          ptx::mbar_arrive_expect_tx(qfull, kChunks * S::kQChunk);
+          const int row = seg.u.r0 * a.heads + seg.hb * p.hs;
+#pragma unroll
+          for (int c = 0; c < kChunks; c++) mma::tma_2d(sb + S::kOffQ + c * S::kQChunk, &q_map, c * 64, row, qfull);
+        }
+        __syncwarp();
+        continue;
+      }
       const int r0 = lane >> 3, pc = lane & 7;
       for (int col = r0; col < kN; col += 4) {
         const int r = col / p.hp, h = col % p.hp, head = seg.hb * p.hs + h;
@@ -626,8 +641,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
-      ictr++;
     } while (next_seg<kSelected>(p, seg, lane == 0));
+    if (p.q_boxes && ictr > 0) mma::wait_warp(qfull, (ictr - 1) & 1, ctl, false);  // lands before the CTA ends
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)
     uint32_t kctr = 0;
@@ -995,37 +1010,43 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     // ---- the cluster's pieces are joined: each CTA for its share of the columns
     // All main loops are over, so shared memory is free: pieces of the CTA's columns at 0,
     // [piece][column][512] fp32, every piece's m and l in the query buffer.
-    const int ctas = p.cluster, mine = blockIdx.x % ctas, share = kN / ctas;
+    const int ctas = p.cluster, mine = blockIdx.x & (ctas - 1);  // two, four or eight
+    const int share = kN / ctas, shift = __ffs(share) - 1;
     float* gather = reinterpret_cast<float*>(smem + S::kOffQ);  // [piece][2][kN]
     float* sm_m = reinterpret_cast<float*>(smem + S::kOffM);
     float* sm_l = reinterpret_cast<float*>(smem + S::kOffF);
     mma::cluster_sync();
     for (int i = threadIdx.x; i < ctas * kN; i += S::kThreads) {
-      const int c = i % kN, to = i / kN;
+      const int c = i & (kN - 1), to = i / kN;
       mma::st_cluster(mma::map_shared(ptx::smem_addr(gather + (mine * 2) * kN + c), to), any ? sm_m[c] : kNoMax);
       mma::st_cluster(mma::map_shared(ptx::smem_addr(gather + (mine * 2 + 1) * kN + c), to), any ? sm_l[c] : 0.f);
     }
-    if (any && warp < S::kSoftWarps) {
+    // Every warp sends 32 dims of a column at a time, 128 adjacent bytes.  (Sixteen bytes a thread,
+    // the columns of a dim together, take twice as long.)
+    if (any) {
       const int qw = warp & 3;
-      const uint32_t lanes = (uint32_t)(qw * 32) << 16;
+      const uint32_t lanes = (uint32_t)(qw * 32) << 16, at = sb + (mine * share * kValue + qw * 32 + lane) * 4;
+      float* local = reinterpret_cast<float*>(smem) + mine * share * kValue + qw * 32 + lane;
 #pragma unroll 1
-      for (int c = (warp >> 2) * kMyCols; c < ((warp >> 2) + 1) * kMyCols; c += 8) {
-#pragma unroll
+      for (int c = (warp >> 2) * 8; c < kN; c += S::kThreads / 128 * 8) {
+#pragma unroll 1
         for (int b = 0; b < 4; b++) {
           float o[8];
           mma::ld_32x8(tmem + b * kN + c + lanes, o);
 #pragma unroll
           for (int e = 0; e < 8; e++) {
-            const int to = (c + e) / share, col = (c + e) % share;
-            mma::st_cluster(mma::map_shared(sb + ((mine * share + col) * kValue + b * 128 + qw * 32 + lane) * 4, to), o[e]);
+            const int to = (c + e) >> shift, col = (c + e) & (share - 1);
+            const int off = col * kValue + b * 128;
+            if (to == mine) local[off] = o[e];
+            else mma::st_cluster(mma::map_shared(at + off * 4, to), o[e]);
           }
         }
       }
     }
     mma::cluster_sync();
     for (int col = warp; col < share; col += S::kThreads / 32) {
-      const int c = mine * share + col, h = c % p.hp, head = seg.hb * p.hs + h;
-      if (c >= p.hp || h >= p.hs || head >= a.heads) continue;  // one row a unit
+      const int c = mine * share + col, head = seg.hb * p.hs + c;  // one row a unit
+      if (c >= p.hs || head >= a.heads) continue;
       float top = kNoMax, total = 0.f, o[16] = {};
       for (int i = 0; i < ctas; i++) top = fmaxf(top, gather[(i * 2) * kN + c]);
       for (int i = 0; i < ctas; i++) {
@@ -1172,13 +1193,13 @@ __global__ void __launch_bounds__(kBlockCols * kGroups * 32) combine_kernel(cons
   if (lane == 0 && a.lse) a.lse[row] = total == 0.f ? -INFINITY : (top + log2f(total)) * 0.6931471805599453f;
 }
 
-// [rows, width] bf16, in boxes of 64 rows x 64 dims, 128-byte swizzle.
-bool encode_cache(CUtensorMap* map, const void* base, int64_t rows, int32_t width) {
+// [rows, width] bf16, in boxes of box_rows rows x 64 dims, 128-byte swizzle.
+bool encode_rows_of(CUtensorMap* map, const void* base, int64_t rows, int32_t width, int box_rows) {
   EncodeTiledFn fn = encode_tiled_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)width * 2};
-  cuuint32_t box[2] = {64, kTile}, es[2] = {1, 1};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -1192,8 +1213,11 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   static_assert(kN * kValue * 4 <= S::kOffQ, "a cluster's pieces fit the stages");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN, kSelected>);
-  CUtensorMap cache_map;
-  if (!encode_cache(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth)) return cudaErrorInvalidValue;
+  CUtensorMap cache_map, q_map;
+  if (!encode_rows_of(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth, kPage) ||
+      !encode_rows_of(&q_map, p.a.q, (int64_t)p.a.n_rows * p.a.heads, kWidth, kN))
+    return cudaErrorInvalidValue;
+  p.q_boxes = p.group == 1 || p.hp == p.a.heads;
   cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
   if (e != cudaSuccess) return e;
   // Both launches may begin while the one before them ends: each waits for it before its
@@ -1224,9 +1248,9 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
     cfg.gridDim = dim3(units_all * c, 1, 1);
-    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, p);
+    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   }
-  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, p);
+  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most
   const bool many = units * 8 <= ctas;  // eight pieces a unit or more
