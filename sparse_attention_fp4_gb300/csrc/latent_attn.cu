@@ -86,60 +86,56 @@ constexpr size_t kWorkBytes =
     2 * kMaxCtas * (sizeof(Record) + 2 * kCols * sizeof(float) + (size_t)kCols * kValue * sizeof(float));
 
 // ---------------------------------------------------------------- the list of tiles
-// Tokens that row t sees: its plain length, and the end of what it sees (0, 0: nothing).
+// Row t's sequence and the tokens that it sees: its plain length, and the end of what it sees
+// (0, 0: nothing).  All loads are in flight together.
 template <bool kSelected>
-__device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& len, int& end, int& err) {
-  const int seq = a.row_seq[t];
+__device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& seq, int& len, int& end, int& err) {
+  seq = a.row_seq[t];
+  const int n = kSelected && !a.context_lens ? a.k : a.context_lens[t];
+  int extra = 0;
+  if (!kSelected) {
+#pragma unroll
+    for (int w = 0; w < FP4IDX_LATENT_MAX_TREE_WORDS; w++) {
+      const uint32_t m = w < a.words ? a.tree[(int64_t)t * a.words + w] : 0;
+      if (m) extra = 32 * w + 32 - __clz(m);
+    }
+  }
   len = end = 0;
   if (seq < 0 || seq >= a.num_seqs) {
     err = FP4IDX_ERR_BAD_PAGE;
-    return;
-  }
-  if (kSelected) {
-    len = end = a.context_lens ? max(0, min(a.k, a.context_lens[t])) : a.k;
-    return;
-  }
-  const int n = a.context_lens[t];
-  int extra = 0;
-  for (int w = 0; w < a.words; w++) {
-    const uint32_t m = a.tree[(int64_t)t * a.words + w];
-    if (m) extra = 32 * w + 32 - __clz(m);
-  }
-  if (n < 0 || (int64_t)n + extra > a.max_context) {
+  } else if (kSelected) {
+    len = end = max(0, min(a.k, n));
+  } else if (n < 0 || (int64_t)n + extra > a.max_context) {
     err = FP4IDX_ERR_BAD_LENGTH;
-    return;
+  } else {
+    len = n;
+    end = n + extra;
   }
-  len = n;
-  end = n + extra;
 }
-__device__ __forceinline__ bool row_sees(const LatentArgs& a, int t, int len, int end, int pos) {
-  if (pos < len) return true;
-  if (pos >= end) return false;
-  const int j = pos - len;
-  return (a.tree[(int64_t)t * a.words + (j >> 5)] >> (j & 31)) & 1;
-}
+__device__ __forceinline__ int tiles_of(int end) { return max(1, (end + kTile - 1) / kTile); }  // an empty unit still writes its zeros
 
 // The unit that starts at row r0: adjacent rows of one sequence, up to p.group.
 struct Unit {
   int r0, rows, seq, tiles;
-  int min_len;  // every row sees the tokens before it
+  int min_len;   // every row sees the tokens before it
+  int len, end;  // of row r0 + lane
 };
+// By a warp, a row a lane (one after the other, eight rows cost eight times the latency of a load).
 template <bool kSelected>
 __device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool report) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = lane < (kSelected ? 1 : p.group) && r0 + lane < p.a.n_rows;
+  int seq = 0, len = 0, end = 0, err = 0;
+  if (mine) row_span<kSelected>(p.a, r0 + lane, seq, len, end, err);
   u.r0 = r0;
-  u.rows = 0;
-  u.seq = p.a.row_seq[r0];
-  u.min_len = INT32_MAX;
-  int most = 0;
-  do {
-    int len, end, err = 0;
-    row_span<kSelected>(p.a, r0 + u.rows, len, end, err);
-    if (err && report) record_error(p.a.status, err);
-    u.min_len = min(u.min_len, len);
-    most = max(most, end);
-    u.rows++;
-  } while (!kSelected && u.rows < p.group && r0 + u.rows < p.a.n_rows && p.a.row_seq[r0 + u.rows] == u.seq);
-  u.tiles = max(1, (most + kTile - 1) / kTile);  // an empty unit still writes its zeros
+  u.seq = __shfl_sync(kFull, seq, 0);
+  u.rows = kSelected ? 1 : __ffs(~__ballot_sync(kFull, mine && seq == u.seq)) - 1;
+  const bool in = lane < u.rows;
+  if (err && in && report) record_error(p.a.status, err);
+  u.len = len;
+  u.end = end;
+  u.min_len = __reduce_min_sync(kFull, in ? len : INT32_MAX);
+  u.tiles = tiles_of(__reduce_max_sync(kFull, in ? end : 0));
 }
 
 // A run of tiles [t0, t1) of a unit's column block.
@@ -188,8 +184,7 @@ struct ScanShared {
   int64_t sums[kMaxWarps];
   int32_t starts[kMaxWarps];
   int32_t enough[kMaxWarps];
-  int32_t tiles[kMaxWarps * 32];
-  Unit unit;
+  int32_t tiles[kMaxWarps * 32], seqs[kMaxWarps * 32], ends[kMaxWarps * 32];
   int32_t found_row, found_hb, found_t0, found_left;
   int64_t cut[2];
 };
@@ -221,38 +216,56 @@ template <bool kSelected>
 __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& run, ScanShared& sh, bool report) {
   const int t = base + (int)threadIdx.x;
   const bool in = t < p.a.n_rows;
-  bool starts = in;
-  if (!kSelected && p.group > 1) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int first = in && (t == 0 || p.a.row_seq[t] != p.a.row_seq[t - 1]) ? t : -1;
+  const bool grouped = !kSelected && p.group > 1;
+  int seq = 0, len, end = 0, err = 0;
+  if (in) row_span<kSelected>(p.a, t, seq, len, end, err);
+  if (err && report) record_error(p.a.status, err);
+  if (!grouped) return in ? Weight{tiles_of(end), 1} : Weight{0, 0};
+  const int before = in && t > 0 ? p.a.row_seq[t - 1] : 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int first = in && (t == 0 || seq != before) ? t : -1;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int u = __shfl_up_sync(kFull, first, d);
-      if (lane >= d) first = max(first, u);
-    }
-    if (lane == 31) sh.starts[warp] = first;
-    __syncthreads();
-    int last = run;
-    for (int w = 0; w < warps; w++) {
-      if (w < warp) first = max(first, sh.starts[w]);
-      last = max(last, sh.starts[w]);
-    }
-    first = max(first, run);
-    __syncthreads();
-    run = last;
-    starts = in && (t - first) % p.group == 0;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int u = __shfl_up_sync(kFull, first, d);
+    if (lane >= d) first = max(first, u);
   }
-  if (!starts) return Weight{0, 0};
-  Unit u;
-  load_unit<kSelected>(p, t, u, report);
-  return Weight{u.tiles, u.rows};
+  if (lane == 31) sh.starts[warp] = first;
+  sh.seqs[threadIdx.x] = seq;
+  sh.ends[threadIdx.x] = end;
+  __syncthreads();
+  int last = run;
+  for (int w = 0; w < warps; w++) {
+    if (w < warp) first = max(first, sh.starts[w]);
+    last = max(last, sh.starts[w]);
+  }
+  first = max(first, run);
+  Weight got{0, 0};
+  if (in && (t - first) % p.group == 0) {
+    int rows = 1;
+    for (; rows < p.group && t + rows < p.a.n_rows; rows++) {
+      int seq1, len1, end1, err1;
+      const int at = (int)threadIdx.x + rows;
+      if (at < (int)blockDim.x) {
+        seq1 = sh.seqs[at];
+        end1 = sh.ends[at];
+      } else {  // of the next chunk
+        row_span<kSelected>(p.a, t + rows, seq1, len1, end1, err1);
+      }
+      if (seq1 != seq) break;
+      end = max(end, end1);
+    }
+    got = Weight{tiles_of(end), rows};
+  }
+  __syncthreads();
+  run = last;
+  return got;
 }
 template <bool kSelected>
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
   const int n = p.a.n_rows, step = blockDim.x;
   if (kSelected && p.cluster) {
     const int u = blockIdx.x >> (__ffs(p.cluster) - 1), j = blockIdx.x & (p.cluster - 1);
-    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x == 0 && j == 0);
+    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x < 32 && j == 0);
     s.hb = u % p.hb;
     s.t0 = (int)((int64_t)s.u.tiles * j / p.cluster);
     s.t1 = (int)((int64_t)s.u.tiles * (j + 1) / p.cluster);
@@ -261,7 +274,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   }
   if (kSelected && p.columns) {
     const int u = blockIdx.x;
-    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x == 0);
+    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x < 32);
     s.hb = u % p.hb;
     s.t0 = 0;
     s.t1 = s.u.tiles;
@@ -300,13 +313,13 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
         if (cta >= total) return false;
         if (cta >= begin && cta < end) {
           const int k = cta - (int)begin, j = k % per;
-          load_unit<kSelected>(p, threadIdx.x, sh.unit, false);
+          sh.found_row = (int)threadIdx.x;
           sh.found_hb = k / per;
           sh.found_t0 = (int)((int64_t)w.tiles * j / per);
           sh.found_left = (int)((int64_t)w.tiles * (j + 1) / per) - sh.found_t0;
         }
         __syncthreads();
-        s.u = sh.unit;
+        load_unit<kSelected>(p, sh.found_row, s.u, false);
         s.hb = sh.found_hb;
         s.t0 = sh.found_t0;
         s.left = sh.found_left;
@@ -499,16 +512,23 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       table2 = a.page_table + (int64_t)seg.u.seq * a.max_pages;
       pos2 = t * kTile + tok;
       rows2 = 0;
-      whole2 = !kSelected && (t + 1) * kTile <= seg.u.min_len;
-      if (pos2 < seg.u.min_len) {
-        rows2 = (1u << seg.u.rows) - 1;
-        if (kSelected) pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
-      } else if (!kSelected) {
-        for (int r = 0; r < seg.u.rows; r++) {
-          int len, end, err;
-          row_span<kSelected>(a, seg.u.r0 + r, len, end, err);
-          rows2 |= (uint32_t)row_sees(a, seg.u.r0 + r, len, end, pos2) << r;
+      if (kSelected) {
+        if (pos2 < seg.u.min_len) {
+          rows2 = 1;
+          pos2 = a.idx[(int64_t)seg.u.r0 * a.k + pos2];
         }
+        return;
+      }
+      whole2 = (t + 1) * kTile <= seg.u.min_len;
+      if (whole2) {
+        rows2 = (1u << seg.u.rows) - 1;
+        return;
+      }
+#pragma unroll 4
+      for (int r = 0; r < seg.u.rows; r++) {
+        const int len = __shfl_sync(kFull, seg.u.len, r), end = __shfl_sync(kFull, seg.u.end, r), j = pos2 - len;
+        const uint32_t word = j >= 0 && pos2 < end ? a.tree[(int64_t)(seg.u.r0 + r) * a.words + (j >> 5)] : 0;
+        rows2 |= (uint32_t)(j < 0 || (word >> (j & 31) & 1)) << r;
       }
     };
     auto pages = [&]() {
@@ -641,7 +661,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
-    } while (next_seg<kSelected>(p, seg, lane == 0));
+    } while (next_seg<kSelected>(p, seg, true));
     if (p.q_boxes && ictr > 0) mma::wait_warp(qfull, (ictr - 1) & 1, ctl, false);  // lands before the CTA ends
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)

@@ -229,7 +229,10 @@ __device__ __forceinline__ void ld_32x32(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 32; i++) v[i] = __uint_as_float(r[i]);
 }
-// 32 lanes x 56 columns: three loads in flight together, one wait.
+// 32 lanes x 56 columns: three loads in flight together, one wait.  (The first load's results
+// must not share registers with the others' addresses.)
+#define FP4IDX_R8E(o) "=&r"(r[o]), "=&r"(r[o + 1]), "=&r"(r[o + 2]), "=&r"(r[o + 3]), "=&r"(r[o + 4]), "=&r"(r[o + 5]), \
+                      "=&r"(r[o + 6]), "=&r"(r[o + 7])
 __device__ __forceinline__ void ld_32x56(uint32_t taddr, float* v) {
   uint32_t r[56];
   asm volatile(
@@ -238,7 +241,7 @@ __device__ __forceinline__ void ld_32x56(uint32_t taddr, float* v) {
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47}, [%57];\n\t"
       "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%48,%49,%50,%51,%52,%53,%54,%55}, [%58];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : FP4IDX_R8(0), FP4IDX_R8(8), FP4IDX_R8(16), FP4IDX_R8(24), FP4IDX_R8(32), FP4IDX_R8(40), FP4IDX_R8(48)
+      : FP4IDX_R8E(0), FP4IDX_R8E(8), FP4IDX_R8E(16), FP4IDX_R8E(24), FP4IDX_R8E(32), FP4IDX_R8E(40), FP4IDX_R8E(48)
       : "r"(taddr), "r"(taddr + 32), "r"(taddr + 48)
       : "memory");
 #pragma unroll
@@ -256,6 +259,7 @@ __device__ __forceinline__ void ld_32x8(uint32_t taddr, float* v) {
   for (int i = 0; i < 8; i++) v[i] = __uint_as_float(r[i]);
 }
 #undef FP4IDX_R8
+#undef FP4IDX_R8E
 __device__ __forceinline__ void st_32x16(uint32_t taddr, const float* v) {
   uint32_t r[16];
 #pragma unroll
