@@ -87,6 +87,10 @@ cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t 
     *out = it->second;
     return cudaSuccess;
   }
+  if (size > 8) {  // above the portable size
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(size, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);

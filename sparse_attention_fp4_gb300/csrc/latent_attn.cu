@@ -12,19 +12,28 @@
 // and the second with M = dims contiguous.
 //
 // One persistent CTA an SM:
-//   warps 0-3   (0-7 with 64 columns, half of them each) softmax: S^T from tensor memory, masks, exp2, P^T to shared memory; at the end
-//               of a segment the output
+//   warps 0-3   (0-7 with 64 columns, half of them each) softmax: S^T from tensor memory,
+//               masks, exp2, P^T to shared memory; at the end of a segment the output
 //   then two warps that issue the MMAs of either product,
-//   a warp      that copies a segment's queries,
-//   a warp      that walks kAhead tiles ahead of the softmax and prefetches their tokens into L2, so
-//               that two stages in shared memory suffice to stream from HBM
+//   a warp      that copies a segment's queries (boxes by TMA where the columns are adjacent rows
+//               of q, else 16 bytes a lane),
+//   a warp      that walks kAhead tiles ahead of the softmax and prefetches their tokens into L2,
+//               so that two stages in shared memory suffice to stream from HBM
 //   the others  groups of four warps, one per stage, copy tiles: whole pages by TMA, listed
 //               tokens and partial pages with 16-byte cp.async (tokens that no row sees become
 //               zero rows)
-// The work is the list of all units' tiles (a unit: one row, or adjacent rows of a sequence,
-// and up to 64 columns), cut into runs of tiles, one a CTA, whatever the lengths are.
-// A unit cut between CTAs leaves each piece's unnormalised output, maximum and sum in the
-// workspace; combine_kernel joins them in order (the same bits every time).
+// A unit is one row, or adjacent rows of a sequence, and up to 64 columns.  Few units get a
+// cluster or a CTA each; else the list of all units' tiles is cut into runs of tiles, one a CTA,
+// whatever the lengths are.  A unit cut between CTAs leaves each piece's unnormalised output,
+// maximum and sum in the workspace; combine_kernel joins them in order.  All joins add in a
+// fixed order: the same bits every time.
+//
+// What bounds it, at the sizes measured (width 576, HBM 6.8 TB/s as measured by a copy):
+//   whole contexts, 16 heads   HBM: 64 sequences of up to 16,384 tokens, 673 MB in 130 us, 5.2 TB/s
+//   a selection a row, 64 or 128 heads, and trees  the chain of a tile: 64 columns take 1.0 us a
+//               tile, of which the MMAs' own time is 0.95 (their M = 64 form needs as long for 64
+//               columns as for 128 rows x 64; the operands' reads from shared memory bound them)
+//   few rows    latency: launch, lengths, list, pages, tokens are dependent reads, some 8 us
 //
 // The reference m of a column is not its running maximum: it is only raised when a score
 // passes it by more than 8 (in powers of two), so that in nearly all tiles the output in
@@ -59,7 +68,7 @@ struct Params {
   int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
   int32_t q_boxes;            // a unit's columns are adjacent rows of q: copied as boxes
   int32_t columns;            // selected rows: CTA c takes units c, c + grid, ... whole
-  int32_t cluster;            // CTAs of a cluster that share one unit; 0: the list is cut
+  int32_t cluster;            // CTAs (a cluster, if more than one) that share a unit; 0: the list is cut
   uint64_t wait_limit_ns;
   int32_t idle_producers;
 };
@@ -170,15 +179,20 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = 
 // 32 tiles make 128 pieces for the joining kernel instead of the 304 of an even cut over 152
 // CTAs (a piece's end costs as much as two tiles, and its 128 KB are written and read again).
 // Taken when `most` is at most an even share plus 1/16 and three tiles.
-// Few units, of rows with a selection each: a cluster of two, four or eight CTAs shares a unit and
-// adds its pieces up through distributed shared memory (no scan, no workspace, no second
-// launch, which together cost what three tiles do).
+// Few units: a cluster of up to 16 CTAs shares a unit and adds its pieces up through distributed
+// shared memory, or one CTA takes it.  There is no workspace and no second launch then, and
+// no scan where units are single rows; together these cost what six to nine tiles do (rows of
+// 12 to 128 heads over 9 to 20 tiles: 30.2 us against 36.3, 21.6 against 25.6, 15.6 against
+// 22.6), so this form is taken while a CTA gets at most kMore tiles above an even share.  Whole
+// contexts differ in length, and the host knows only the longest that may come: the list
+// is cut evenly above kMost tiles a CTA.
 // More units, of rows with a selection each, where whole rounds of units waste at most a
 // twentieth: CTA c takes units c, c + grid, ... whole.  No pieces, and the rows of one
 // sequence, whose selections overlap, are read at the same time (L2 then holds what they
 // share; one CTA taking them one after the other read all of it from HBM again).
 // Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
 // edge moves to the edge (no piece then, for 1/20 more work).
+constexpr int kMore = 8, kMost = 32;
 constexpr int kMaxWarps = 20;
 struct ScanShared {
   int64_t sums[kMaxWarps];
@@ -261,12 +275,33 @@ __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& ru
   return got;
 }
 template <bool kSelected>
-__device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh) {
+__device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh, int& u) {
   const int n = p.a.n_rows, step = blockDim.x;
-  if (kSelected && p.cluster) {
-    const int u = blockIdx.x >> (__ffs(p.cluster) - 1), j = blockIdx.x & (p.cluster - 1);
-    load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x < 32 && j == 0);
+  if (p.cluster) {
+    const int j = blockIdx.x & (p.cluster - 1);
+    int row = u / p.hb;
     s.hb = u % p.hb;
+    if (!kSelected && p.group > 1) {
+      // the u-th unit's first row (all rows are one chunk here), and the cluster's next unit
+      int run = -1;
+      int64_t units;
+      const Weight w = unit_weight<kSelected>(p, 0, run, sh, false);
+      const int64_t at = block_scan(w.tiles > 0, sh, units);
+      if (w.tiles > 0 && at == u + 1) sh.found_row = threadIdx.x;
+      __syncthreads();
+      if (u >= units) {  // fewer units than clusters
+        u = -1;
+        s.u.rows = s.u.r0 = 0;
+        return false;
+      }
+      u += gridDim.x >> (__ffs(p.cluster) - 1);
+      if (u >= units) u = -1;
+      row = sh.found_row;
+      s.hb = 0;
+    } else {
+      u = -1;
+    }
+    load_unit<kSelected>(p, row, s.u, threadIdx.x < 32 && j == 0);
     s.t0 = (int)((int64_t)s.u.tiles * j / p.cluster);
     s.t1 = (int)((int64_t)s.u.tiles * (j + 1) / p.cluster);
     s.left = s.t1 - s.t0;
@@ -437,7 +472,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   const uint32_t qfull = bar(4 * kStages), qempty = bar(4 * kStages + 1), done = bar(4 * kStages + 6);
   const auto sfull = [&](int b) { return bar(4 * kStages + 2 + b); };
   const auto pfull = [&](int b) { return bar(4 * kStages + 4 + b); };  // by the tile's parity, as sfull
-  if (threadIdx.x == 0) {
+  const auto init_barriers = [&]() {
     for (int s = 0; s < kStages; s++) {
       for (int half = 0; half < 2; half++) {
         ptx::mbar_init(kfull(s, half), 4);
@@ -451,9 +486,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::mbar_init(pfull(0), S::kSoftWarps);
     ptx::mbar_init(pfull(1), S::kSoftWarps);
     ptx::mbar_init(done, 2);
-    *abort_flag = 0;
     *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 8) = 0;  // tiles that the softmax has begun
     ptx::fence_mbar_init();
+  };
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    init_barriers();
   }
   if (warp == kScoreWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
   // Lists, page table and queries into L2, a line a thread of the whole grid, while the run is
@@ -466,13 +504,17 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  int unit = p.cluster ? (int)blockIdx.x >> (__ffs(p.cluster) - 1) : -1;
+  bool gave_up = false;
+again:  // (clusters take unit after unit if a call has more than the host counts on)
   Seg seg;
-  const bool any = first_seg<kSelected>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ));
+  const bool any = first_seg<kSelected>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ), unit) && !gave_up;
   Work wk = work_view(a.workspace);
-  if (threadIdx.x == 0 && !(kSelected && p.cluster)) {
+  if (threadIdx.x == 0 && !p.cluster) {
     wk.rec[2 * blockIdx.x] = Record{0, 0, 0, 0};
     wk.rec[2 * blockIdx.x + 1] = Record{0, 0, 0, 0};
   }
+  ptx::fence_proxy_async_smem();  // the scratch lies where queries will be copied to
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -964,7 +1006,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
       if (threadIdx.x < kN) {
         const int c = threadIdx.x;
         const float total = red[c] + red[kN + c] + red[2 * kN + c] + red[3 * kN + c];
-        if (kSelected && p.cluster) {
+        if (p.cluster > 1) {
           sm_f[c] = total;
         } else if (whole) {
           sm_f[c] = total == 0.f ? 0.f : 1.f / total;
@@ -977,12 +1019,12 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
           wk.ml[slot * 2 * kCols + kCols + c] = total;
         }
       }
-      if (!whole && !(kSelected && p.cluster) && threadIdx.x == 0)
+      if (!whole && p.cluster <= 1 && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
       ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
-      if (kSelected && p.cluster) break;  // the one piece: joined below
+      if (p.cluster > 1) break;  // the one piece: joined below
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
       if (whole) {
@@ -1026,7 +1068,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (kSelected && p.cluster) {
+  if (p.cluster > 1) {
     // ---- the cluster's pieces are joined: each CTA for its share of the columns
     // All main loops are over, so shared memory is free: pieces of the CTA's columns at 0,
     // [piece][column][512] fp32, every piece's m and l in the query buffer.
@@ -1065,8 +1107,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     }
     mma::cluster_sync();
     for (int col = warp; col < share; col += S::kThreads / 32) {
-      const int c = mine * share + col, head = seg.hb * p.hs + c;  // one row a unit
-      if (c >= p.hs || head >= a.heads) continue;
+      const int c = mine * share + col, r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
+      if (r >= seg.u.rows || h >= p.hs || head >= a.heads) continue;
       float top = kNoMax, total = 0.f, o[16] = {};
       for (int i = 0; i < ctas; i++) top = fmaxf(top, gather[(i * 2) * kN + c]);
       for (int i = 0; i < ctas; i++) {
@@ -1085,7 +1127,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
         }
       }
       const float inv = total == 0.f ? 0.f : 1.f / total;
-      const int64_t row = (int64_t)seg.u.r0 * a.heads + head;
+      const int64_t row = (int64_t)(seg.u.r0 + r) * a.heads + head;
 #pragma unroll
       for (int q = 0; q < 4; q++)
         *reinterpret_cast<uint2*>(a.out + row * kValue + q * 128 + lane * 4) =
@@ -1096,6 +1138,14 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
+  }
+  if (p.cluster && unit >= 0) {
+    gave_up = *abort_flag;  // (the cluster's other CTAs count on this one until the end)
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < S::kBars; i++) mma::mbar_inval(bar(i));
+      init_barriers();
+    }
+    goto again;  // its barriers are seen behind the next __syncthreads
   }
   if (warp == kScoreWarp) ptx::tmem_dealloc(tmem, S::kTmemCols);
 }
@@ -1252,29 +1302,37 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(S::kThreads, 1, 1);
   cfg.dynamicSmemBytes = S::kBytes;
-  // A cluster a unit, of the largest size of which the device holds that many, if its CTAs get
-  // at most three tiles more than an even cut would give them.
-  const int units_all = p.a.n_rows * p.hb, tiles = (p.a.k + kTile - 1) / kTile;
-  for (int c = 8; kSelected && c >= 2 && may_split; c /= 2) {
-    if ((int64_t)units_all * c > ctas || (tiles + c - 1) / c > ((int64_t)tiles * units_all + ctas - 1) / ctas + 3) continue;
-    int fit = 0;
-    e = resident_clusters(kernel, c, S::kThreads, S::kBytes, &fit);
-    if (e != cudaSuccess) return e;
-    if (fit < units_all) continue;
+  // A cluster a unit, of the largest size of which the device holds that many, or a CTA a unit
+  // (c = 1).  Units of several rows are counted as if every sequence's rows were adjacent; if
+  // there are more, the clusters take them in rounds.
+  const int runs = std::min(p.a.n_rows, p.a.num_seqs);
+  const int units = p.group == 1 ? p.a.n_rows * p.hb : runs + (p.a.n_rows - runs) / p.group;
+  const int tiles = ((kSelected ? p.a.k : p.a.max_context) + kTile - 1) / kTile;
+  const bool one_chunk = p.group == 1 || p.a.n_rows <= S::kThreads;
+  for (int c = 16; c >= 1 && may_split && one_chunk; c /= 2) {
+    const int64_t share = (tiles + c - 1) / c, even = ((int64_t)tiles * units + ctas - 1) / ctas;
+    if ((int64_t)units * c > ctas || share > even + kMore || (!kSelected && share > kMost)) continue;
+    if (c > 1 && (c >= 2 * tiles || (c == 16 && tiles <= 8 * 3))) continue;  // as fast with half as many
+    if (c > 1) {
+      int fit = 0;
+      e = resident_clusters(kernel, c, S::kThreads, S::kBytes, &fit);
+      if (e != cudaSuccess) return e;
+      if (fit < units) continue;
+      attr[1].id = cudaLaunchAttributeClusterDimension;
+      attr[1].val.clusterDim.x = c;
+      attr[1].val.clusterDim.y = 1;
+      attr[1].val.clusterDim.z = 1;
+      cfg.numAttrs = 2;
+    }
     p.cluster = c;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = c;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.numAttrs = 2;
-    cfg.gridDim = dim3(units_all * c, 1, 1);
+    cfg.gridDim = dim3(units * c, 1, 1);
     return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   }
   e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   if (e != cudaSuccess || !may_split) return e;
-  const int units = std::min(ctas, p.a.n_rows * p.hb);  // at most
-  const bool many = units * 8 <= ctas;  // eight pieces a unit or more
-  cfg.gridDim = dim3(units, many ? kN / 2 : kN / 8, 1);
+  const int cut = std::min(ctas, p.a.n_rows * p.hb);  // units in pieces, at most
+  const bool many = cut * 8 <= ctas;  // eight pieces a unit or more
+  cfg.gridDim = dim3(cut, many ? kN / 2 : kN / 8, 1);
   cfg.blockDim = dim3(many ? 1024 : 256, 1, 1);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, many ? combine_kernel<2, 16> : combine_kernel<8, 1>, p, ctas);

@@ -30,6 +30,11 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, const p
   return __all_sync(pipe::kFull, ok);
 }
 
+// Before a barrier is set up anew; nothing may be waiting on it.
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared.b64 [%0];" ::"r"(bar) : "memory");
+}
+
 // Operands lie in shared memory as rows of 128 bytes (64 bf16), eight rows an atom of 1,024
 // bytes whose 16-byte pieces are stored at piece ^ (row & 7).  K-major: rows are M or N,
 // 1,024 bytes (sbo) between groups of eight rows; the 16 elements of K of one MMA start 32

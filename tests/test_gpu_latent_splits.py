@@ -111,3 +111,57 @@ def test_waits_run_out():
     finally:
         fp4idx.test_pipeline_waits(False, 0)
     calls(True)
+
+
+def alternating(heads, width, n=24, most=500):
+    """Rows whose sequence changes from row to row: as many units as rows, more than two
+    sequences of twelve rows would have."""
+    b = Batch(12, [most, most - 7], n // 2, heads, width)
+    seqs = [(i * 5 % 7) & 1 for i in range(n)]
+    assert b.T == n
+    b.row_seq = i32(seqs)
+    L = [(i * 131) % most if i % 5 else 0 for i in range(n)]
+    return b, L
+
+
+@pytest.mark.parametrize("heads,width", [(8, 512), (12, 576), (32, 512), (40, 576), (128, 512)])
+def test_whole_contexts_in_clusters(heads, width):
+    """Few short units share a cluster each; units that outnumber the clusters come round after
+    round, and clusters without one write nothing."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    b, L = alternating(heads, width)
+    status = i32([0])
+    out, lse = b.buffers()
+    fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(L), 500, b.scale, workspace(b), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 0
+    b.check(out, lse, [list(range(v)) for v in L])
+    # 12 rows of the last of seven sequences: two units where up to seven and more could be
+    c = Batch(13, [3, 4, 5, 6, 7, 8, 450], 2, heads, width)
+    c.row_seq = i32([6] * c.T)
+    L = [450 - (c.T - 1 - i) for i in range(c.T)]
+    out, lse = c.buffers()
+    fp4idx.latent_attn(c.q, c.cache, c.table, c.row_seq, i32(L), 450, c.scale, workspace(c), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 0
+    c.check(out, lse, [list(range(v)) for v in L])
+
+
+@pytest.mark.parametrize("heads", [8, 64])
+def test_waits_run_out_in_clusters(heads):
+    from sparse_attention_fp4_gb300 import fp4idx
+    b, L = alternating(heads, 576)
+
+    def call(want):
+        status = i32([0])
+        out, lse = b.buffers()
+        fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(L), 500, b.scale, workspace(b), out, lse=lse, status=status)
+        assert fp4idx.read_status(status) == want
+        if want == 0:
+            b.check(out, lse, [list(range(v)) for v in L])
+
+    call(0)
+    try:
+        fp4idx.test_pipeline_waits(True, 30_000_000)
+        call(6)
+    finally:
+        fp4idx.test_pipeline_waits(False, 0)
+    call(0)
