@@ -67,7 +67,7 @@ struct Params {
   LatentArgs a;
   int32_t hb, hs, hp, group;  // head blocks, heads a block, heads a block padded to 8, rows a unit at most
   int32_t q_boxes;            // a unit's columns are adjacent rows of q: copied as boxes
-  int32_t columns;            // selected rows: CTA c takes units c, c + grid, ... whole
+  int32_t whole;              // selected rows: CTAs take whole units, one after the other
   int32_t cluster;            // CTAs (a cluster, if more than one) that share a unit; 0: the list is cut
   uint64_t wait_limit_ns;
   int32_t idle_producers;
@@ -82,6 +82,7 @@ struct Work {
   Record* rec;
   float* ml;
   float* o;
+  uint32_t* taken;  // units that CTAs have asked for (zero before a launch that counts)
 };
 __host__ __device__ __forceinline__ Work work_view(void* ws) {
   uint8_t* p = reinterpret_cast<uint8_t*>(ws);
@@ -89,10 +90,11 @@ __host__ __device__ __forceinline__ Work work_view(void* ws) {
   w.rec = reinterpret_cast<Record*>(p);
   w.ml = reinterpret_cast<float*>(p + 2 * kMaxCtas * sizeof(Record));
   w.o = w.ml + 2 * kMaxCtas * 2 * kCols;
+  w.taken = reinterpret_cast<uint32_t*>(w.o + (size_t)2 * kMaxCtas * kCols * kValue);
   return w;
 }
 constexpr size_t kWorkBytes =
-    2 * kMaxCtas * (sizeof(Record) + 2 * kCols * sizeof(float) + (size_t)kCols * kValue * sizeof(float));
+    2 * kMaxCtas * (sizeof(Record) + 2 * kCols * sizeof(float) + (size_t)kCols * kValue * sizeof(float)) + 128;
 
 // ---------------------------------------------------------------- the list of tiles
 // Row t's sequence and the tokens that it sees: its plain length, and the end of what it sees
@@ -152,17 +154,52 @@ struct Seg {
   Unit u;
   int hb, t0, t1;
   int64_t left;  // tiles of the CTA from t0 on
+  uint32_t n;    // segments of the CTA before this one
+};
+// Whole units: the first warp of a CTA that needs the next one (a loader) asks for it and passes it
+// on through a ring in shared memory: (segment's number, unit; kNoUnit behind the last).  The
+// loaders look at most four times three tiles ahead of the slowest warp, so entries are not
+// overtaken, but for the prefetches', which then stop.
+constexpr uint32_t kFeed = 32, kNoUnit = ~0u;
+struct Feed {
+  volatile uint64_t* ring;
+  uint32_t* asked;  // segments asked for
+  Ctl ctl;
 };
 template <bool kSelected>
-__device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = false) {
-  s.left -= s.t1 - s.t0;
-  if (s.left <= 0) return false;
-  if (kSelected && p.columns) {
-    const int64_t u = (int64_t)s.u.r0 * p.hb + s.hb + gridDim.x;
-    if (u >= (int64_t)p.a.n_rows * p.hb) return false;
+__device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& feed, bool report = false) {
+  if (kSelected && p.whole) {
+    const uint32_t n = ++s.n;
+    uint32_t u = kNoUnit;
+    if ((threadIdx.x & 31) == 0) {
+      if (atomicCAS(feed.asked, n - 1, n) == n - 1) {
+        u = gridDim.x + atomicAdd(work_view(p.a.workspace).taken, 1u);
+        if (u >= (uint32_t)(p.a.n_rows * p.hb)) u = kNoUnit;
+        feed.ring[n % kFeed] = (uint64_t)n << 32 | u;
+      } else {
+        const int64_t t0 = clock64();
+        uint64_t got;
+        while ((uint32_t)((got = feed.ring[n % kFeed]) >> 32) < n) {
+          if (*feed.ctl.abort) break;
+          if (clock64() - t0 > (int64_t)feed.ctl.timeout_ns) {
+            pipe::give_up(feed.ctl);
+            break;
+          }
+        }
+        if ((uint32_t)(got >> 32) == n) u = (uint32_t)got;
+      }
+    }
+    u = __shfl_sync(kFull, u, 0);
+    if (u == kNoUnit) return false;
     s.hb = (int)(u % p.hb);
     load_unit<kSelected>(p, (int)(u / p.hb), s.u, report);
-  } else if (++s.hb == p.hb) {
+    s.t0 = 0;
+    s.t1 = s.u.tiles;
+    return true;
+  }
+  s.left -= s.t1 - s.t0;
+  if (s.left <= 0) return false;
+  if (++s.hb == p.hb) {
     s.hb = 0;
     load_unit<kSelected>(p, s.u.r0 + s.u.rows, s.u, false);
   }
@@ -187,9 +224,11 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, bool report = 
 // contexts differ in length, and the host knows only the longest that may come: the list
 // is cut evenly above kMost tiles a CTA.
 // More units, of rows with a selection each, where whole rounds of units waste at most a
-// twentieth: CTA c takes units c, c + grid, ... whole.  No pieces, and the rows of one
-// sequence, whose selections overlap, are read at the same time (L2 then holds what they
-// share; one CTA taking them one after the other read all of it from HBM again).
+// twentieth: the CTAs take whole units in order, each the next one when it needs one (dealt out in
+// turn, the slowest CTA of 1,488 units over 2,048 tokens ended at 631 us, half of them before
+// 545).  No pieces, and the rows of one sequence, whose selections overlap, are read at the same
+// time (L2 then holds what they share; one CTA taking them one after the other read all of it
+// from HBM again).
 // Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
 // edge moves to the edge (no piece then, for 1/20 more work).
 constexpr int kMore = 8, kMost = 32;
@@ -307,13 +346,12 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
     s.left = s.t1 - s.t0;
     return s.left > 0;
   }
-  if (kSelected && p.columns) {
+  if (kSelected && p.whole) {
     const int u = blockIdx.x;
     load_unit<kSelected>(p, u / p.hb, s.u, threadIdx.x < 32);
     s.hb = u % p.hb;
     s.t0 = 0;
     s.t1 = s.u.tiles;
-    s.left = INT64_MAX;
     return true;
   }
   const bool report = blockIdx.x == 0;
@@ -437,7 +475,8 @@ struct Shape {
   // kfull[stages][2], kempty[stages][2], qfull, qempty, sfull[2], pfull[2], done
   static constexpr int kBars = 4 * kStages + 7;
   static constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
-  static constexpr uint32_t kBytes = kOffMisc + 16 + 1024;  // and the base's alignment
+  static constexpr uint32_t kOffFeed = kOffMisc + 16;
+  static constexpr uint32_t kBytes = kOffFeed + kFeed * 8 + 1024;  // and the base's alignment
   static_assert(kQChunk <= kTile * 128, "the weights fit a block of keys");
   static __device__ __forceinline__ uint32_t off_p(int stage) {
     return kOwnP ? kOffP + stage * kQChunk : stage * kStageBytes + 8 * kTile * 128;
@@ -463,6 +502,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
 
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + S::kOffMisc);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffMisc + 4);
+  volatile uint64_t* feed_ring = reinterpret_cast<volatile uint64_t*>(smem + S::kOffFeed);
   auto bar = [&](int i) { return sb + S::kOffBar + i * 8; };
   // A stage is filled and freed in two halves, dims 0..255 and the rest, so that the scores'
   // product begins while the second half is on its way, and the next tile's first half is
@@ -491,6 +531,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   };
   if (threadIdx.x == 0) {
     *abort_flag = 0;
+    for (uint32_t i = 0; i < kFeed; i++) feed_ring[i] = 0;
+    *reinterpret_cast<volatile uint32_t*>(smem + S::kOffMisc + 12) = 0;
     init_barriers();
   }
   if (warp == kScoreWarp) ptx::tmem_alloc(ptx::smem_addr(tmem_slot), S::kTmemCols);
@@ -508,6 +550,7 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   bool gave_up = false;
 again:  // (clusters take unit after unit if a call has more than the host counts on)
   Seg seg;
+  seg.n = 0;
   const bool any = first_seg<kSelected>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ), unit) && !gave_up;
   Work wk = work_view(a.workspace);
   if (threadIdx.x == 0 && !p.cluster) {
@@ -520,6 +563,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, a.status, 2 * p.wait_limit_ns};  // in cycles: at most 2.07 a ns
+  const Feed feed{feed_ring, reinterpret_cast<uint32_t*>(smem + S::kOffMisc + 12), ctl};
   const uint32_t tm_s = tmem + 4 * kN;  // two S^T buffers behind the output
 
   if (any && warp >= kLoadWarp) {
@@ -536,7 +580,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
       t += n;
       while (t >= seg.t1) {
         n = t - seg.t1;
-        if (!next_seg<kSelected>(p, seg)) {
+        if (!next_seg<kSelected>(p, seg, feed)) {
           have = false;
           return;
         }
@@ -703,7 +747,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
-    } while (next_seg<kSelected>(p, seg, true));
+    } while (next_seg<kSelected>(p, seg, feed, true));
     if (p.q_boxes && ictr > 0) mma::wait_warp(qfull, (ictr - 1) & 1, ctl, false);  // lands before the CTA ends
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)
@@ -737,7 +781,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
           }
         }
       }
-    } while (on && next_seg<kSelected>(p, seg));
+    } while (on && next_seg<kSelected>(p, seg, feed));
   } else if (any && warp == kScoreWarp) {
     // ------------------------------------------------------------ the first product (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
@@ -786,7 +830,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
           phase ^= 1;
         }
       }
-    } while (ok && next_seg<kSelected>(p, seg));
+    } while (ok && next_seg<kSelected>(p, seg, feed));
     // nothing of this CTA's may be under way in the tensor cores when it ends
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
@@ -819,7 +863,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
         __syncwarp();
         if (++stage == kStages) stage = 0;
       }
-    } while (ok && next_seg<kSelected>(p, seg));
+    } while (ok && next_seg<kSelected>(p, seg, feed));
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
     mma::wait_warp(done, 0, ctl, false);
@@ -1063,7 +1107,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
       }
       ptx::tc_fence_before();
       ptx::named_bar_sync(1, kSoft);  // red, sm_m and sm_f are free again
-    } while (next_seg<kSelected>(p, seg));
+    } while (next_seg<kSelected>(p, seg, feed));
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -1328,6 +1372,11 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
     cfg.gridDim = dim3(units * c, 1, 1);
     return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   }
+  if (p.whole) {
+    e = cudaMemsetAsync(work_view(p.a.workspace).taken, 0, sizeof(uint32_t), stream);
+    if (e != cudaSuccess) return e;
+    cfg.numAttrs = 0;  // the launch before is not a kernel's
+  }
   e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int cut = std::min(ctas, p.a.n_rows * p.hb);  // units in pieces, at most
@@ -1374,8 +1423,8 @@ cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool selected
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sms, kMaxCtas);
   const int units = a.n_rows * p.hb, rounds = (units + ctas - 1) / ctas;
-  p.columns = selected && units > ctas && (int64_t)rounds * ctas * 20 <= (int64_t)units * 21;
-  const bool may_split = !p.columns && (selected ? a.k : a.max_context) > kTile;
+  p.whole = selected && units > ctas && (units >= 5 * ctas || (int64_t)rounds * ctas * 20 <= (int64_t)units * 21);
+  const bool may_split = !p.whole && (selected ? a.k : a.max_context) > kTile;
   const int cols = p.group * p.hp;
   return selected ? launch_shape<true>(p, width, cols, ctas, may_split, stream)
                   : launch_shape<false>(p, width, cols, ctas, may_split, stream);

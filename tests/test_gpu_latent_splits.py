@@ -165,3 +165,51 @@ def test_waits_run_out_in_clusters(heads):
     finally:
         fp4idx.test_pipeline_waits(False, 0)
     call(0)
+
+
+def test_whole_units():
+    """More selections than CTAs: captured and replayed, two at once, and with loads that never
+    come; whatever the workspace holds."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    rows = 608
+    lens = [1 + (37 * i) % 500 for i in range(rows)]
+    b = Batch(14, lens, 1, 24, 576)
+    idx, want = selection(b, 150, 2, lens)
+    ws = [workspace(b) for _ in range(2)]
+    bufs = [b.buffers() for _ in range(2)]
+    status = i32([0])
+
+    def call(i, stream=None):
+        fp4idx.latent_attn_topk(b.q, b.cache, b.table, b.row_seq, idx, b.scale, ws[i], bufs[i][0], lse=bufs[i][1],
+                                status=status, stream=stream)
+
+    call(0)
+    call(1)
+    b.check(*bufs[0], want, rows=range(0, rows, 17))
+    first = [v.clone() for v in bufs[0]]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    side = torch.cuda.Stream()
+    for fill in (0, 255, 7):
+        for w, (out, lse) in zip(ws, bufs):
+            w.view(torch.uint8).fill_(fill)
+            out.fill_(3.0)
+            lse.fill_(3.0)
+        side.wait_stream(torch.cuda.current_stream())
+        graph.replay()
+        call(1, stream=side)
+        torch.cuda.synchronize()
+        assert fp4idx.read_status(status) == 0
+        for out, lse in bufs:
+            assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    try:
+        fp4idx.test_pipeline_waits(True, 30_000_000)
+        call(0)
+        assert fp4idx.read_status(status) == 6
+    finally:
+        fp4idx.test_pipeline_waits(False, 0)
+    status.zero_()
+    call(0)
+    assert fp4idx.read_status(status) == 0
+    assert torch.equal(bufs[0][0], first[0]) and torch.equal(bufs[0][1], first[1])
