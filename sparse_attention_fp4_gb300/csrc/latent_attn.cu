@@ -223,12 +223,12 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& fe
 // 22.6), so this form is taken while a CTA gets at most kMore tiles above an even share.  Whole
 // contexts differ in length, and the host knows only the longest that may come: the list
 // is cut evenly above kMost tiles a CTA.
-// More units, of rows with a selection each, where whole rounds of units waste at most a
-// twentieth: the CTAs take whole units in order, each the next one when it needs one (dealt out in
-// turn, the slowest CTA of 1,488 units over 2,048 tokens ended at 631 us, half of them before
-// 545).  No pieces, and the rows of one sequence, whose selections overlap, are read at the same
-// time (L2 then holds what they share; one CTA taking them one after the other read all of it
-// from HBM again).
+// More units, of rows with a selection each: the CTAs take whole units in order, each the next
+// one when it needs one.  No pieces, and the rows of one sequence, whose selections overlap,
+// are read at the same time (L2 then holds what they share).  1,488 units of 2,048 tokens: 655
+// us by an even cut, 491 so; 360 of 500 tokens and two head blocks 106 and 83; 384 of 2,048
+// 162 and 149.  With less than two units a CTA only where the last round adds at most kMore
+// tiles (235 of 1,667: 92 us either way).
 // Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
 // edge moves to the edge (no piece then, for 1/20 more work).
 constexpr int kMore = 8, kMost = 32;
@@ -697,19 +697,18 @@ again:  // (clusters take unit after unit if a call has more than the host count
           mma::cp_async16(dst + c * (kTile * 128) + mma::sw128(wrow + g * 4, piece), src[g] + c * 64, bytes[g]);
       }
       mma::cp_async_commit();
-      const uint32_t kdone = kcur;
+      mma::cp_async_wait_group<1>();
+      ptx::fence_proxy_async_smem();
+      arrive_warp(kfull(s, 0), lane);
       kcur = kctr;
       if (have) {
         pages();
         advance(kStages);
         if (have) positions();
       }
-      mma::cp_async_wait_group<1>();
-      ptx::fence_proxy_async_smem();
-      arrive_warp(kfull(kdone % kStages, 0), lane);
       mma::cp_async_wait_group<0>();
       ptx::fence_proxy_async_smem();
-      arrive_warp(kfull(kdone % kStages, 1), lane);
+      arrive_warp(kfull(s, 1), lane);
     }
     mma::cp_async_wait_all();
     // every copy lands before the CTA ends
@@ -1422,8 +1421,9 @@ cudaError_t launch_latent_attn(const LatentArgs& a, int32_t width, bool selected
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const int ctas = std::min(sms, kMaxCtas);
-  const int units = a.n_rows * p.hb, rounds = (units + ctas - 1) / ctas;
-  p.whole = selected && units > ctas && (units >= 5 * ctas || (int64_t)rounds * ctas * 20 <= (int64_t)units * 21);
+  const int units = a.n_rows * p.hb, rounds = (units + ctas - 1) / ctas, tiles = (a.k + kTile - 1) / kTile;
+  p.whole = selected && units > ctas &&
+            (units >= 2 * ctas || (int64_t)rounds * tiles <= (int64_t)tiles * units / ctas + kMore);
   const bool may_split = !p.whole && (selected ? a.k : a.max_context) > kTile;
   const int cols = p.group * p.hp;
   return selected ? launch_shape<true>(p, width, cols, ctas, may_split, stream)
