@@ -135,7 +135,7 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
   fp4idx::PrefillArgs a{};
   a.q = q; a.kv = kv; a.k_rope = k_rope; a.cu_q = cu_q; a.cu_kv = cu_kv; a.out = out; a.lse = lse;
   a.status = status_dev; a.n_q = (int32_t)n_q; a.n_kv = (int32_t)n_kv; a.n_seqs = (int32_t)n_seqs; a.heads = n_heads;
-  a.max_q = max_q; a.max_kv = max_kv; a.scale = scale;
+  a.max_q = max_q < a.n_q ? max_q : a.n_q; a.max_kv = max_kv; a.scale = scale;  // (loose bounds launch no more)
   return from_cuda(fp4idx::launch_latent_prefill(a, as_stream(stream)));
 }
 

@@ -144,3 +144,13 @@ def test_nothing():
         fp4idx.latent_prefill(p.q, p.kv[:, :, :200], p.kr, p.cu_q, p.cu_k, 4, 5, 1.0, out)
     with pytest.raises(ValueError):
         fp4idx.latent_prefill(p.q, p.kv, p.kr[:2], p.cu_q, p.cu_k, 4, 5, 1.0, out)
+
+
+def test_loose_bounds():
+    """Bounds far above the lengths change nothing."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    p = Prompts(15, [5, 130], [9, 300], 2, behind=3)
+    status = i32([0])
+    out, lse = p.run(status, max_q=2 ** 31 - 1, max_kv=2 ** 31 - 1)
+    assert fp4idx.read_status(status) == 0
+    p.check(out, lse, every=9)
