@@ -436,6 +436,7 @@ int fp4idx_topk_merge(const float* cand_values, const int32_t* cand_idx, int64_t
  *   cu_rows, cu_context [n_seqs+1] int32 (written): offsets of the sequences' rows, and
  *              of their entries after the step, each packed in sequence order
  *   counts [4] int32 (written): rows, stores, pages taken, sequences planned
+ *   max_rows, max_stores <= 2^30
  * *free_head and cached_lens are not written: the caller adds counts[2] and new_lens
  * when the step is done (a repeated call gives the same result).
  * Sequences are planned in order; the first whose rows, stores or pages do not fit in

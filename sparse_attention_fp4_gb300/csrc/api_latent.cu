@@ -42,7 +42,7 @@ int fp4idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int64_
                      int32_t* cu_rows, int32_t* cu_context, int32_t* counts, int32_t* status_dev, void* stream) {
   if (n_seqs < 0 || n_free < 0 || max_pages < 1 || max_rows < 0 || max_stores < 0 || ratio < 1 || ratio > 64)
     return FP4IDX_ERR_INVALID_ARG;
-  if (n_seqs > 65536 || max_pages > kMaxPages || n_free > INT32_MAX || max_rows > INT32_MAX || max_stores > INT32_MAX)
+  if (n_seqs > 65536 || max_pages > kMaxPages || n_free > INT32_MAX || max_rows > (1 << 30) || max_stores > (1 << 30))
     return FP4IDX_ERR_UNSUPPORTED;
   if (!cu_rows || !cu_context || !counts) return FP4IDX_ERR_INVALID_ARG;
   if (n_seqs > 0 && (!cached_lens || !new_lens || !page_table)) return FP4IDX_ERR_INVALID_ARG;

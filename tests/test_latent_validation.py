@@ -99,3 +99,11 @@ def test_latent_prefill(lib):
     for name in ("cq", "ck"):
         assert f(**{name: None}) == INVALID and f(**{name: M1}) == INVALID, name
     assert f(heads=1025) == UNSUPPORTED and f(seqs=65536) == UNSUPPORTED and f(nq=(1 << 24) + 1) == UNSUPPORTED
+
+
+def test_plan_step_limits(lib):
+    """Row and store counters are 32 bits and advance by a grid of threads: half of them stay free."""
+    base = dict(cached=A, new=A, n=3, ratio=4, free=A, n_free=9, head=A, table=A, max_pages=8, qp=A, rs=A, cl=A, rows=5,
+                sp=A, ss=A, stores=5, cu=A, cuc=A, counts=A, status=None, stream=None)
+    assert call(lib.fp4idx_plan_step, base, rows=(1 << 30) + 1) == UNSUPPORTED
+    assert call(lib.fp4idx_plan_step, base, stores=(1 << 30) + 1) == UNSUPPORTED
