@@ -3,7 +3,7 @@
 // Bound by HBM (2,304 bytes a row of 576).  A warp walks rows `step` apart; rows and their
 // cos/sin come by bulk copies into a ring of four a warp, 82 KB in flight an SM: 65,536 rows
 // take 51 us with plain loads, 39 us with loads a row ahead in registers (16 warps an SM) and
-// 32 us with the ring (4.8 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds
+// 31 us with the ring (4.9 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds
 // dims 8l..8l+7 and 256 + 8l.. of the 512; the rotated dims are taken from the ring again, a pair
 // (i, i + 32) a lane (pairs exchanged by shuffles, by eight lanes: 347 warp instructions a row and
 // 36 us).
@@ -114,7 +114,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
     for (int done = 0; done < count; done++) {
       const int i = __ffs(left) - 1, s = done % kRing;
       left &= left - 1;
-      if (!mma::wait_warp(bars + s * 8, phases >> s & 1, ctl, false)) return;
+      if (!mma::wait_warp(bars + s * 8, phases >> s & 1, ctl, false)) {
+        // the other copies in flight land before the CTA ends
+        for (int x = done + 1; x < asked; x++) mma::wait_warp(bars + (x % kRing) * 8, phases >> (x % kRing) & 1, ctl, false);
+        return;
+      }
       phases ^= 1u << s;
       const uint8_t* x = ring + s * R::kSlot;
       float a[8], b[8];
