@@ -28,12 +28,16 @@
 // maximum and sum in the workspace; combine_kernel joins them in order.  All joins add in a
 // fixed order: the same bits every time.
 //
-// What bounds it, at the sizes measured (width 576, HBM 6.8 TB/s as measured by a copy):
-//   whole contexts, 16 heads   HBM: 64 sequences of up to 16,384 tokens, 673 MB in 130 us, 5.2 TB/s
-//   a selection a row, 64 or 128 heads, and trees  the chain of a tile: 64 columns take 1.0 us a
-//               tile, of which the MMAs' own time is 0.95 (their M = 64 form needs as long for 64
-//               columns as for 128 rows x 64; the operands' reads from shared memory bound them)
-//   few rows    latency: launch, lengths, list, pages, tokens are dependent reads, some 8 us
+// What bounds it, at the sizes measured (a plain copy reaches 6.8 TB/s):
+//   whole contexts, 16 heads, width 576   HBM: 64 sequences of up to 16,384 tokens, 673 MB in
+//               129 us, 5.2 TB/s
+//   64 columns (selections with 64 heads, trees)   shared memory: a tile takes 2,650 cycles, of
+//               which 2,500 are its operands' bytes at 128 a cycle: keys and queries for the
+//               scores (M = 64 re-reads the queries every tile) 1,152, values and four times the
+//               weights 768, the tile's arrival 576.  1,536 selections of 2,048 tokens, 64 heads,
+//               width 576: 493 us
+//   few rows    latency: launch, lengths, list, pages and tokens are dependent reads, some 8 us;
+//               one row of 64 heads over 512 tokens 12 to 13 us
 //
 // The reference m of a column is not its running maximum: it is only raised when a score
 // passes it by more than 8 (in powers of two), so that in nearly all tiles the output in
