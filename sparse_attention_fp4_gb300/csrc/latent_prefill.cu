@@ -69,6 +69,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_prefill_kernel(const __gri
                                                                     const __grid_constant__ Params p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const PrefillArgs& a = p.a;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int seq = blockIdx.z, head = blockIdx.y;
   const int64_t q0 = a.cu_q[seq], q1 = a.cu_q[seq + 1], k0 = a.cu_kv[seq], k1 = a.cu_kv[seq + 1];
   if (q0 < 0 || q1 < q0 || q1 > a.n_q || k0 < 0 || k1 < k0 || k1 > a.n_kv || q1 - q0 > a.max_q || k1 - k0 > a.max_kv) {
@@ -443,8 +445,7 @@ cudaError_t launch_latent_prefill(const PrefillArgs& a, cudaStream_t stream) {
   cudaError_t e = set_smem_attr_once(kernel, kBytes);
   if (e != cudaSuccess) return e;
   const dim3 grid((a.max_q + 2 * kRows - 1) / (2 * kRows), a.heads, a.n_seqs);
-  latent_prefill_kernel<<<grid, kThreads, kBytes, stream>>>(q_map, kv_map, r_map, p);
-  return cudaGetLastError();
+  return launch_early(latent_prefill_kernel, grid, kThreads, kBytes, stream, q_map, kv_map, r_map, p);
 }
 
 }  // namespace fp4idx

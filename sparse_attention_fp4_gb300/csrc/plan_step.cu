@@ -63,6 +63,8 @@ __global__ void __launch_bounds__(kThreads, 1) plan_step_kernel(const PlanArgs a
   __shared__ Chunk sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int at = blockIdx.x * kThreads + tid, step = gridDim.x * kThreads;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const bool first = blockIdx.x == 0;
   int64_t head = a.free_head ? *a.free_head : 0;
   int64_t avail = (int64_t)a.n_free - head;
@@ -180,8 +182,7 @@ cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.max_rows + a.max_stores;
   const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, items / (2 * kThreads)));
-  plan_step_kernel<<<ctas, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_early(plan_step_kernel, dim3(ctas), kThreads, 0, stream, a);
 }
 
 }  // namespace fp4idx

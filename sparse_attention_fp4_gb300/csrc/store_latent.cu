@@ -3,7 +3,7 @@
 // Bound by HBM (2,304 bytes a row of 576).  A warp walks rows `step` apart; rows and their
 // cos/sin come by bulk copies into a ring of four a warp, 82 KB in flight an SM: 65,536 rows
 // take 51 us with plain loads, 39 us with loads a row ahead in registers (16 warps an SM) and
-// 31 us with the ring (4.9 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds
+// 30 us with the ring (5.4 TB/s; six or eight deep, or two CTAs an SM, the same).  Lane l holds
 // dims 8l..8l+7 and 256 + 8l.. of the 512; the rotated dims are taken from the ring again, a pair
 // (i, i + 32) a lane (pairs exchanged by shuffles, by eight lanes: 347 warp instructions a row and
 // 36 us).
@@ -47,9 +47,9 @@ struct Ring {
 
 template <int kWidth>
 __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
-    const uint16_t* __restrict__ kv, int64_t n_rows, const int32_t* __restrict__ positions,
-    const int32_t* __restrict__ slots, const uint16_t* __restrict__ norm_w, float eps,
-    const uint16_t* __restrict__ cos_sin, int32_t max_pos, uint16_t* __restrict__ cache, int64_t num_pages,
+    const uint16_t* kv, int64_t n_rows, const int32_t* positions,
+    const int32_t* slots, const uint16_t* norm_w, float eps,
+    const uint16_t* cos_sin, int32_t max_pos, uint16_t* cache, int64_t num_pages,
     int32_t* status, uint64_t wait_cycles) {
   using R = Ring<kWidth>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -65,6 +65,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
     ptx::fence_proxy_async_smem();
   }
   __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const pipe::Ctl ctl{abort_flag, status, wait_cycles};
   float w0[8], w1[8];
   unpack(*reinterpret_cast<const uint4*>(norm_w + lane * 8), w0);
@@ -82,8 +84,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
     const int64_t mine = n0 + lane * step;
     int32_t slot = -1, pos = 0;
     if (mine < n_rows) {
-      slot = __ldg(slots + mine);
-      pos = __ldg(positions + mine);
+      slot = slots[mine];
+      pos = positions[mine];
     }
     if (slot >= 0) {
       const bool bad_slot = slot >= num_pages * kPage;
@@ -167,9 +169,8 @@ cudaError_t launch_store_latent(const uint16_t* kv, int64_t n_rows, int32_t widt
   e = resident_ctas(reinterpret_cast<const void*>(kernel), kWarps * 32, bytes, &fit);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<int64_t>(fit, (n_rows + kWarps - 1) / kWarps);
-  kernel<<<grid, kWarps * 32, bytes, stream>>>(kv, n_rows, positions, slots, norm_w, eps, cos_sin, max_pos, cache,
-                                               num_pages, status, 2 * pipeline_wait_limit_ns());
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(grid), kWarps * 32, bytes, stream, kv, n_rows, positions, slots, norm_w, eps, cos_sin,
+                      max_pos, cache, num_pages, status, 2 * pipeline_wait_limit_ns());
 }
 
 }  // namespace fp4idx
