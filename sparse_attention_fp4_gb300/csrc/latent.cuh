@@ -10,21 +10,26 @@ namespace fp4idx {
 // memory fit on the current device at once, computed once per (kernel, size, device).
 cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t smem, int* out);
 
-// A launch that may begin while the one before it on the stream ends: the kernel waits
+// A launch, of clusters of `cluster` CTAs along x, that may begin while the one before it on the stream ends: the kernel waits
 // (griddepcontrol.wait) before its first access to global memory, and reads none of it as
 // read-only data, which the compiler may move above the wait.
 template <class... A, class... B>
-cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream, const B&... args) {
-  cudaLaunchAttribute attr[1];
+cudaError_t launch_early(void (*kernel)(A...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                         const B&... args) {
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<A>(args)...);
 }
 

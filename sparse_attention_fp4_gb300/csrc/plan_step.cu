@@ -182,7 +182,7 @@ cudaError_t launch_plan_step(const PlanArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const int64_t items = (int64_t)a.max_rows + a.max_stores;
   const int ctas = (int)std::max<int64_t>(1, std::min<int64_t>(sms, items / (2 * kThreads)));
-  return launch_early(plan_step_kernel, dim3(ctas), kThreads, 0, stream, a);
+  return launch_early(plan_step_kernel, dim3(ctas), kThreads, 0, 1, stream, a);
 }
 
 }  // namespace fp4idx

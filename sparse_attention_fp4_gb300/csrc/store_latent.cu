@@ -169,7 +169,7 @@ cudaError_t launch_store_latent(const uint16_t* kv, int64_t n_rows, int32_t widt
   e = resident_ctas(reinterpret_cast<const void*>(kernel), kWarps * 32, bytes, &fit);
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<int64_t>(fit, (n_rows + kWarps - 1) / kWarps);
-  return launch_early(kernel, dim3(grid), kWarps * 32, bytes, stream, kv, n_rows, positions, slots, norm_w, eps, cos_sin,
+  return launch_early(kernel, dim3(grid), kWarps * 32, bytes, 1, stream, kv, n_rows, positions, slots, norm_w, eps, cos_sin,
                       max_pos, cache, num_pages, status, 2 * pipeline_wait_limit_ns());
 }
 

@@ -154,3 +154,44 @@ def test_loose_bounds():
     out, lse = p.run(status, max_q=2 ** 31 - 1, max_kv=2 ** 31 - 1)
     assert fp4idx.read_status(status) == 0
     p.check(out, lse, every=9)
+
+
+@pytest.mark.parametrize("heads,nq,nk", [(1, [1], [2000]), (1, [300], [1900]), (2, [36, 1, 0, 257], [1100, 1000, 0, 300]),
+                                         (1, [256, 5], [4, 2300]), (3, [129], [1000]), (4, [700, 20], [700, 30])])
+def test_keys_of_a_block_split(heads, nq, nk):
+    """Few blocks of queries: clusters of two to eight CTAs share a block's keys, with pieces that
+    some rows or all see nothing of; the same bits every time."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    p = Prompts(heads + sum(nk), nq, nk, heads, behind=5)
+    status = i32([0])
+    out, lse = p.run(status)
+    p.check(out, lse, every=7)
+    for _ in range(3):
+        out2, lse2 = p.run(status)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+    assert fp4idx.read_status(status) == 0
+    try:
+        fp4idx.test_pipeline_waits(True, 30_000_000)
+        p.run(status)
+        assert fp4idx.read_status(status) == 6
+    finally:
+        fp4idx.test_pipeline_waits(False, 0)
+    status.zero_()
+    out2, lse2 = p.run(status)
+    assert fp4idx.read_status(status) == 0 and torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+def test_keys_split_nan():
+    """A NaN row of values in one piece: NaN for the rows that see it and up to 255 before it."""
+    p = Prompts(21, [200], [1500], 1)
+    p.kv[1450, 0, 130:] = math.nan
+    out, lse = p.run()
+    first = 1450 - 1300  # the first query that sees it
+    assert bool(out[first:, 0, 2:].isnan().all()) and not bool(lse.isnan().any())
+    q = Prompts(21, [200], [1500], 1)
+    want, _ = q.run()
+    assert torch.equal(out[:, 0, :2], want[:, 0, :2])
+    p.kv[1450, 0, 130:] = 0
+    p.kv[3, 0, 0] = math.nan
+    out, lse = p.run()
+    assert bool(out.isnan().all()) and bool(lse.isnan().all())
