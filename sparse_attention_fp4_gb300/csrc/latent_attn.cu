@@ -154,10 +154,11 @@ __device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool
 }
 
 // A run of tiles [t0, t1) of a unit's column block.
+constexpr int kEnd = 2;  // tiles that the end of a unit, its output and the next one's start cost
 struct Seg {
   Unit u;
   int hb, t0, t1;
-  int64_t left;  // tiles of the CTA from t0 on
+  int64_t left;  // tiles of the CTA from t0 on, and kEnd for each unit that ends
   uint32_t n;    // segments of the CTA before this one
 };
 // Whole units: the first warp of a CTA that needs the next one (a loader) asks for it and passes it
@@ -201,7 +202,7 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& fe
     s.t1 = s.u.tiles;
     return true;
   }
-  s.left -= s.t1 - s.t0;
+  s.left -= s.t1 - s.t0 + (s.t1 == s.u.tiles ? kEnd : 0);
   if (s.left <= 0) return false;
   if (++s.hb == p.hb) {
     s.hb = 0;
@@ -233,8 +234,9 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& fe
 // us by an even cut, 491 so; 360 of 500 tokens and two head blocks 106 and 83; 384 of 2,048
 // 162 and 149.  With less than two units a CTA only where the last round adds at most kMore
 // tiles (235 of 1,667: 92 us either way).
-// Otherwise the list of tiles is cut evenly, and a cut within 1/20 of a run from a unit's
-// edge moves to the edge (no piece then, for 1/20 more work).
+// Otherwise the list of tiles is cut evenly, a unit's end counting as kEnd tiles (without that, a
+// CTA with 19 empty units took 122 us where the others took 65), and a cut within 1/20 of a run
+// from a unit's edge moves to the edge (no piece then, for 1/20 more work).
 constexpr int kMore = 8, kMost = 32;
 constexpr int kMaxWarps = 20;
 struct ScanShared {
@@ -248,6 +250,7 @@ struct ScanShared {
 struct Weight {
   int32_t tiles, rows;  // of the unit that starts at the thread's row; 0 tiles: none does
 };
+__device__ __forceinline__ int64_t weight_of(const Weight& w) { return w.tiles ? w.tiles + kEnd : 0; }
 __device__ __forceinline__ int64_t block_scan(int64_t v, ScanShared& sh, int64_t& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
@@ -364,7 +367,7 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   Weight w{0, 0};
   for (int base = 0; base < n; base += step) {
     w = unit_weight<kSelected>(p, base, run, sh, report);
-    incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
+    incl = block_scan(weight_of(w) * p.hb, sh, total);
     all += total;
   }
   const int ctas = gridDim.x, cta = blockIdx.x;
@@ -374,7 +377,8 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
     if (units <= ctas) {
       // each warp tries one number of tiles a CTA
       const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = step >> 5;
-      const int least = (int)((all + ctas - 1) / ctas), span = (int)(all / ctas / 16) + 3;
+      const int64_t tiles = all - (int64_t)kEnd * units;
+      const int least = (int)((tiles + ctas - 1) / ctas), span = (int)(tiles / ctas / 16) + 3;
       const int gap = (span + warps - 1) / warps;
       const int mine = least + warp * gap;
       int need = 0;
@@ -413,23 +417,23 @@ __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& s
   for (int base = 0; base < n; base += step) {
     if (n > step) {
       w = unit_weight<kSelected>(p, base, run, sh, false);
-      incl = block_scan((int64_t)w.tiles * p.hb, sh, total);
+      incl = block_scan(weight_of(w) * p.hb, sh, total);
     }
-    const int64_t end = carry + incl, begin = end - (int64_t)w.tiles * p.hb;
+    const int64_t weight = weight_of(w), end = carry + incl, begin = end - weight * p.hb;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
       int64_t x = i ? x1 : x0;
       if (x < begin || x >= end) continue;
-      const int off = (int)((x - begin) % w.tiles);
+      const int off = (int)((x - begin) % weight);
       if (off <= near) x -= off;
-      else if (w.tiles - off <= near) x += w.tiles - off;
+      else if (weight - off <= near + kEnd) x += weight - off;
       sh.cut[i] = x;
       if (i == 0) {
         const int64_t at = x - begin;
         const bool past = x == end;
         sh.found_row = base + (int)threadIdx.x + (past ? w.rows : 0);
-        sh.found_hb = past ? 0 : (int)(at / w.tiles);
-        sh.found_t0 = past ? 0 : (int)(at % w.tiles);
+        sh.found_hb = past ? 0 : (int)(at / weight);
+        sh.found_t0 = past ? 0 : (int)(at % weight);
       }
     }
     carry += total;

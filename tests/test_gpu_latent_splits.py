@@ -213,3 +213,16 @@ def test_whole_units():
     call(0)
     assert fp4idx.read_status(status) == 0
     assert torch.equal(bufs[0][0], first[0]) and torch.equal(bufs[0][1], first[1])
+
+
+@pytest.mark.parametrize("heads", [8, 32, 128])
+def test_empty_units_among_long_ones(heads):
+    """Sequences of no tokens, one and many, in runs, before, between and behind the long ones."""
+    from sparse_attention_fp4_gb300 import fp4idx
+    lens = [0] * 9 + [2900] + [1] * 30 + [0] * 40 + [2500, 64, 65] + [0] * 25
+    b = Batch(16, lens, 1, heads, 512)
+    status = i32([0])
+    out, lse = b.buffers()
+    fp4idx.latent_attn(b.q, b.cache, b.table, b.row_seq, i32(lens), 2900, b.scale, workspace(b), out, lse=lse, status=status)
+    assert fp4idx.read_status(status) == 0
+    b.check(out, lse, [list(range(v)) for v in lens])
