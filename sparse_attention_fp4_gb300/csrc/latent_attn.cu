@@ -154,7 +154,7 @@ __device__ __forceinline__ void load_unit(const Params& p, int r0, Unit& u, bool
 }
 
 // A run of tiles [t0, t1) of a unit's column block.
-constexpr int kEnd = 2;  // tiles that the end of a unit, its output and the next one's start cost
+constexpr int kEnd = 3;  // tiles that the end of a unit, its output and the next one's start cost
 struct Seg {
   Unit u;
   int hb, t0, t1;
