@@ -1360,7 +1360,7 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   const int units = p.group == 1 ? p.a.n_rows * p.hb : runs + (p.a.n_rows - runs) / p.group;
   const int tiles = ((kSelected ? p.a.k : p.a.max_context) + kTile - 1) / kTile;
   const bool one_chunk = p.group == 1 || p.a.n_rows <= S::kThreads;
-  for (int c = 16; c >= 1 && may_split && one_chunk; c /= 2) {
+  for (int c = 16; c >= 1 && one_chunk; c /= 2) {
     const int64_t share = (tiles + c - 1) / c, even = ((int64_t)tiles * units + ctas - 1) / ctas;
     if ((int64_t)units * c > ctas || share > even + kMore || (!kSelected && share > kMost)) continue;
     if (c > 1 && (c >= 2 * tiles || (c == 16 && tiles <= 8 * 3))) continue;  // as fast with half as many
