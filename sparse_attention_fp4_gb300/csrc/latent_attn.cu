@@ -1334,11 +1334,12 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   static_assert(kN * kValue * 4 <= S::kOffQ, "a cluster's pieces fit the stages");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
   const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN, kSelected>);
-  CUtensorMap cache_map, q_map;
-  if (!encode_rows_of(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth, kPage) ||
-      !encode_rows_of(&q_map, p.a.q, (int64_t)p.a.n_rows * p.a.heads, kWidth, kN))
-    return cudaErrorInvalidValue;
+  // (a map that the kernel will not use is not encoded)
+  CUtensorMap cache_map{}, q_map{};
   p.q_boxes = p.group == 1 || p.hp == p.a.heads;
+  if ((!kSelected && !encode_rows_of(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth, kPage)) ||
+      (p.q_boxes && !encode_rows_of(&q_map, p.a.q, (int64_t)p.a.n_rows * p.a.heads, kWidth, kN)))
+    return cudaErrorInvalidValue;
   cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
   if (e != cudaSuccess) return e;
   // Both launches may begin while the one before them ends: each waits for it before its

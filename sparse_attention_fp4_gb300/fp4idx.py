@@ -422,10 +422,15 @@ PREFILL_KEY = 192
 PREFILL_VALUE = 128
 
 
+# (torch.cuda.current_device, without its check that CUDA is set up, which any CUDA tensor implies)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here(stream):
     """The current device, and the stream to launch on."""
-    dev = torch.cuda.current_device()
-    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    dev = _current_device()
+    return dev, _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _addr(t, name, dtypes, numel, dev):
@@ -433,7 +438,7 @@ def _addr(t, name, dtypes, numel, dev):
     at least `numel` elements.  (A plain function: a decode step's calls are short, and their
     argument checks are most of the host's time.)"""
     try:
-        if t.dtype in dtypes and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+        if t.dtype in dtypes and t.get_device() == dev and (not numel or t.numel() >= numel) and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
@@ -495,11 +500,13 @@ def latent_attn_workspace_bytes(max_rows, n_heads) -> int:
 
 
 def _latent_shapes(q, cache, page_table):
-    if q.dim() != 3 or cache.dim() != 3 or cache.shape[1] != PAGE_TOKENS or cache.shape[2] != q.shape[2]:
+    """n_rows, heads, width; num_pages; num_seqs, max_pages."""
+    rows, pool, table = q.shape, cache.shape, page_table.shape
+    if len(rows) != 3 or len(pool) != 3 or pool[1] != PAGE_TOKENS or pool[2] != rows[2]:
         raise ValueError("q must be [n_rows, heads, width] and cache [num_pages, 64, width]")
-    if page_table.dim() != 2:
+    if len(table) != 2:
         raise ValueError("page_table must be [num_seqs, max_pages]")
-    return q.shape
+    return rows, pool[0], table
 
 
 def latent_attn_topk(q, cache, page_table, row_seq, topk_idx, scale, workspace, out, lse=None, context_lens=None,
@@ -507,13 +514,14 @@ def latent_attn_topk(q, cache, page_table, row_seq, topk_idx, scale, workspace, 
     """Absorbed latent attention of q [T, H, width] over the tokens that topk_idx [T, k] lists:
     out [T, H, 512] bf16, lse [T, H] fp32 (workspace: latent_attn_workspace_bytes)."""
     dev, on = _here(stream)
-    T, H, width = _latent_shapes(q, cache, page_table)
-    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+    (T, H, width), num_pages, (num_seqs, max_pages) = _latent_shapes(q, cache, page_table)
+    listed = topk_idx.shape
+    if len(listed) != 2 or listed[0] != T:
         raise ValueError("topk_idx must be [n_rows, k]")
     rc = _lib.fp4idx_latent_attn_topk(
-        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), cache.shape[0],
-        _addr(page_table, "page_table", _I32, 0, dev), page_table.shape[0], page_table.shape[1],
-        _addr(row_seq, "row_seq", _I32, T, dev), _addr(topk_idx, "topk_idx", _I32, 0, dev), topk_idx.shape[1],
+        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), num_pages,
+        _addr(page_table, "page_table", _I32, 0, dev), num_seqs, max_pages,
+        _addr(row_seq, "row_seq", _I32, T, dev), _addr(topk_idx, "topk_idx", _I32, 0, dev), listed[1],
         None if context_lens is None else _addr(context_lens, "context_lens", _I32, T, dev), scale,
         _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(),
         _addr(out, "out", _BF16, T * H * LATENT_VALUE, dev),
@@ -527,15 +535,15 @@ def latent_attn(q, cache, page_table, row_seq, context_lens, max_context, scale,
     """Absorbed latent attention of q [T, H, width] over each row's whole context and, with
     tree_mask [T, words] int32, the drafted tokens behind it whose bits are set."""
     dev, on = _here(stream)
-    T, H, width = _latent_shapes(q, cache, page_table)
+    (T, H, width), num_pages, (num_seqs, max_pages) = _latent_shapes(q, cache, page_table)
     words = 0
     if tree_mask is not None:
         if tree_mask.dim() != 2 or tree_mask.shape[0] != T or tree_mask.shape[1] == 0:
             raise ValueError("tree_mask must be [n_rows, words]")
         words = tree_mask.shape[1]
     rc = _lib.fp4idx_latent_attn(
-        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), cache.shape[0],
-        _addr(page_table, "page_table", _I32, 0, dev), page_table.shape[0], page_table.shape[1],
+        _addr(q, "q", _BF16, 0, dev), T, H, width, _addr(cache, "cache", _BF16, 0, dev), num_pages,
+        _addr(page_table, "page_table", _I32, 0, dev), num_seqs, max_pages,
         _addr(row_seq, "row_seq", _I32, T, dev), _addr(context_lens, "context_lens", _I32, T, dev), int(max_context),
         None if tree_mask is None else _addr(tree_mask, "tree_mask", _I32, 0, dev), words, scale,
         _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(),
