@@ -127,7 +127,8 @@ __device__ __forceinline__ void row_span(const LatentArgs& a, int t, int& seq, i
     end = n + extra;
   }
 }
-__device__ __forceinline__ int tiles_of(int end) { return max(1, (end + kTile - 1) / kTile); }  // an empty unit still writes its zeros
+// (an empty unit still writes its zeros)
+__device__ __forceinline__ int tiles_of(int end) { return max(1, (end + kTile - 1) / kTile); }
 
 // The unit that starts at row r0: adjacent rows of one sequence, up to p.group.
 struct Unit {
@@ -499,7 +500,8 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
                                                                                    const __grid_constant__ Params p) {
   using S = Shape<kWidth, kN>;
   constexpr int kStages = S::kStages, kChunks = S::kChunks, kSoft = S::kSoftWarps * 32;
-  constexpr int kScoreWarp = S::kScoreWarp, kOutWarp = S::kOutWarp, kQueryWarp = S::kQueryWarp, kAheadWarp = S::kAheadWarp, kLoadWarp = S::kLoadWarp;
+  constexpr int kScoreWarp = S::kScoreWarp, kOutWarp = S::kOutWarp, kQueryWarp = S::kQueryWarp;
+  constexpr int kAheadWarp = S::kAheadWarp, kLoadWarp = S::kLoadWarp;
   constexpr int kMyCols = kN * 4 / S::kSoftWarps, kJ = kMyCols / 8;  // columns of a softmax warp
   extern __shared__ uint8_t smem_raw[];
   const LatentArgs& a = p.a;
