@@ -464,8 +464,8 @@ int fp4idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int64_
  * RoPE on the last 64 dims, pairs (i, i+32) as in the index keys (width 512: the
  * normalised dims 448..511; width 576: dims 512..575, which are not normalised).  fp32
  * throughout, rounded to bf16 once.
- * Device errors: BAD_PAGE, BAD_POSITION; the row is skipped.  Slots of one call must be
- * distinct.
+ * Device errors: BAD_PAGE, BAD_POSITION; the row is skipped.  TIMEOUT: rows may be missing
+ * from the cache.  Slots of one call must be distinct.
  */
 int fp4idx_store_latent(const uint16_t* kv, int64_t n_rows, int32_t width, const int32_t* positions,
                         const int32_t* slots, const uint16_t* norm_w, float eps, const uint16_t* cos_sin,
@@ -548,7 +548,7 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
                           void* stream);
 
 /*
- * Test support for the bounded waits of the logits and attention kernels (failure
+ * Test support for the bounded waits of the logits, attention and latent store kernels (failure
  * detection), with no counterpart on the pages.  Every wait of such a pipeline gives up after
  * wait_limit_ns (0 restores the default, 2 s): the CTA then records FP4IDX_ERR_TIMEOUT
  * in status_dev, lets the copies it issued land, frees its tensor memory and returns,

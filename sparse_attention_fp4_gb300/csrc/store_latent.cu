@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
     const uint16_t* kv, int64_t n_rows, const int32_t* positions,
     const int32_t* slots, const uint16_t* norm_w, float eps,
     const uint16_t* cos_sin, int32_t max_pos, uint16_t* cache, int64_t num_pages,
-    int32_t* status, uint64_t wait_cycles) {
+    int32_t* status, uint64_t wait_cycles, int32_t idle) {
   using R = Ring<kWidth>;
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
       const int i = __ffs(ahead) - 1;
       ahead &= ahead - 1;
       const int32_t at = __shfl_sync(~0u, pos, i);
-      if (lane == 0) {
+      if (lane == 0 && !idle) {
         const uint32_t bar = bars + (asked % kRing) * 8, dst = ptx::smem_addr(ring) + (asked % kRing) * R::kSlot;
         ptx::mbar_arrive_expect_tx(bar, R::kSlot);
         ptx::bulk_g2s(dst, kv + (n0 + i * step) * kWidth, R::kRow, bar);
@@ -117,8 +117,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) store_latent_kernel(
       const int i = __ffs(left) - 1, s = done % kRing;
       left &= left - 1;
       if (!mma::wait_warp(bars + s * 8, phases >> s & 1, ctl, false)) {
-        // the other copies in flight land before the CTA ends
-        for (int x = done + 1; x < asked; x++) mma::wait_warp(bars + (x % kRing) * 8, phases >> (x % kRing) & 1, ctl, false);
+        // every copy asked for, the late one too, lands before the CTA ends
+        for (int x = done; x < asked && !idle; x++) mma::wait_warp(bars + (x % kRing) * 8, phases >> (x % kRing) & 1, ctl, false);
         return;
       }
       phases ^= 1u << s;
@@ -170,7 +170,7 @@ cudaError_t launch_store_latent(const uint16_t* kv, int64_t n_rows, int32_t widt
   if (e != cudaSuccess) return e;
   const int grid = (int)std::min<int64_t>(fit, (n_rows + kWarps - 1) / kWarps);
   return launch_early(kernel, dim3(grid), kWarps * 32, bytes, 1, stream, kv, n_rows, positions, slots, norm_w, eps, cos_sin,
-                      max_pos, cache, num_pages, status, 2 * pipeline_wait_limit_ns());
+                      max_pos, cache, num_pages, status, 2 * pipeline_wait_limit_ns(), pipeline_idle_producers() ? 1 : 0);
 }
 
 }  // namespace fp4idx
