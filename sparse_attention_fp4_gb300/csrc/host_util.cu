@@ -87,10 +87,6 @@ cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t 
     *out = it->second;
     return cudaSuccess;
   }
-  if (size > 8) {  // above the portable size
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(size, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
@@ -103,7 +99,16 @@ cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  // (eight CTAs are the portable limit)
+  if (size > 8) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+  if (e == cudaErrorInvalidClusterSize || e == cudaErrorInvalidConfiguration || e == cudaErrorInvalidValue ||
+      e == cudaErrorNotSupported) {
+    // a size that this device does not place: none fit, and the caller takes another form
+    cudaGetLastError();
+    e = cudaSuccess;
+    n = 0;
+  }
   if (e != cudaSuccess) return e;
   *out = n;
   known[{kernel, size, dev}] = n;

@@ -7,7 +7,8 @@
 namespace fp4idx {
 
 // How many clusters of `size` CTAs of `threads` threads and `smem` bytes of dynamic shared
-// memory fit on the current device at once, computed once per (kernel, size, device).
+// memory fit on the current device at once (none of a size that it cannot place), computed once
+// per (kernel, size, device).
 cudaError_t resident_clusters(const void* kernel, int size, int threads, size_t smem, int* out);
 
 // A launch, of clusters of `cluster` CTAs along x, that may begin while the one before it on the stream ends: the kernel waits
