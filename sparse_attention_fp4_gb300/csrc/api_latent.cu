@@ -17,12 +17,13 @@ int check_attn(const uint16_t* q, int64_t n_rows, int32_t n_heads, int32_t width
                int64_t num_pages, const int32_t* page_table, int64_t num_seqs, int32_t max_pages,
                const int32_t* row_seq, float scale, const void* workspace, size_t workspace_bytes,
                const uint16_t* out, const float* lse, const int32_t* status) {
-  if (n_rows < 0 || n_heads < 1 || num_pages < 1 || num_seqs < 1 || max_pages < 1) return FP4IDX_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_heads < 1 || num_pages < 0 || num_seqs < 0 || max_pages < 0) return FP4IDX_ERR_INVALID_ARG;
   if (!std::isfinite(scale)) return FP4IDX_ERR_INVALID_ARG;
   if (width != 512 && width != 576) return FP4IDX_ERR_UNSUPPORTED;
   if (n_heads > FP4IDX_LATENT_MAX_HEADS || n_rows > FP4IDX_LATENT_MAX_ROWS) return FP4IDX_ERR_UNSUPPORTED;
   if (num_pages > kMaxPages || max_pages > kMaxPages || num_seqs > INT32_MAX) return FP4IDX_ERR_UNSUPPORTED;
-  if (n_rows == 0) return FP4IDX_OK;
+  if (n_rows == 0) return FP4IDX_OK;  // (a step without a sequence has no table either)
+  if (num_pages < 1 || num_seqs < 1 || max_pages < 1) return FP4IDX_ERR_INVALID_ARG;
   if (!q || !cache || !page_table || !row_seq || !out || !workspace) return FP4IDX_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(workspace)) return FP4IDX_ERR_INVALID_ARG;
   if (!aligned4(page_table) || !aligned4(row_seq) || !aligned4(lse) || !aligned4(status))
