@@ -424,7 +424,7 @@ PREFILL_VALUE = 128
 
 # (torch.cuda.current_device, without its check that CUDA is set up, which any CUDA tensor implies)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _here(stream):
