@@ -440,11 +440,12 @@ int fp4idx_topk_merge(const float* cand_values, const int32_t* cand_idx, int64_t
  * *free_head and cached_lens are not written: the caller adds counts[2] and new_lens
  * when the step is done (a repeated call gives the same result).
  * Sequences are planned in order; the first whose rows, stores or pages do not fit in
- * max_rows, max_stores or the free pages, and all behind it, get no rows, pages or
- * context (CAPACITY).  A sequence with a negative length, or more entries than
- * 64*max_pages, gets none either (BAD_LENGTH); those behind it are planned.  An entry
- * whose page id is negative or above 2^25-1 gets slot -1 (BAD_PAGE).  The outputs must
- * not overlap one another or the inputs.  All pointers 4-byte aligned.
+ * max_rows, max_stores or the free pages, or with whom cu_context would pass 2^31-1, and
+ * all behind it, get no rows, pages or context (CAPACITY).  A sequence with a negative
+ * length, or more entries than 64*max_pages, gets none either (BAD_LENGTH); those behind
+ * it are planned.  An entry whose page id is negative or above 2^25-1 gets slot -1
+ * (BAD_PAGE).  The outputs must not overlap one another or the inputs.  All pointers
+ * 4-byte aligned.
  */
 int fp4idx_plan_step(const int32_t* cached_lens, const int32_t* new_lens, int64_t n_seqs, int32_t ratio,
                      const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* page_table,
