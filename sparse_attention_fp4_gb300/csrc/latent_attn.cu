@@ -172,8 +172,9 @@ struct Feed {
   uint32_t* asked;  // segments asked for
   Ctl ctl;
 };
-template <bool kSelected>
+template <bool kSelected, bool kShared>
 __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& feed, bool report = false) {
+  if (kShared) return false;  // one segment a unit
   if (kSelected && p.whole) {
     const uint32_t n = ++s.n;
     uint32_t u = kNoUnit;
@@ -321,10 +322,10 @@ __device__ __forceinline__ Weight unit_weight(const Params& p, int base, int& ru
   run = last;
   return got;
 }
-template <bool kSelected>
+template <bool kSelected, bool kShared>
 __device__ __forceinline__ bool first_seg(const Params& p, Seg& s, ScanShared& sh, int& u) {
   const int n = p.a.n_rows, step = blockDim.x;
-  if (p.cluster) {
+  if (kShared) {
     const int j = blockIdx.x & (p.cluster - 1);
     int row = u / p.hb;
     s.hb = u % p.hb;
@@ -494,7 +495,10 @@ struct Shape {
 };
 // The scan's scratch lies in the query buffer, which is not in use yet.
 
-template <int kWidth, int kN, bool kSelected>
+// kShared: a cluster or a CTA a unit, joined here.  (A kernel of its own: with both forms in one, one
+// long sequence took 48.4 us instead of 47.4, trees of 13 drafts 132.8 instead of 130.5, a batch of
+// whole contexts 129.7 instead of 127.7, one selected row 12.3 instead of 11.6.)
+template <int kWidth, int kN, bool kSelected, bool kShared>
 __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_kernel(const __grid_constant__ CUtensorMap cache_map,
                                                                                    const __grid_constant__ CUtensorMap q_map,
                                                                                    const __grid_constant__ Params p) {
@@ -556,14 +560,15 @@ __global__ void __launch_bounds__(Shape<kWidth, kN>::kThreads, 1) latent_attn_ke
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int unit = p.cluster ? (int)blockIdx.x >> (__ffs(p.cluster) - 1) : -1;
+  const int cluster = kShared ? p.cluster : 0;
+  int unit = kShared ? (int)blockIdx.x >> (__ffs(cluster) - 1) : -1;
   bool gave_up = false;
 again:  // (clusters take unit after unit if a call has more than the host counts on)
   Seg seg;
   seg.n = 0;
-  const bool any = first_seg<kSelected>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ), unit) && !gave_up;
+  const bool any = first_seg<kSelected, kShared>(p, seg, *reinterpret_cast<ScanShared*>(smem + S::kOffQ), unit) && !gave_up;
   Work wk = work_view(a.workspace);
-  if (threadIdx.x == 0 && !p.cluster) {
+  if (threadIdx.x == 0 && !kShared) {
     wk.rec[2 * blockIdx.x] = Record{0, 0, 0, 0};
     wk.rec[2 * blockIdx.x + 1] = Record{0, 0, 0, 0};
   }
@@ -590,7 +595,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
       t += n;
       while (t >= seg.t1) {
         n = t - seg.t1;
-        if (!next_seg<kSelected>(p, seg, feed)) {
+        if (!next_seg<kSelected, kShared>(p, seg, feed)) {
           have = false;
           return;
         }
@@ -756,7 +761,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
       mma::cp_async_wait_all();
       ptx::fence_proxy_async_smem();
       arrive_warp(qfull, lane);
-    } while (next_seg<kSelected>(p, seg, feed, true));
+    } while (next_seg<kSelected, kShared>(p, seg, feed, true));
     if (p.q_boxes && ictr > 0) mma::wait_warp(qfull, (ictr - 1) & 1, ctl, false);  // lands before the CTA ends
   } else if (any && warp == kAheadWarp) {
     // ------------------------------------------------------------ prefetches (two tokens a lane)
@@ -790,7 +795,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
           }
         }
       }
-    } while (on && next_seg<kSelected>(p, seg, feed));
+    } while (on && next_seg<kSelected, kShared>(p, seg, feed));
   } else if (any && warp == kScoreWarp) {
     // ------------------------------------------------------------ the first product (the warp as one)
     constexpr uint32_t kIdS = mma::idesc_bf16(64, kN, false, false);
@@ -839,7 +844,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
           phase ^= 1;
         }
       }
-    } while (ok && next_seg<kSelected>(p, seg, feed));
+    } while (ok && next_seg<kSelected, kShared>(p, seg, feed));
     // nothing of this CTA's may be under way in the tensor cores when it ends
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
@@ -872,7 +877,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
         __syncwarp();
         if (++stage == kStages) stage = 0;
       }
-    } while (ok && next_seg<kSelected>(p, seg, feed));
+    } while (ok && next_seg<kSelected, kShared>(p, seg, feed));
     if (mma::elect_one()) ptx::mma_commit(done);
     __syncwarp();
     mma::wait_warp(done, 0, ctl, false);
@@ -1059,9 +1064,9 @@ again:  // (clusters take unit after unit if a call has more than the host count
       if (threadIdx.x < kN) {
         const int c = threadIdx.x;
         const float total = red[c] + red[kN + c] + red[2 * kN + c] + red[3 * kN + c];
-        if (p.cluster > 1) {
+        if (cluster > 1) {
           sm_f[c] = total;
-        } else if (whole) {
+        } else if (kShared || whole) {
           sm_f[c] = total == 0.f ? 0.f : 1.f / total;
           const int r = c / p.hp, h = c % p.hp, head = seg.hb * p.hs + h;
           if (a.lse && r < seg.u.rows && h < p.hs && head < a.heads)
@@ -1072,15 +1077,15 @@ again:  // (clusters take unit after unit if a call has more than the host count
           wk.ml[slot * 2 * kCols + kCols + c] = total;
         }
       }
-      if (!whole && p.cluster <= 1 && threadIdx.x == 0)
+      if (!kShared && !whole && threadIdx.x == 0)
         wk.rec[slot] = Record{seg.u.r0, seg.u.rows, seg.hb, kUsed | (begins ? kBegins : 0) | (ends ? kEnds : 0)};
       const uint32_t last = kctr - 1;
       ok = mma::wait_warp(kempty(last % kStages, 1), (last / kStages) & 1, ctl);
       if (mma::bar_any(1, kSoft, !ok)) break;
-      if (p.cluster > 1) break;  // the one piece: joined below
+      if (cluster > 1) break;  // the one piece: joined below
       ptx::tc_fence_after();
       // lane = dim, columns = heads: a warp writes 32 dims of one head at a time
-      if (whole) {
+      if (kShared || whole) {
 #pragma unroll 1
         for (int r = 0; r < seg.u.rows; r++) {
           const int head0 = seg.hb * p.hs, heads = min(p.hs, a.heads - head0);
@@ -1116,16 +1121,16 @@ again:  // (clusters take unit after unit if a call has more than the host count
       }
       ptx::tc_fence_before();
       ptx::named_bar_sync(1, kSoft);  // red, sm_m and sm_f are free again
-    } while (next_seg<kSelected>(p, seg, feed));
+    } while (next_seg<kSelected, kShared>(p, seg, feed));
   }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (p.cluster > 1) {
+  if (cluster > 1) {
     // ---- the cluster's pieces are joined: each CTA for its share of the columns
     // All main loops are over, so shared memory is free: pieces of the CTA's columns at 0,
     // [piece][column][512] fp32, every piece's m and l in the query buffer.
-    const int ctas = p.cluster, mine = blockIdx.x & (ctas - 1);  // two, four or eight
+    const int ctas = cluster, mine = blockIdx.x & (ctas - 1);  // two, four, eight or sixteen
     const int share = kN / ctas, shift = __ffs(share) - 1;
     float* gather = reinterpret_cast<float*>(smem + S::kOffQ);  // [piece][2][kN]
     float* sm_m = reinterpret_cast<float*>(smem + S::kOffM);
@@ -1192,7 +1197,7 @@ again:  // (clusters take unit after unit if a call has more than the host count
     __syncthreads();
     ptx::tc_fence_after();
   }
-  if (p.cluster && unit >= 0) {
+  if (kShared && unit >= 0) {
     gave_up = *abort_flag;  // (the cluster's other CTAs count on this one until the end)
     if (threadIdx.x == 0) {
       for (int i = 0; i < S::kBars; i++) mma::mbar_inval(bar(i));
@@ -1335,14 +1340,16 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   static_assert(S::kThreads <= kMaxWarps * 32, "");
   static_assert(kN * kValue * 4 <= S::kOffQ, "a cluster's pieces fit the stages");
   static_assert(sizeof(ScanShared) <= S::kChunks * S::kQChunk, "the scan's scratch fits the query buffer");
-  const void* kernel = reinterpret_cast<const void*>(latent_attn_kernel<kWidth, kN, kSelected>);
+  const auto cut_kernel = latent_attn_kernel<kWidth, kN, kSelected, false>;
+  const auto shared_kernel = latent_attn_kernel<kWidth, kN, kSelected, true>;
   // (a map that the kernel will not use is not encoded)
   CUtensorMap cache_map{}, q_map{};
   p.q_boxes = p.group == 1 || p.hp == p.a.heads;
   if ((!kSelected && !encode_rows_of(&cache_map, p.a.cache, (int64_t)p.a.num_pages * kPage, kWidth, kPage)) ||
       (p.q_boxes && !encode_rows_of(&q_map, p.a.q, (int64_t)p.a.n_rows * p.a.heads, kWidth, kN)))
     return cudaErrorInvalidValue;
-  cudaError_t e = set_smem_attr_once(kernel, S::kBytes);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(cut_kernel), S::kBytes);
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(shared_kernel), S::kBytes);
   if (e != cudaSuccess) return e;
   // Both launches may begin while the one before them ends: each waits for it before its
   // first access to global memory.
@@ -1369,7 +1376,7 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
     if (c > 1 && (c >= 2 * tiles || (c == 16 && tiles <= 8 * 3))) continue;  // as fast with half as many
     if (c > 1) {
       int fit = 0;
-      e = resident_clusters(kernel, c, S::kThreads, S::kBytes, &fit);
+      e = resident_clusters(reinterpret_cast<const void*>(shared_kernel), c, S::kThreads, S::kBytes, &fit);
       if (e != cudaSuccess) return e;
       if (fit < units) continue;
       attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -1380,14 +1387,14 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
     }
     p.cluster = c;
     cfg.gridDim = dim3(units * c, 1, 1);
-    return cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
+    return cudaLaunchKernelEx(&cfg, shared_kernel, cache_map, q_map, p);
   }
   if (p.whole) {
     e = cudaMemsetAsync(work_view(p.a.workspace).taken, 0, sizeof(uint32_t), stream);
     if (e != cudaSuccess) return e;
     cfg.numAttrs = 0;  // the launch before is not a kernel's
   }
-  e = cudaLaunchKernelEx(&cfg, latent_attn_kernel<kWidth, kN, kSelected>, cache_map, q_map, p);
+  e = cudaLaunchKernelEx(&cfg, cut_kernel, cache_map, q_map, p);
   if (e != cudaSuccess || !may_split) return e;
   const int cut = std::min(ctas, p.a.n_rows * p.hb);  // units in pieces, at most
   const bool many = cut * 8 <= ctas;  // eight pieces a unit or more
