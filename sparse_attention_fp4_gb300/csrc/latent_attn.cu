@@ -30,19 +30,19 @@
 //
 // What bounds it, at the sizes measured (a plain copy reaches 6.8 TB/s):
 //   whole contexts, 16 heads, width 576   HBM: 64 sequences of up to 16,384 tokens, 673 MB in
-//               129 us, 5.2 TB/s
+//               128 us, 5.3 TB/s
 //   64 columns (selections with 64 heads, trees)   shared memory: a tile takes 2,650 cycles, of
 //               which 2,500 are its operands' bytes at 128 a cycle: keys and queries for the
 //               scores (M = 64 re-reads the queries every tile) 1,152, values and four times the
 //               weights 768, the tile's arrival 576.  1,536 selections of 2,048 tokens, 64 heads,
-//               width 576: 493 us
+//               width 576: 496 to 507 us
 //   few rows    latency: launch, lengths, list, pages and tokens are dependent reads, some 8 us;
-//               one row of 64 heads over 512 tokens 12 to 13 us
+//               one row of 64 heads over 512 tokens 11.7 us
 //
 // The reference m of a column is not its running maximum: it is only raised when a score
 // passes it by more than 8 (in powers of two), so that in nearly all tiles the output in
 // tensor memory needs no rescaling and the warps exchange one vote.  The result does not
-// depend on m; weights stay below 2^8.
+// depend on m, up to rounding; weights stay below 2^8.
 #include <algorithm>
 #include <cmath>
 
@@ -233,7 +233,7 @@ __device__ __forceinline__ bool next_seg(const Params& p, Seg& s, const Feed& fe
 // More units, of rows with a selection each: the CTAs take whole units in order, each the next
 // one when it needs one.  No pieces, and the rows of one sequence, whose selections overlap,
 // are read at the same time (L2 then holds what they share).  1,488 units of 2,048 tokens: 655
-// us by an even cut, 491 so; 360 of 500 tokens and two head blocks 106 and 83; 384 of 2,048
+// us by an even cut, 496 so; 360 of 500 tokens and two head blocks 106 and 83; 384 of 2,048
 // 162 and 149.  With less than two units a CTA only where the last round adds at most kMore
 // tiles (235 of 1,667: 92 us either way).
 // Otherwise the list of tiles is cut evenly, a unit's end counting as kEnd tiles (without that, a
@@ -1352,7 +1352,7 @@ cudaError_t launch(Params p, int ctas, bool may_split, cudaStream_t stream) {
   if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(shared_kernel), S::kBytes);
   if (e != cudaSuccess) return e;
   // Both launches may begin while the one before them ends: each waits for it before its
-  // first access to global memory.
+  // first load or store (only prefetches into L2 come earlier).
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -12,8 +12,9 @@
 // both tiles' scores are done at once, and the tensor cores then wait for both softmaxes:
 // 1.06 ms instead of 0.85 for prompts of 6,000 and 4,000 tokens with 64 heads.)
 // Bound by the tensor cores and the shared memory that feeds them: a step of 112 tokens takes
-// 2,900 cycles, its MMAs alone (two tiles, measured apart) 2,400; 1.43 PFLOP/s over those
-// prompts (750 us), of which 2,400 CTAs' set-up and output cost a seventh.
+// 2,900 cycles, its MMAs alone (two tiles, measured apart) 2,400; 1.34 PFLOP/s over those
+// prompts (795 us with changing inputs among other work, 750 us repeated by themselves), of which
+// 2,560 CTAs' set-up and output cost a seventh.
 //   warps 0-7, 8-15 softmax and output of tile 0, 1: two threads a row, 56 columns each
 //   warps 16, 17    issue the MMAs of tile 0, 1
 //   warp 18         issues the TMA loads into a ring of nine 14 KB blocks (112 tokens x 64
@@ -21,7 +22,7 @@
 //                   room for eight: two of a step's five blocks then come when they are
 //                   needed, not before (800 us)
 // m is raised only when the weights of a row's half tile sum to more than 2^16, so O is hardly
-// ever rescaled and no maximum is taken after the first tile; the result does not depend on m.
+// ever rescaled and no maximum is taken after the first tile; the result depends on m by rounding only.
 // Queries of longer contexts have smaller block indices: the longest work starts first.
 //
 // Where all blocks together are few, a cluster of two, four or eight CTAs takes a block, each a
@@ -46,7 +47,7 @@ constexpr int kRing = 9;
 constexpr uint32_t kQBlock = kRows * 128, kBlock = kTokens * 128;  // bytes: rows of 64 bf16
 constexpr uint32_t kOffRing = 6 * kQBlock;  // behind the two query tiles
 constexpr uint32_t kOffBar = kOffRing + kRing * kBlock;
-// full[8], empty[8], qfull[2], sfull[2], pfull[2], ofull[2], done, tail, issued[2]
+// full[9], empty[9], qfull[2], sfull[2], pfull[2], ofull[2], done, tail, issued[2]
 constexpr int kBars = 2 * kRing + 12;
 constexpr uint32_t kOffMisc = kOffBar + kBars * 8;
 constexpr uint32_t kOffRed = kOffMisc + 16;  // [tile][half][row] floats
