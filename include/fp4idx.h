@@ -14,7 +14,9 @@
  * then a per-row top-k of compressed-token indices, ascending.
  * Around the indexer: the step's maps built on the device (fp4idx_plan_step), and the cache
  * and attention that the selection is for (fp4idx_store_latent, fp4idx_latent_attn_topk,
- * fp4idx_latent_attn, fp4idx_latent_prefill).
+ * fp4idx_latent_attn, fp4idx_latent_prefill).  For requests decoded as several hypotheses:
+ * the choice of the hypotheses that go on (fp4idx_beam_select), and the page pool's care
+ * (fp4idx_fork_pages, fp4idx_copy_pages, fp4idx_compact_pages).
  *
  * Conventions for every entry point
  *   - Pointers are DEVICE pointers (cudaMalloc / torch CUDA memory on the current
@@ -70,6 +72,13 @@ extern "C" {
 #define FP4IDX_LATENT_MAX_TREE_WORDS 8 /* 256 drafted tokens a sequence */
 #define FP4IDX_PREFILL_KEY 192   /* expanded attention: 128 dims of the head's own key, 64 shared rotated dims */
 #define FP4IDX_PREFILL_VALUE 128
+#define FP4IDX_BEAM_MAX_BEAMS 64
+#define FP4IDX_BEAM_MAX_K 64
+#define FP4IDX_BEAM_MAX_VOCAB (1 << 19)
+#define FP4IDX_BEAM_MAX_ROWS (1 << 20)
+#define FP4IDX_FORK_MAX_ROWS 16384          /* rows of a page table, old and new */
+#define FP4IDX_MAX_POOL_PAGES (1 << 23)     /* fork and compaction: pages of a pool */
+#define FP4IDX_COPY_MAX_REGIONS 256         /* caches of one fp4idx_copy_pages call */
 #define FP4IDX_TOPK_NOALLOC_MAX_BYTES (16u * 1024u * 1024u) /* fixed scratch of fp4idx_topk_noalloc */
 
 typedef enum {
@@ -85,7 +94,9 @@ typedef enum {
   FP4IDX_ERR_SCHEDULE = 9,     /* schedule built for another row count or grid, or its selection
                                   counters were left non-zero by a call that failed: rebuild it */
   FP4IDX_ERR_SCRATCH_LIMIT = 10, /* fp4idx_topk_noalloc: the call needs more than its fixed scratch */
-  FP4IDX_ERR_CAPACITY = 11       /* device: fp4idx_plan_step ran out of rows, stores or free pages */
+  FP4IDX_ERR_CAPACITY = 11,      /* device: a plan or a fork ran out of rows, stores or free pages, or a free
+                                    list of room */
+  FP4IDX_ERR_BAD_VALUE = 12      /* device: fp4idx_beam_select met a NaN or +inf */
 } fp4idx_status;
 
 /* Human-readable name of a status code (static string). */
@@ -547,6 +558,134 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
                           const uint16_t* k_rope, const int32_t* cu_q, const int32_t* cu_kv, int64_t n_seqs,
                           int32_t max_q, int32_t max_kv, float scale, uint16_t* out, float* lse, int32_t* status_dev,
                           void* stream);
+
+/*
+ * Beam selection -- the hypotheses of a request that go on, over its beams and the
+ * vocabulary.  The pages stop at the attention; this and the page operators below are
+ * interface additions for requests that are decoded as several hypotheses.
+ * Rows g*n_beams .. g*n_beams + n_beams - 1 are the beams of group (request) g:
+ *   total[r,v] = scores[r] + (logits[r,v] - log sum_u exp(logits[r,u]))
+ * and a finished row (done[r] != 0) has the one candidate (end_token, scores[r]); its
+ * logits are not read.  Per group the k largest totals, in descending order; equal totals:
+ * the lower row, then the larger logit, then the lower token.
+ *   logits      [n_rows, vocab] of type logits_type (0 bf16, 1 fp16, 2 fp32), row r at
+ *               element r*logits_stride; aligned to its element type; a token is ruled out
+ *               by -inf
+ *   scores      [n_rows] fp32, the rows' scores so far; -inf: the row is dead (no
+ *               candidate, its logits are not read)
+ *   n_rows a multiple of n_beams, n_beams 1..64, k 1..64, vocab 1..2^19
+ *   done        [n_rows] int32, nullable (with it, end_token is a token of the vocabulary)
+ *   end_token   -1: none
+ *   out_scores, out_rows, out_tokens [n_rows/n_beams, k] (written): total (fp32), row (of
+ *               all n_rows: the parents of fp4idx_fork_pages) and token; -inf, -1 and -1
+ *               where a group has no candidate left
+ *   done_out    [n_rows/n_beams, k] int32, nullable (written): 1 where the row was finished
+ *               or the token is end_token, else 0
+ * Sums are fp32 within 16,384 tokens and fp64 above; totals are compared in fp64, so that
+ * totals of different rows closer than about 1e-7 may change places.  A row whose scores or
+ * logits hold a NaN or +inf has no candidate (BAD_VALUE).  The outputs must not overlap one
+ * another or the inputs.  workspace: fp4idx_beam_select_workspace_bytes(n_rows, vocab, k)
+ * bytes, 16-byte aligned, nothing in it needs to be initialised; calls that may overlap need
+ * one each.
+ */
+size_t fp4idx_beam_select_workspace_bytes(int64_t max_rows, int32_t vocab, int32_t k);
+int fp4idx_beam_select(const void* logits, int32_t logits_type, int64_t logits_stride, int32_t vocab,
+                       const float* scores, int64_t n_rows, int32_t n_beams, int32_t k, const int32_t* done,
+                       int32_t end_token, void* workspace, size_t workspace_bytes, float* out_scores,
+                       int32_t* out_rows, int32_t* out_tokens, int32_t* done_out, int32_t* status_dev, void* stream);
+
+/*
+ * Fork of page tables -- the rows of a batch go on as other rows (the beams that were
+ * chosen, a prompt that becomes several samples, a batch without its ended sequences),
+ * and the pages that no row holds any more go back to the free list of fp4idx_plan_step.
+ * Row r of the old table holds ceil(e/64) pages, e = floor(cached_lens[r] / ratio) entries.
+ * Row i of the new table goes on from row parents[i] (-1: it is empty):
+ *   - it shares all of that row's full pages;
+ *   - of the rows that go on from one parent, the first keeps the page that is only partly
+ *     filled (unless it is pinned); each other one gets a page of its own, listed in
+ *     copy_src / copy_dst: copy these (fp4idx_copy_pages) before the next store.
+ * Pages that were held by rows from which none goes on, and by none of the others, and are
+ * not pinned, come back, in ascending order.  The first of them serve as the new pages of
+ * this call; what is missing is taken from free_pages at *free_head on, what is left over
+ * is written just below *free_head.
+ *   page_table  [n_old, max_pages] int32, cached_lens [n_old] int32, ratio 1..64
+ *   parents     [n_new] int32;  n_old, n_new <= 16384
+ *   num_pages   pages of the pool (1..2^23); ids of the table and the list lie below it
+ *   pinned      [ceil(num_pages/32)] uint32 bit patterns, nullable: bit p % 32 of word p / 32
+ *               is set for a page that something else holds too (a prefix cache); it is
+ *               neither freed nor written to
+ *   free_pages  [n_free] int32 (read from *free_head on, written below), free_head: device
+ *               int32, nullable = 0; n_free may be 0
+ *   page_table_out [n_new, max_pages] (written; -1 behind a row's pages), cached_out [n_new]
+ *               (written), copy_src, copy_dst [n_new] (written; -1 behind the last copy)
+ *   counts [4]  (written): copies, pages that came back, the change of *free_head (new
+ *               pages minus pages that came back), rows that go on
+ * *free_head is not written: the caller adds counts[2] (a repeated call gives the same
+ * result).  A page that is partly filled must be held by no other row (rows that the step
+ * plan and this call built are so); such rows may share full pages in any way.
+ * The first row whose new page is not in the list, and all behind it that need one, are
+ * left empty; if the pages that came back do not fit below *free_head, the lowest of those
+ * left over are not listed; if *free_head is outside [0, n_free], none is taken or listed
+ * (each CAPACITY; pages lost to the list come back with fp4idx_compact_pages).  A parent
+ * outside [-1, n_old) (BAD_PAGE), and one whose length is negative or needs more than
+ * max_pages pages (BAD_LENGTH), leave their rows empty; such a parent's pages do not come
+ * back.  An id outside [0, num_pages) is handed on as it is and never comes back, a partly
+ * filled page with such an id is not copied (BAD_PAGE).  The outputs must not overlap one
+ * another or the inputs (page_table_out and cached_out are buffers of their own).
+ */
+int fp4idx_fork_pages(const int32_t* page_table, const int32_t* cached_lens, int64_t n_old, int32_t max_pages,
+                      int32_t ratio, const int32_t* parents, int64_t n_new, int64_t num_pages, const uint32_t* pinned,
+                      int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* page_table_out,
+                      int32_t* cached_out, int32_t* copy_src, int32_t* copy_dst, int32_t* counts, int32_t* status_dev,
+                      void* stream);
+
+/*
+ * Copies of whole pages, in several caches at once -- the page src[i] of each cache is
+ * copied over its page dst[i].
+ *   src, dst    [n_copies] int32; a pair with a negative id is padding
+ *   count       device int32, nullable: only the first *count pairs are read (counts of
+ *               fp4idx_fork_pages and fp4idx_compact_pages)
+ *   regions     host array of n_regions (0..256) device pointers, page_bytes host array of the
+ *               bytes of a page in each (a multiple of 16, at most 2^30): page p of region c at byte
+ *               p*page_bytes[c].  16-byte aligned; read before the call returns.
+ *   num_pages   pages in every region (0..2^31-1); a pair with an id from num_pages on is
+ *               skipped (BAD_PAGE)
+ * No page may be both a source and a destination of one call, or a destination twice
+ * (a page copied onto itself stays as it is).
+ */
+int fp4idx_copy_pages(const int32_t* src, const int32_t* dst, int64_t n_copies, const int32_t* count,
+                      void* const* regions, const int64_t* page_bytes, int32_t n_regions, int64_t num_pages,
+                      int32_t* status_dev, void* stream);
+
+/*
+ * Compaction of a page pool -- the pages in use (held by a row, or pinned) move to the
+ * lowest ids, so that the end of the pool can be given away, and the free list is rebuilt
+ * from what is in use.  n pages are in use: the i-th page from id n on that is held and not
+ * pinned moves to the i-th id below n that is not in use (ascending), for the first
+ * max_moves of them.
+ *   page_table [n_seqs, max_pages], cached_lens [n_seqs], ratio, num_pages, pinned as
+ *              fp4idx_fork_pages; n_seqs <= 65536.  A pinned page keeps its id.
+ *   page_table_out [n_seqs, max_pages] (written): the table after the moves, -1 behind a
+ *              row's pages
+ *   move_src, move_dst [max_moves] int32 (written; -1 behind the last move): copy these
+ *              pages (fp4idx_copy_pages) before the next store or read of the cache
+ *   free_pages [n_free] int32 (written from index counts[3] on): the ids not in use after
+ *              the moves, ascending, at the end of the buffer
+ *   counts [4] (written): moves, pages in use, the highest id in use after the moves + 1, the
+ *              index of the first free id in free_pages (the new *free_head)
+ * Where n_free is less than the ids that are free, the highest n_free of them are listed
+ * (CAPACITY).  A row with a negative length or one that needs more than max_pages pages
+ * gets an empty table row, and holds nothing (BAD_LENGTH); an id outside [0, num_pages) is
+ * handed on as it is (BAD_PAGE).  workspace: fp4idx_compact_pages_workspace_bytes(num_pages)
+ * bytes, 16-byte aligned, nothing in it needs to be initialised; calls that may overlap need
+ * one each.  The outputs must not overlap one another or the inputs.
+ */
+size_t fp4idx_compact_pages_workspace_bytes(int64_t num_pages);
+int fp4idx_compact_pages(const int32_t* page_table, const int32_t* cached_lens, int64_t n_seqs, int32_t max_pages,
+                         int32_t ratio, int64_t num_pages, const uint32_t* pinned, void* workspace,
+                         size_t workspace_bytes, int32_t* free_pages, int64_t n_free, int32_t* page_table_out,
+                         int32_t* move_src, int32_t* move_dst, int64_t max_moves, int32_t* counts, int32_t* status_dev,
+                         void* stream);
 
 /*
  * Test support for the bounded waits of the logits, attention and latent store kernels (failure

@@ -45,6 +45,7 @@ const char* fp4idx_status_string(int status) {
     case FP4IDX_ERR_SCHEDULE: return "schedule does not match the call";
     case FP4IDX_ERR_SCRATCH_LIMIT: return "call needs more than the fixed top-k scratch";
     case FP4IDX_ERR_CAPACITY: return "plan ran out of rows, stores or free pages";
+    case FP4IDX_ERR_BAD_VALUE: return "a score or logit is NaN or +inf";
     default: return "unknown status";
   }
 }

@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,6 +30,7 @@ STATUS = {
     5: "page id or slot outside the cache", 6: "pipeline wait timed out", 7: "RoPE position outside the table",
     8: "context length out of range", 9: "schedule does not match the call",
     10: "call needs more than the fixed top-k scratch", 11: "plan ran out of rows, stores or free pages",
+    12: "a score or logit is NaN or +inf",
 }
 
 
@@ -93,6 +95,15 @@ _SIGS = {
                                           _f32, _vp, _sz, _vp, _vp, _vp, _vp]),
     "fp4idx_latent_prefill": (ctypes.c_int, [_vp, _i64, _i32, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i32, _f32, _vp,
                                              _vp, _vp, _vp]),
+    "fp4idx_beam_select_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "fp4idx_beam_select": (ctypes.c_int, [_vp, _i32, _i64, _i32, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _sz, _vp, _vp, _vp,
+                                          _vp, _vp, _vp]),
+    "fp4idx_fork_pages": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp]),
+    "fp4idx_copy_pages": (ctypes.c_int, [_vp, _vp, _i64, _vp, _vp, _vp, _i32, _i64, _vp, _vp]),
+    "fp4idx_compact_pages_workspace_bytes": (_sz, [_i64]),
+    "fp4idx_compact_pages": (ctypes.c_int, [_vp, _vp, _i64, _i32, _i32, _i64, _vp, _vp, _sz, _vp, _i64, _vp, _vp, _vp,
+                                            _i64, _vp, _vp, _vp]),
     "fp4idx_test_pipeline_waits": (ctypes.c_int, [_i32, _i64]),
     "fp4idx_read_status": (ctypes.c_int, [_vp, ctypes.POINTER(_i32), _vp]),
 }
@@ -573,6 +584,107 @@ def latent_prefill(q, kv, k_rope, cu_q, cu_kv, max_q, max_kv, scale, out, lse=No
         None if lse is None else _addr(lse, "lse", _F32, n_q * H, dev),
         None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_latent_prefill", rc)
+
+
+# ------------------------------------------------------------------ several hypotheses a request
+_LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def beam_select_workspace_bytes(max_rows, vocab, k) -> int:
+    return int(_lib.fp4idx_beam_select_workspace_bytes(max_rows, vocab, k))
+
+
+def beam_select(logits, scores, n_beams, k, workspace, out_scores, out_rows, out_tokens, done=None, end_token=-1,
+                done_out=None, status=None, stream=None):
+    """The k best continuations of each group of n_beams rows: logits [n_rows, vocab] (bf16, fp16 or
+    fp32; rows may lie apart, a row's logits together), scores [n_rows] fp32; out_scores, out_rows
+    and out_tokens [n_rows / n_beams, k] (fp4idx_beam_select)."""
+    dev, on = _here(stream)
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.get_device() != dev or logits.dtype not in _LOGITS:
+        raise ValueError("logits must be [n_rows, vocab] bf16, fp16 or fp32 on the current device")
+    T, V = logits.shape
+    stride, inner = logits.stride()
+    if T <= 1:
+        stride = max(V, 1)  # (of a dimension of one, any stride will do)
+    if (inner != 1 and V > 1) or stride < V:
+        raise ValueError("each row of logits must be contiguous, and rows must not overlap")
+    n = T // n_beams * k if n_beams > 0 else 0
+    rc = _lib.fp4idx_beam_select(
+        logits.data_ptr(), _LOGITS[logits.dtype], stride, V, _addr(scores, "scores", _F32, T, dev), T, n_beams, k,
+        None if done is None else _addr(done, "done", _I32, T, dev), end_token,
+        _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(), _addr(out_scores, "out_scores", _F32, n, dev),
+        _addr(out_rows, "out_rows", _I32, n, dev), _addr(out_tokens, "out_tokens", _I32, n, dev),
+        None if done_out is None else _addr(done_out, "done_out", _I32, n, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
+    _check("fp4idx_beam_select", rc)
+
+
+def _pinned(pinned, num_pages, dev):
+    return None if pinned is None else _addr(pinned, "pinned", _I32, (num_pages + 31) // 32, dev)
+
+
+def fork_pages(page_table, cached_lens, ratio, parents, num_pages, free_pages, page_table_out, cached_out, copy_src,
+               copy_dst, counts, free_head=None, pinned=None, status=None, stream=None):
+    """Row i of the new table goes on from row parents[i] of the old one (-1: empty): full pages
+    shared, partly filled ones listed for copy_pages, pages that nobody holds any more back on
+    the free list (fp4idx_fork_pages)."""
+    dev, on = _here(stream)
+    if page_table.dim() != 2 or page_table_out.dim() != 2 or page_table_out.shape[1] != page_table.shape[1]:
+        raise ValueError("page_table and page_table_out must be [rows, max_pages]")
+    (A, most), B = page_table.shape, parents.numel()
+    if page_table_out.shape[0] != B:
+        raise ValueError("page_table_out must have %d rows" % B)
+    rc = _lib.fp4idx_fork_pages(
+        _addr(page_table, "page_table", _I32, 0, dev), _addr(cached_lens, "cached_lens", _I32, A, dev), A, most, ratio,
+        _addr(parents, "parents", _I32, 0, dev), B, num_pages, _pinned(pinned, num_pages, dev),
+        _addr(free_pages, "free_pages", _I32, 0, dev), free_pages.numel(),
+        None if free_head is None else _addr(free_head, "free_head", _I32, 1, dev),
+        _addr(page_table_out, "page_table_out", _I32, 0, dev), _addr(cached_out, "cached_out", _I32, B, dev),
+        _addr(copy_src, "copy_src", _I32, B, dev), _addr(copy_dst, "copy_dst", _I32, B, dev),
+        _addr(counts, "counts", _I32, 4, dev), None if status is None else _addr(status, "status", _I32, 1, dev), on)
+    _check("fp4idx_fork_pages", rc)
+
+
+def copy_pages(src, dst, caches, count=None, status=None, stream=None):
+    """Page src[i] of every tensor of `caches` (each [num_pages, ...], of any type) is copied over its page
+    dst[i]; with `count` (device int32) only the first count[0] pairs (fp4idx_copy_pages)."""
+    dev, on = _here(stream)
+    n, m = src.numel(), len(caches)
+    pages = caches[0].shape[0] if m else 0
+    base, size = (_vp * m)(), (_i64 * m)()
+    for i, c in enumerate(caches):
+        if c.get_device() != dev or not c.is_contiguous() or c.dim() < 1 or c.shape[0] != pages:
+            raise ValueError("caches must be contiguous CUDA tensors on the current device, of one number of pages")
+        base[i] = c.data_ptr()
+        size[i] = math.prod(c.shape[1:]) * c.element_size()
+    rc = _lib.fp4idx_copy_pages(
+        _addr(src, "src", _I32, 0, dev), _addr(dst, "dst", _I32, n, dev), n,
+        None if count is None else _addr(count, "count", _I32, 1, dev), base, size, m, pages,
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
+    _check("fp4idx_copy_pages", rc)
+
+
+def compact_pages_workspace_bytes(num_pages) -> int:
+    return int(_lib.fp4idx_compact_pages_workspace_bytes(num_pages))
+
+
+def compact_pages(page_table, cached_lens, ratio, num_pages, workspace, free_pages, page_table_out, move_src, move_dst,
+                  counts, pinned=None, status=None, stream=None):
+    """The pages in use move to the lowest ids, at most move_src.numel() of them: the new table, the
+    moves for copy_pages, and the free list rebuilt (fp4idx_compact_pages)."""
+    dev, on = _here(stream)
+    if page_table.dim() != 2 or page_table_out.shape != page_table.shape:
+        raise ValueError("page_table and page_table_out must be [n_seqs, max_pages]")
+    B, most = page_table.shape
+    moves = move_src.numel()
+    rc = _lib.fp4idx_compact_pages(
+        _addr(page_table, "page_table", _I32, 0, dev), _addr(cached_lens, "cached_lens", _I32, B, dev), B, most, ratio,
+        num_pages, _pinned(pinned, num_pages, dev), _addr(workspace, "workspace", _U8, 0, dev), workspace.numel(),
+        _addr(free_pages, "free_pages", _I32, 0, dev), free_pages.numel(),
+        _addr(page_table_out, "page_table_out", _I32, 0, dev), _addr(move_src, "move_src", _I32, 0, dev),
+        _addr(move_dst, "move_dst", _I32, moves, dev), moves, _addr(counts, "counts", _I32, 4, dev),
+        None if status is None else _addr(status, "status", _I32, 1, dev), on)
+    _check("fp4idx_compact_pages", rc)
 
 
 def test_pipeline_waits(idle_producers: bool, wait_limit_ns: int = 0) -> None:
