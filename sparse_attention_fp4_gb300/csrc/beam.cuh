@@ -7,10 +7,10 @@
 namespace fp4idx {
 
 // What one chunk of a row's tokens leaves for the join: the largest logit, the sum of
-// exp(logit - largest), and how many candidates its list holds.
+// exp(logit - largest) as the sum of two floats, and how many candidates its list holds.
 struct BeamStat {
-  float top, sum;
-  int32_t count, unused;
+  float top, sum, sum_low;
+  int32_t count;
 };
 struct BeamItem {
   float logit;
@@ -26,7 +26,8 @@ struct BeamArgs {
   BeamStat* stats;  // [n_rows, chunks]
   BeamItem* lists;  // [n_rows, chunks, k], each in descending order
   int64_t stride;
-  int32_t n_rows, vocab, beams, k, chunks, end_token;
+  int32_t n_rows, vocab, beams, k, end_token;
+  int32_t chunks, chunk_vecs;  // chunks of a row, and how many 16-byte vectors of logits one has
 };
 size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k);
 cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaStream_t stream);

@@ -13,12 +13,51 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kRanked = 256;  // up to here places are sorted by counting
+constexpr int kAll = 128;     // up to here a join sorts all of a group's candidates at once
 constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
 __device__ __forceinline__ float to_float(float v) { return v; }
+
+// A number as the unevaluated sum of two floats, the second at most half a unit of the first (Knuth's exact
+// sum of two floats; some 46 bits).  FP64 would do as well, but this GPU has next to no units for it: the
+// exponentials and logarithms of a group's few sums took 3.5 to 22 us of a join in it.
+struct Two {
+  float hi, lo;
+};
+__device__ __forceinline__ Two sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return Two{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Two operator+(const Two& a, const Two& b) {
+  const Two s = sum_of(a.hi, b.hi);
+  return sum_of(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two operator+(const Two& a, float b) { return a + Two{b, 0.f}; }
+__device__ __forceinline__ Two operator-(const Two& a) { return Two{-a.hi, -a.lo}; }
+__device__ __forceinline__ Two scaled(const Two& a, float power) { return Two{a.hi * power, a.lo * power}; }
+__device__ __forceinline__ Two xor_lane(const Two& a, int d) {
+  return Two{__shfl_xor_sync(~0u, a.hi, d), __shfl_xor_sync(~0u, a.lo, d)};
+}
+// log(v) for a normal v > 0: v = 2^e f with f in [3/4, 3/2), log f = 2 artanh(s), s = (f - 1) / (f + 1) (the first
+// term of its series in two floats, the others, below 0.006, in one); within 2e-9.
+__device__ __forceinline__ Two log_of(const Two& v) {
+  int e = (__float_as_int(v.hi) >> 23) - 127;
+  float f = __int_as_float((__float_as_int(v.hi) & 0x7FFFFF) | 0x3F800000);
+  if (f >= 1.5f) f *= 0.5f, e++;
+  const float n = f - 1.f;  // exact
+  const Two d = sum_of(f, 1.f);
+  const float s = __fdiv_rn(n, d.hi);
+  const float low = (__fmaf_rn(-s, d.hi, n) - s * d.lo) / d.hi;  // of n / d
+  const float z = s * s;
+  const float rest = s * z * (0.33333334f + z * (0.2f + z * (0.14285715f + z * (0.11111111f + z * (0.09090909f + z * 0.07692308f)))));
+  // ln 2 in two parts: the first has 16 bits, so that its product with e is exact
+  const Two base = sum_of(e * 0.693145751953125f, 2.f * s);
+  return base + (2.f * (low + rest) + e * 1.4286068203094173e-6f + v.lo / v.hi);
+}
 
 // What a row contributes: nothing (dead, or its score is no number), its tokens, or its end.
 enum Kind : int32_t { kNone, kTokens, kEnd };
@@ -32,12 +71,15 @@ __device__ __forceinline__ Kind kind_of(const BeamArgs& a, int row, float score,
 }
 
 // ---------------------------------------------------------------- scan
-constexpr int kSlots = 128;        // threads of a chunk that may hold candidates
-constexpr int kFound = kThreads;   // candidates of a chunk before the last ranking
+constexpr int kScan = 512, kScanWarps = kScan / 32;
+constexpr int kVecs = 4;          // vectors (16 bytes of logits) that a thread takes at once
+constexpr int kFound = kScan;     // candidates of a chunk before the last ranking
 constexpr int kSegments = 128;
+constexpr int kOwners = kScan / 2;  // threads whose vectors are read again
+constexpr float kLog2e = 1.4426950408889634f;
 
 template <class T>
-struct Elems;  // sixteen bytes of logits
+struct Elems;
 template <>
 struct Elems<__nv_bfloat16> {
   static constexpr uint32_t kMasked = 0xFF80FF80u;  // -inf
@@ -46,7 +88,7 @@ struct Elems<__nv_bfloat16> {
 };
 template <>
 struct Elems<__half> {
-  static constexpr uint32_t kMasked = 0xFC00FC00u;
+  static constexpr uint32_t kMasked = 0xFC00FC00u;  // -inf
   using Pair = __half2;
   __device__ static float2 pair(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
 };
@@ -70,28 +112,28 @@ __device__ __forceinline__ void each(const uint4& v, F&& f) {
   }
 }
 // The largest element (NaN left out).
-template <class T, int kVecs>
-__device__ __forceinline__ float largest(const uint4 (&v)[kVecs]) {
+template <class T, int kN>
+__device__ __forceinline__ float largest(const uint4 (&v)[kN]) {
   if constexpr (sizeof(T) == 4) {
     float m = -kInf;
 #pragma unroll
-    for (int j = 0; j < kVecs; j++)
+    for (int j = 0; j < kN; j++)
       m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(v[j].x), __uint_as_float(v[j].y)),
                          fmaxf(__uint_as_float(v[j].z), __uint_as_float(v[j].w))));
     return m;
   } else {
     using P = typename Elems<T>::Pair;
-    uint32_t w = Elems<T>::kMasked;
+    uint32_t w = v[0].x;
     P m = *reinterpret_cast<P*>(&w);
 #pragma unroll
-    for (int j = 0; j < kVecs; j++)
+    for (int j = 0; j < kN; j++)
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
+      for (int i = j == 0; i < 4; i++) {
         uint32_t u = word_of(v[j], i);
         m = __hmax2(m, *reinterpret_cast<P*>(&u));
       }
     const float2 f = Elems<T>::pair(*reinterpret_cast<uint32_t*>(&m));
-    return fmaxf(f.x, f.y);
+    return fmaxf(-kInf, fmaxf(f.x, f.y));
   }
 }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -106,30 +148,63 @@ __device__ __forceinline__ uint4 load_once(const uint4* p) {
                : "l"(p));
   return v;
 }
-// A vector that reaches over the row's first or last token: nothing outside is read.
-template <class T>
-__device__ __noinline__ uint4 load_edge(const T* x, int p0, int vocab) {
-  constexpr int kE = 16 / sizeof(T);
-  uint4 v = make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
-  T* e = reinterpret_cast<T*>(&v);
-  for (int i = 0; i < kE; i++)
-    if (p0 + i >= 0 && p0 + i < vocab) e[i] = x[p0 + i];
-  return v;
-}
 // Numbers in the order of their bits; larger is larger.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const int32_t i = __float_as_int(v + 0.f);
   return (uint32_t)i ^ (i < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-template <int kVecs>
+// The largest of what a thread has read, and the sum of exp(value - largest): 2^((value - largest) log2 e).
+struct Running {
+  float top = -kInf, sum = 0.f;
+
+  __device__ static float ref(float m) { return m == -kInf ? 0.f : m; }
+  __device__ float rescaled(float to) const { return sum * exp2_approx((top - to) * kLog2e); }
+  __device__ void add(float v) {
+    const float m = fmaxf(top, v);
+    sum = rescaled(ref(m)) + exp2_approx((v - ref(m)) * kLog2e);
+    top = m;
+  }
+  template <class T, int kN>
+  __device__ void add(const uint4 (&v)[kN]) {
+    const float m = fmaxf(top, largest<T>(v)), r = ref(m);
+    uint64_t part[2] = {0, 0};
+    const uint64_t minus = pack(-r, -r), scale = pack(kLog2e, kLog2e);
+#pragma unroll
+    for (int j = 0; j < kN; j++)
+#pragma unroll
+      for (int i = 0; i < 4; i += sizeof(T) / 2) {
+        float2 u;
+        if constexpr (sizeof(T) == 4) u = make_float2(__uint_as_float(word_of(v[j], i)), __uint_as_float(word_of(v[j], i + 1)));
+        else u = Elems<T>::pair(word_of(v[j], i));
+        uint64_t d = pack(u.x, u.y);
+        asm("add.rn.f32x2 %0, %0, %1;\n\tmul.rn.f32x2 %0, %0, %2;" : "+l"(d) : "l"(minus), "l"(scale));
+        const float2 e = unpack(d);
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(part[i >> (sizeof(T) / 4) & 1]) : "l"(pack(exp2_approx(e.x), exp2_approx(e.y))));
+      }
+    const float2 p = unpack(part[0]), q = unpack(part[1]);
+    sum = rescaled(r) + ((p.x + p.y) + (q.x + q.y));
+    top = m;
+  }
+  __device__ static uint64_t pack(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+  }
+  __device__ static float2 unpack(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+
 struct ScanShared {
-  uint4 slot[kSlots][kVecs];
   float segment[kSegments];
-  float top[kWarps], sum[kWarps];
+  float top[kScanWarps];
+  Two sum[kScanWarps];
   BeamItem found[kFound];
-  int32_t owner[kSlots];
-  int32_t slots, n, count[2];
+  int32_t owner[kScan];
+  int32_t owners, n, count[2];
   float bound;
 };
 
@@ -144,136 +219,140 @@ __device__ __forceinline__ int block_sum(int v, int32_t* count, int slot) {
   return all;
 }
 
-template <class T, int kVecs>
-__global__ void __launch_bounds__(kThreads) scan_kernel(const BeamArgs a) {
-  constexpr int kE = 16 / sizeof(T), kChunk = kThreads * kVecs;  // vectors of a chunk
-  __shared__ ScanShared<kVecs> sm;
+// A row's tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a
+// chunk takes `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.
+template <class T>
+__global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
+  constexpr int kE = 16 / sizeof(T);
+  __shared__ ScanShared sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
-  if (tid == 0) sm.slots = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
+  if (tid == 0) sm.owners = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (kind_of(a, row, a.scores[row], false) != kTokens) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.stride;
-  const int lead = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));  // elements before the row in its first vector
-  const uint4* vecs = reinterpret_cast<const uint4*>(x - lead);
-  const int v0 = chunk * kChunk + tid;
-  auto token = [&](int vec, int e) { return vec * kE - lead + e; };
-  auto load = [&](int vec) {
-    const int p0 = token(vec, 0);
-    return p0 >= 0 && p0 + kE <= a.vocab ? load_once(vecs + vec) : load_edge(x, p0, a.vocab);
+  const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
+  const int vecs = (a.vocab - head) / kE, rest = head + vecs * kE;
+  const int first = min(vecs, chunk * a.chunk_vecs), end = min(vecs, first + a.chunk_vecs);
+  const uint4* body = reinterpret_cast<const uint4*>(x + head);
+  // the token of lane l of the first warp at the row's ends, -1 for none
+  const int edge = chunk > 0 ? -1 : tid < head ? tid : tid >= 8 && tid < 8 + a.vocab - rest ? rest + tid - 8 : -1;
+  Running run;
+  // the next vectors are on their way while these are taken in
+  auto load = [&](int i, uint4 (&v)[kVecs]) {
+#pragma unroll
+    for (int j = 0; j < kVecs; j++)
+      v[j] = i + j * kScan < end ? load_once(body + i + j * kScan) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
   };
-  uint4 v[kVecs];
-  if ((lead == 0 || chunk > 0) && token((chunk + 1) * kChunk, 0) <= a.vocab) {
-#pragma unroll
-    for (int j = 0; j < kVecs; j++) v[j] = load_once(vecs + v0 + j * kThreads);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kVecs; j++) v[j] = load(v0 + j * kThreads);
+  constexpr int kTile = kVecs * kScan;
+  uint4 v[2][kVecs];
+  load(first + tid, v[0]);
+  for (int i = first + tid; i < end; i += 2 * kTile) {
+    load(i + kTile, v[1]);
+    run.add<T>(v[0]);
+    load(i + 2 * kTile, v[0]);
+    if (i + kTile < end) run.add<T>(v[1]);
   }
-  // the chunk's largest, and the largest of its segments (of four threads each; two for long lists)
-  const float mine = largest<T>(v);
-  const int span = a.k > 32 ? 2 : 4, segments = kThreads / span;
-  float top = fmaxf(mine, __shfl_xor_sync(~0u, mine, 1));
-  if (span == 4) top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-  if (tid % span == 0) sm.segment[tid / span] = top;
+  // (earlier, the join's CTAs would take the places of CTAs of this scan that have not begun)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (edge >= 0) run.add(to_float(x[edge]));
+  // the largest of all, and of segments (of eight threads; four for long lists)
+  const int span = a.k > 32 ? 4 : 8, segments = kScan / span;
+  float top = run.top;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  for (int d = 1; d < 32; d <<= 1) {
+    if (d == span && (lane & (span - 1)) == 0) sm.segment[tid / span] = top;
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  }
   if (lane == 0) sm.top[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWarps; w++) top = fmaxf(top, sm.top[w]);
+  for (int w = 0; w < kScanWarps; w++) top = fmaxf(top, sm.top[w]);
+  Two sum{run.rescaled(Running::ref(top)), 0.f};
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum = sum + xor_lane(sum, d);
+  if (lane == 0) sm.sum[warp] = sum;
   // a bound for the k largest: the k-th largest segment
   if (tid < segments) {
     const float u = sm.segment[tid];
     int rank = 0;
-    for (int i = 0; i < segments; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(&sm.segment[i]);
-      rank += (q.x > u || (q.x == u && i < tid)) + (q.y > u || (q.y == u && i + 1 < tid)) +
-              (q.z > u || (q.z == u && i + 2 < tid)) + (q.w > u || (q.w == u && i + 3 < tid));
+    for (int s = 0; s < segments; s += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(&sm.segment[s]);
+      rank += (q.x > u || (q.x == u && s < tid)) + (q.y > u || (q.y == u && s + 1 < tid)) +
+              (q.z > u || (q.z == u && s + 2 < tid)) + (q.w > u || (q.w == u && s + 3 < tid));
     }
     if (rank == a.k - 1) sm.bound = u;
   }
-  // the sum of exponentials: exp(x - top) = 2^((x - top) log2 e)
-  const float ref = top == -kInf ? 0.f : top;
-  float sums[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int j = 0; j < kVecs; j++)
-    each<T>(v[j], [&](int e, float u) { sums[e & 3] += exp2_approx((u - ref) * 1.4426950408889634f); });
-  float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-#pragma unroll
-  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-  if (lane == 0) sm.sum[warp] = sum;
   __syncthreads();
-  // threads with a candidate hand their vectors to whole warps
+  // what threads with a candidate have read is read once more, by all threads
   const float bound = sm.bound;
-  if (mine >= bound && mine > -kInf) {
-    const int s = atomicAdd(&sm.slots, 1);
-    if (s < kSlots) {
-      sm.owner[s] = tid;
-#pragma unroll
-      for (int j = 0; j < kVecs; j++) sm.slot[s][j] = v[j];
+  auto keep = [&](float u, int token) {
+    if (u >= bound && u > -kInf) {
+      const int at = atomicAdd(&sm.n, 1);
+      if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token};
     }
-  }
+  };
+  if (run.top >= bound && run.top > -kInf) sm.owner[atomicAdd(&sm.owners, 1)] = tid;
+  if (edge >= 0) keep(to_float(x[edge]), edge);
   __syncthreads();
-  bool fits = sm.slots <= kSlots;
-  if (fits) {
-    for (int s = warp; s < sm.slots; s += kWarps) {
-      const T* e = reinterpret_cast<const T*>(sm.slot[s]);
-      const int first = chunk * kChunk + sm.owner[s];
-      for (int i = lane; i < kVecs * kE; i += 32) {
-        const float u = to_float(e[i]);
-        if (u >= bound && u > -kInf) {
-          const int at = atomicAdd(&sm.n, 1);
-          if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token(first + i / kE * kThreads, i % kE)};
-        }
+  const int owners = sm.owners, steps = (end - first + kScan - 1) / kScan;
+  if (owners <= kOwners) {
+    for (int w = tid; w < owners * steps && *(volatile int32_t*)&sm.n <= kFound; w += 8 * kScan) {
+      uint4 u[8];
+      int at[8];
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const int o = w + j * kScan;
+        at[j] = o < owners * steps ? first + sm.owner[o / steps] + o % steps * kScan : end;
+        u[j] = at[j] < end ? load_once(body + at[j]) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; j++) {
+        const uint4 one[1] = {u[j]};
+        if (largest<T>(one) >= bound) each<T>(u[j], [&](int e, float x) { keep(x, head + at[j] * kE + e); });
       }
     }
-    __syncthreads();
-    fits = sm.n <= kFound;
   }
-  if (!fits) {
-    // many equal values, or all tokens that are not masked within few threads: the k-th largest exactly,
-    // then of those that equal it the first ones, bit by bit.  (The logits are read again for every bit:
-    // held in registers they cost the common path its occupancy.)
+  __syncthreads();
+  if (owners > kOwners || sm.n > kFound) {
+    // many equal values, or all tokens that are not masked within few threads: the k-th largest
+    // exactly, then of those that equal it the first ones, bit by bit
     int turn = 0;
+    auto all_of = [&](auto&& f) {
+      for (int v = first + tid; v < end; v += kScan) each<T>(body[v], [&](int e, float u) { f(ordered(u), u, head + v * kE + e); });
+      if (edge >= 0) f(ordered(to_float(x[edge])), to_float(x[edge]), edge);
+    };
     auto count = [&](auto&& f) {
       int n = 0;
-#pragma unroll 1
-      for (int j = 0; j < kVecs; j++) each<T>(load(v0 + j * kThreads), [&](int e, float u) { n += f(ordered(u), j, e); });
+      all_of([&](uint32_t o, float, int token) { n += f(o, token); });
       n = block_sum(n, sm.count, turn);
       turn ^= 1;
       return n;
     };
-    const uint32_t none = ordered(-kInf);
-    uint32_t kth = none + 1;
-    int all = count([&](uint32_t u, int, int) { return u >= kth; });
-    int last = INT32_MAX;  // of the equal ones, those up to here
-    if (all > a.k) {
+    uint32_t kth = ordered(-kInf) + 1;
+    int last = INT32_MAX;  // of the equal ones, those up to this token
+    if (count([&](uint32_t o, int) { return o >= kth; }) > a.k) {
       kth = 0;
       for (int b = 31; b >= 0; b--) {
         const uint32_t next = kth | 1u << b;
-        if (count([&](uint32_t u, int, int) { return u >= next; }) >= a.k) kth = next;
+        if (count([&](uint32_t o, int) { return o >= next; }) >= a.k) kth = next;
       }
-      const int want = a.k - count([&](uint32_t u, int, int) { return u > kth; });
-      last = -1;  // (the largest position with fewer than `want` of them at or before it)
-      for (int b = 14; b >= 0; b--) {
+      const int want = a.k - count([&](uint32_t o, int) { return o > kth; });
+      last = -1;  // (the largest token with fewer than `want` of them at or before it)
+      for (int b = 19; b >= 0; b--) {
         const int next = last + (1 << b);
-        if (count([&](uint32_t u, int j, int e) { return u == kth && (j * kThreads + tid) * kE + e <= next; }) < want) last = next;
+        if (count([&](uint32_t o, int token) { return o == kth && token <= next; }) < want) last = next;
       }
       last++;
     }
     if (tid == 0) sm.n = 0;
     __syncthreads();
-#pragma unroll 1
-    for (int j = 0; j < kVecs; j++)
-      each<T>(load(v0 + j * kThreads), [&](int e, float u) {
-        const uint32_t o = ordered(u);
-        if (o > kth || (o == kth && (j * kThreads + tid) * kE + e <= last)) {
-          const int at = atomicAdd(&sm.n, 1);
-          if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token(v0 + j * kThreads, e)};
-        }
-      });
+    all_of([&](uint32_t o, float u, int token) {
+      if (o > kth || (o == kth && token <= last)) {
+        const int at = atomicAdd(&sm.n, 1);
+        if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token};
+      }
+    });
     __syncthreads();
   }
   const int n = min(sm.n, kFound);
@@ -281,64 +360,64 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(const BeamArgs a) {
   if (tid < n) {
     const BeamItem it = sm.found[tid];
     int rank = 0;
-    for (int i = 0; i < n; i++) {
-      const BeamItem o = sm.found[i];
+    for (int s = 0; s < n; s++) {
+      const BeamItem o = sm.found[s];
       rank += o.logit > it.logit || (o.logit == it.logit && o.token < it.token);
     }
     if (rank < a.k) a.lists[out * a.k + rank] = it;
   }
   if (tid == 0) {
-    sum = 0.f;
-    for (int w = 0; w < kWarps; w++) sum += sm.sum[w];
-    a.stats[out] = BeamStat{top, sum, min(n, a.k), 0};
+    sum = sm.sum[0];
+    for (int w = 1; w < kScanWarps; w++) sum = sum + sm.sum[w];
+    // (of a NaN or an infinity the second float is no number)
+    a.stats[out] = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
   }
 }
 
 // ---------------------------------------------------------------- join
 // A candidate's place: `total` orders first (larger is better), `rest` breaks ties (smaller is better: row,
-// then larger logit, then token).  {0, ...}: no candidate.
+// then larger logit, then token).  Where there is no candidate, `total` is 0 and `rest` the place's own index.
 struct __align__(16) Place {
   uint64_t total, rest;
 };
 __device__ __forceinline__ bool before(const Place& a, const Place& b) {
   return a.total > b.total || (a.total == b.total && a.rest < b.rest);
 }
-__device__ __forceinline__ Place place(double total, int beam, float logit, int token) {
-  const int64_t t = __double_as_longlong(total + 0.0);
-  const int32_t v = __float_as_int(logit);
-  const uint32_t up = (uint32_t)v ^ (v < 0 ? 0xFFFFFFFFu : 0x80000000u);
-  return Place{(uint64_t)t ^ (t < 0 ? ~0ull : 1ull << 63), (uint64_t)beam << 52 | (uint64_t)~up << 20 | (uint32_t)token};
+__device__ __forceinline__ Place no_place(int i) { return Place{0, (uint64_t)i}; }
+__device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
+// `quarter`: a fourth of the total, which no finite score and logits make overflow.
+__device__ __forceinline__ Place place(const Two& quarter, int beam, float logit, int token) {
+  return Place{(uint64_t)ordered(quarter.hi) << 32 | ordered(quarter.lo),
+               (uint64_t)beam << 52 | (uint64_t)~ordered(logit) << 20 | (uint32_t)token};
 }
 
-// Descending order; n is a power of two.
+// Descending order; n is a power of two.  No two places are equal.
 __device__ void sort_places(Place* p, int n) {
-  if (n <= kThreads) {  // by the number of those before
-    const int i = threadIdx.x;
+  __syncthreads();
+  if (n <= kRanked) {  // by the number of those before; adjacent lanes share an element
+    const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
     Place mine;
     int rank = 0;
-    __syncthreads();
     if (i < n) {
       mine = p[i];
-      for (int j = 0; j < n; j++) {
-        const Place o = p[j];
-        rank += before(o, mine) || (j < i && !before(mine, o));
-      }
+#pragma unroll 4
+      for (int j = part; j < n; j += share) rank += before(p[j], mine);
     }
+    for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     __syncthreads();
-    if (i < n) p[rank] = mine;
+    if (i < n && part == 0) p[rank] = mine;
     __syncthreads();
     return;
   }
   for (int size = 2; size <= n; size <<= 1)
     for (int d = size >> 1; d; d >>= 1) {
-      __syncthreads();
       for (int i = threadIdx.x; i < n / 2; i += kThreads) {
         const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
         const Place u = p[lo], v = p[hi];
         if (before(v, u) == ((lo & size) == 0)) p[lo] = v, p[hi] = u;
       }
+      __syncthreads();
     }
-  __syncthreads();
 }
 __host__ __device__ inline int pow2_from(int n) {
   int p = 1;
@@ -346,91 +425,122 @@ __host__ __device__ inline int pow2_from(int n) {
   return p;
 }
 
-__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
+// Some 4 k candidates, and k at the least, make the bound of a join.
+__host__ __device__ inline int depth(int k, int lists) {
+  const int d = (4 * k + lists - 1) / lists;
+  return d < k ? d : k;
+}
+
+// The lists of a group are read once, next to the rows' sums; what follows stays in shared memory.
+__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a, int32_t pool_size) {
   extern __shared__ __align__(16) uint8_t smem[];
   Place* pool = reinterpret_cast<Place*>(smem);
+  BeamItem* items = reinterpret_cast<BeamItem*>(pool + pool_size);
   // lse = top + rest, kept apart: next to a large top the sum's logarithm would be lost
   __shared__ float tops[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ double rest[FP4IDX_BEAM_MAX_BEAMS];
+  __shared__ Two rest[FP4IDX_BEAM_MAX_BEAMS];
   __shared__ float score[FP4IDX_BEAM_MAX_BEAMS];
   __shared__ int32_t kind[FP4IDX_BEAM_MAX_BEAMS];
   __shared__ int32_t open[FP4IDX_BEAM_MAX_K];  // lists that hold a candidate
   __shared__ int32_t n_open, n_found;
   __shared__ Place least;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = blockIdx.x * a.beams, k = a.k;
+  const int first = blockIdx.x * a.beams, k = a.k, lists = a.beams * a.chunks;
+  int32_t* sizes = reinterpret_cast<int32_t*>(items + lists * k);
+  if (tid == 0) n_open = n_found = 0, least = Place{0, ~0ull};
+  // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
+  int lanes = 1;
+  while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  for (int b = warp; b < a.beams; b += kWarps) {
-    const int row = first + b;
-    const float s = a.scores[row];
-    Kind what = kind_of(a, row, s, lane == 0);
-    double total = 0.0;
+  // (of rows without lists this reads what the workspace held; it is not looked at)
+  const BeamItem* from = a.lists + (int64_t)first * a.chunks * k;
+  for (int i = tid; i < lists * k; i += kThreads) items[i] = from[i];
+  for (int b0 = 0; b0 < a.beams; b0 += kThreads / lanes) {
+    const int b = b0 + tid / lanes, c0 = tid & (lanes - 1);
+    const bool live = b < a.beams;
+    const float s = live ? a.scores[first + b] : -kInf;
+    const BeamStat* st = a.stats + (int64_t)(first + b) * a.chunks;
+    Kind what = live ? kind_of(a, first + b, s, c0 == 0) : kNone;
+    Two total{0.f, 0.f};
     float top = -kInf;
+    if (what == kTokens)
+      for (int c = c0; c < a.chunks; c += lanes) top = fmaxf(top, st[c].top);
+    for (int d = lanes >> 1; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (what == kTokens)
+      for (int c = c0; c < a.chunks; c += lanes) {
+        const BeamStat t = st[c];
+        const float w = exp2_approx((t.top - Running::ref(top)) * kLog2e);  // (one for the chunk of the largest)
+        total = total + Two{t.sum * w, t.sum_low * w};
+      }
+    for (int d = lanes >> 1; d; d >>= 1) total = total + xor_lane(total, d);
     if (what == kTokens) {
-      const BeamStat* st = a.stats + (int64_t)row * a.chunks;
-      for (int c = lane; c < a.chunks; c += 32) top = fmaxf(top, st[c].top);
-      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      for (int c = lane; c < a.chunks; c += 32) {
-        const float sum = st[c].sum;
-        if (sum != 0.f) total += (double)sum * exp(top == -kInf ? 0.0 : (double)st[c].top - top);
-      }
-      for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(~0u, total, d);
-      if (!(total < (double)kInf)) {  // a logit is NaN or +inf
-        if (lane == 0) record_error(a.status, FP4IDX_ERR_BAD_VALUE);
+      if (!(total.hi < kInf)) {  // a logit is NaN or +inf
+        if (c0 == 0) record_error(a.status, FP4IDX_ERR_BAD_VALUE);
         what = kNone;
-      } else if (total == 0.0) {
+      } else if (total.hi == 0.f) {
         what = kNone;
+      } else {
+        total = log_of(total);
       }
-      total = log(total);
     }
-    if (lane == 0) kind[b] = what, score[b] = s, tops[b] = top, rest[b] = total;
+    if (live) {
+      for (int c = c0; c < a.chunks; c += lanes) sizes[b * a.chunks + c] = what == kTokens ? st[c].count : what == kEnd && c == 0;
+      if (c0 == 0) kind[b] = what, score[b] = s, tops[b] = top, rest[b] = total;
+    }
   }
-  if (tid == 0) n_open = n_found = 0, least = Place{0, ~0ull};
   __syncthreads();
   // the i-th candidate of list l (list l = beam * chunks + chunk)
-  auto size_of = [&](int l) {
-    const int b = l / a.chunks, c = l - b * a.chunks;
-    return kind[b] == kTokens ? a.stats[(int64_t)(first + b) * a.chunks + c].count : kind[b] == kEnd && c == 0 ? 1 : 0;
-  };
   auto item = [&](int l, int i) {
     const int b = l / a.chunks;
-    if (kind[b] == kEnd) return place(score[b], b, 0.f, a.end_token);
-    const BeamItem it = a.lists[((int64_t)first * a.chunks + l) * k + i];
-    return place((double)score[b] + (((double)it.logit - tops[b]) - rest[b]), b, it.logit, it.token);
+    const float s = score[b] * 0.25f;
+    if (kind[b] == kEnd) return place(Two{s, 0.f}, b, 0.f, a.end_token);
+    const BeamItem it = items[l * k + i];
+    return place(sum_of(it.logit * 0.25f, tops[b] * -0.25f) + -scaled(rest[b], 0.25f) + s, b, it.logit, it.token);
   };
-  // A bound: the k-th best of each list's first `deep` candidates (k candidates at the least, if
-  // there are that many).  At most k lists begin with one that is no worse.
-  const int lists = a.beams * a.chunks, deep = (k + lists - 1) / lists, heads = pow2_from(lists * deep);
-  for (int i = tid; i < heads; i += kThreads) {
-    const int l = i / deep, at = i - l * deep;
-    pool[i] = l < lists && at < size_of(l) ? item(l, at) : Place{0, ~0ull};
-  }
-  sort_places(pool, heads);
-  if (tid == 0 && k <= heads) least = pool[k - 1];
-  __syncthreads();
-  for (int l = tid; l < lists; l += kThreads)
-    if (size_of(l) > 0 && !before(least, item(l, 0))) open[atomicAdd(&n_open, 1)] = l;
-  __syncthreads();
-  for (int o = warp; o < n_open; o += kWarps) {
-    const int l = open[o], n = size_of(l);
-    for (int i = lane; i < n; i += 32) {
-      const Place p = item(l, i);
-      if (!before(least, p)) pool[atomicAdd(&n_found, 1)] = p;
+  if (lists * k <= kAll) {
+    const int all = pow2_from(lists * k);
+    for (int i = tid; i < all; i += kThreads) {
+      const int l = i / k, at = i - l * k;
+      const bool live = l < lists && at < sizes[l];
+      pool[i] = live ? item(l, at) : no_place(i);
+      if (live) atomicAdd(&n_found, 1);
     }
+    sort_places(pool, all);
+  } else {
+    // a bound: the k-th best of each list's first `deep` candidates.  At most k lists begin with one that is
+    // no worse (or fewer than k candidates are all there are).
+    const int deep = depth(k, lists), heads = pow2_from(lists * deep);
+    for (int i = tid; i < heads; i += kThreads) {
+      const int l = i / deep, at = i - l * deep;
+      pool[i] = l < lists && at < sizes[l] ? item(l, at) : no_place(i);
+    }
+    sort_places(pool, heads);
+    if (tid == 0 && pool[k - 1].total) least = pool[k - 1];
+    __syncthreads();
+    for (int l = tid; l < lists; l += kThreads)
+      if (sizes[l] > 0 && !before(least, item(l, 0))) open[atomicAdd(&n_open, 1)] = l;
+    __syncthreads();
+    for (int o = warp; o < n_open; o += kWarps) {
+      const int l = open[o], n = sizes[l];
+      for (int i = lane; i < n; i += 32) {
+        const Place p = item(l, i);
+        if (!before(least, p)) pool[atomicAdd(&n_found, 1)] = p;
+      }
+    }
+    __syncthreads();
+    const int padded = pow2_from(n_found);
+    for (int i = n_found + tid; i < padded; i += kThreads) pool[i] = no_place(i);
+    sort_places(pool, padded);
   }
-  __syncthreads();
-  const int found = n_found, padded = pow2_from(found);
-  for (int i = found + tid; i < padded; i += kThreads) pool[i] = Place{0, ~0ull};
-  sort_places(pool, padded);
+  const int found = n_found;
   for (int i = tid; i < k; i += kThreads) {
     const int64_t o = (int64_t)blockIdx.x * k + i;
     float total = -kInf;
     int row = -1, token = -1, ended = 0;
     if (i < found) {
       const Place p = pool[i];
-      const uint64_t t = p.total ^ (p.total >> 63 ? 1ull << 63 : ~0ull);
-      total = (float)__longlong_as_double((int64_t)t);
+      total = 4.f * unordered((uint32_t)(p.total >> 32));
       const int b = (int)(p.rest >> 52);
       row = first + b;
       token = (int)(p.rest & 0xFFFFF);
@@ -443,49 +553,48 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   }
 }
 
-// Chunks of a row, `vecs` vectors of `elems` logits a thread (a row may begin anywhere in its first vector).
-int64_t chunks_of(int32_t vocab, int elems, int vecs) {
-  return ((int64_t)vocab + elems - 1 + (int64_t)elems * kThreads * vecs - 1) / ((int64_t)elems * kThreads * vecs);
-}
-// Small chunks where large ones would leave SMs without work.
-constexpr int kLong = 8, kShort = 2, kManyCtas = 304;
-bool short_chunks(int64_t n_rows, int32_t vocab, int elems) { return n_rows * chunks_of(vocab, elems, kLong) < kManyCtas; }
-
-template <class T>
-cudaError_t launch_scan(const BeamArgs& a, bool brief, cudaStream_t stream) {
-  return launch_early(brief ? scan_kernel<T, kShort> : scan_kernel<T, kLong>, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)),
-                      kThreads, 0, 1, stream, a);
-}
+// CTAs of a scan that run at once, the least and the most vectors of a row that one of them takes, and the candidates
+// that a join keeps in shared memory.
+constexpr int kCtas = 304, kLeastVecs = kScan, kMostVecs = 32 * kVecs * kScan, kMostItems = 8192;
+struct Cut {
+  int32_t chunks, vecs;
+  Cut(int64_t n_rows, int32_t beams, int32_t k, int32_t vocab, int elems) {
+    const int64_t all = std::max(1, vocab / elems);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kCtas / n_rows, kMostItems / (beams * k)));
+    int64_t each = std::max<int64_t>(kLeastVecs, (all + want - 1) / want);
+    each = std::min<int64_t>((each + 31) / 32 * 32, kMostVecs);
+    vecs = (int32_t)each;
+    chunks = (int32_t)((all + each - 1) / each);
+  }
+};
 
 }  // namespace
 
 size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k) {
+  // enough for up to n_rows rows of any type (of fewer rows each may have more chunks)
   int64_t most = 1;
   for (int elems : {4, 8}) {
-    // (up to n_rows rows: the short chunks of fewer rows may be more)
-    const int64_t few = std::min(n_rows, (kManyCtas - 1) / chunks_of(vocab, elems, kLong));
-    most = std::max({most, few * chunks_of(vocab, elems, kShort), n_rows * chunks_of(vocab, elems, kLong)});
+    const int64_t all = std::max(1, vocab / elems), least = (all + kMostVecs - 1) / kMostVecs;
+    most = std::max(most, std::min(n_rows * ((all + kLeastVecs - 1) / kLeastVecs), std::max<int64_t>(kCtas, n_rows * least)));
   }
   return (size_t)most * (sizeof(BeamStat) + k * sizeof(BeamItem));
 }
 
 cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaStream_t stream) {
-  const int elems = type == 2 ? 4 : 8;
-  const bool brief = short_chunks(a.n_rows, a.vocab, elems);
-  a.chunks = (int32_t)chunks_of(a.vocab, elems, brief ? kShort : kLong);
+  const Cut cut(a.n_rows, a.beams, a.k, a.vocab, type == 2 ? 4 : 8);
+  a.chunks = cut.chunks;
+  a.chunk_vecs = cut.vecs;
   a.stats = static_cast<BeamStat*>(workspace);
   a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
-  cudaError_t e = type == 0   ? launch_scan<__nv_bfloat16>(a, brief, stream)
-                  : type == 1 ? launch_scan<__half>(a, brief, stream)
-                              : launch_scan<float>(a, brief, stream);
+  auto scan = type == 0 ? scan_kernel<__nv_bfloat16> : type == 1 ? scan_kernel<__half> : scan_kernel<float>;
+  cudaError_t e = launch_early(scan, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, 0, 1, stream, a);
   if (e != cudaSuccess) return e;
-  const int lists = a.beams * a.chunks, deep = (a.k + lists - 1) / lists;
-  const size_t smem = sizeof(Place) * std::max(pow2_from(lists * deep), pow2_from(std::min(lists, a.k) * a.k));
-  if (smem > 40 * 1024) {
-    e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 128 * 1024);
-    if (e != cudaSuccess) return e;
-  }
-  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, smem, 1, stream, a);
+  const int lists = a.beams * a.chunks;
+  const int pool = lists * a.k <= kAll ? pow2_from(lists * a.k) : std::max(pow2_from(lists * depth(a.k, lists)), pow2_from(std::min(lists, a.k) * a.k));
+  const size_t smem = sizeof(Place) * pool + (size_t)lists * (a.k * sizeof(BeamItem) + 4);
+  e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 160 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, smem, 1, stream, a, pool);
 }
 
 }  // namespace fp4idx
