@@ -74,8 +74,8 @@ __device__ __forceinline__ Kind kind_of(const BeamArgs& a, int row, float score,
 constexpr int kScan = 512, kScanWarps = kScan / 32;
 constexpr int kVecs = 4;          // vectors (16 bytes of logits) that a thread takes at once
 constexpr int kFound = kScan;     // candidates of a chunk before the last ranking
+constexpr int kTile = kVecs * kScan;
 constexpr int kSegments = 128;
-constexpr int kOwners = kScan / 2;  // threads whose vectors are read again
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <class T>
@@ -166,8 +166,8 @@ struct Running {
     top = m;
   }
   template <class T, int kN>
-  __device__ void add(const uint4 (&v)[kN]) {
-    const float m = fmaxf(top, largest<T>(v)), r = ref(m);
+  __device__ float add(const uint4 (&v)[kN]) {  // (the largest of these)
+    const float here = largest<T>(v), m = fmaxf(top, here), r = ref(m);
     uint64_t part[2] = {0, 0};
     const uint64_t minus = pack(-r, -r), scale = pack(kLog2e, kLog2e);
 #pragma unroll
@@ -185,6 +185,7 @@ struct Running {
     const float2 p = unpack(part[0]), q = unpack(part[1]);
     sum = rescaled(r) + ((p.x + p.y) + (q.x + q.y));
     top = m;
+    return here;
   }
   __device__ static uint64_t pack(float x, float y) {
     uint64_t r;
@@ -203,7 +204,7 @@ struct ScanShared {
   float top[kScanWarps];
   Two sum[kScanWarps];
   BeamItem found[kFound];
-  int32_t owner[kScan];
+  int32_t owner[kScan];  // thread + tile * kScan
   int32_t owners, n, count[2];
   float bound;
 };
@@ -225,6 +226,7 @@ template <class T>
 __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
   constexpr int kE = 16 / sizeof(T);
   __shared__ ScanShared sm;
+  extern __shared__ float tops[];  // the largest of each thread's tiles
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
   if (tid == 0) sm.owners = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
@@ -244,14 +246,13 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
     for (int j = 0; j < kVecs; j++)
       v[j] = i + j * kScan < end ? load_once(body + i + j * kScan) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
   };
-  constexpr int kTile = kVecs * kScan;
   uint4 v[2][kVecs];
   load(first + tid, v[0]);
-  for (int i = first + tid; i < end; i += 2 * kTile) {
+  for (int i = first + tid, t = tid; i < end; i += 2 * kTile, t += 2 * kScan) {
     load(i + kTile, v[1]);
-    run.add<T>(v[0]);
+    tops[t] = run.add<T>(v[0]);
     load(i + 2 * kTile, v[0]);
-    if (i + kTile < end) run.add<T>(v[1]);
+    if (i + kTile < end) tops[t + kScan] = run.add<T>(v[1]);
   }
   // (earlier, the join's CTAs would take the places of CTAs of this scan that have not begun)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -272,19 +273,21 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum = sum + xor_lane(sum, d);
   if (lane == 0) sm.sum[warp] = sum;
-  // a bound for the k largest: the k-th largest segment
-  if (tid < segments) {
-    const float u = sm.segment[tid];
+  // a bound for the k largest: the k-th largest segment (adjacent lanes share one)
+  {
+    const int i = tid / span;
+    const float u = sm.segment[i];
     int rank = 0;
-    for (int s = 0; s < segments; s += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(&sm.segment[s]);
-      rank += (q.x > u || (q.x == u && s < tid)) + (q.y > u || (q.y == u && s + 1 < tid)) +
-              (q.z > u || (q.z == u && s + 2 < tid)) + (q.w > u || (q.w == u && s + 3 < tid));
+#pragma unroll 4
+    for (int s = tid & (span - 1); s < segments; s += span) {
+      const float q = sm.segment[s];
+      rank += q > u || (q == u && s < i);
     }
-    if (rank == a.k - 1) sm.bound = u;
+    for (int d = 1; d < span; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+    if (rank == a.k - 1 && (tid & (span - 1)) == 0) sm.bound = u;
   }
   __syncthreads();
-  // what threads with a candidate have read is read once more, by all threads
+  // the tiles with a candidate are read once more, a vector a thread
   const float bound = sm.bound;
   auto keep = [&](float u, int token) {
     if (u >= bound && u > -kInf) {
@@ -292,29 +295,26 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
       if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token};
     }
   };
-  if (run.top >= bound && run.top > -kInf) sm.owner[atomicAdd(&sm.owners, 1)] = tid;
+  if (run.top >= bound && run.top > -kInf)
+    for (int t = tid, i = first + tid; i < end; t += kScan, i += kTile)
+      if (tops[t] >= bound && tops[t] > -kInf) {
+        const int o = atomicAdd(&sm.owners, 1);
+        if (o < kScan) sm.owner[o] = t;
+      }
   if (edge >= 0) keep(to_float(x[edge]), edge);
   __syncthreads();
-  const int owners = sm.owners, steps = (end - first + kScan - 1) / kScan;
-  if (owners <= kOwners) {
-    for (int w = tid; w < owners * steps && *(volatile int32_t*)&sm.n <= kFound; w += 8 * kScan) {
-      uint4 u[8];
-      int at[8];
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const int o = w + j * kScan;
-        at[j] = o < owners * steps ? first + sm.owner[o / steps] + o % steps * kScan : end;
-        u[j] = at[j] < end ? load_once(body + at[j]) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; j++) {
-        const uint4 one[1] = {u[j]};
-        if (largest<T>(one) >= bound) each<T>(u[j], [&](int e, float x) { keep(x, head + at[j] * kE + e); });
+  const int owners = sm.owners;
+  if (owners <= kScan) {
+    for (int w = tid; w < owners * kVecs && *(volatile int32_t*)&sm.n <= kFound; w += kScan) {
+      const int t = sm.owner[w / kVecs], i = first + t / kScan * kTile + w % kVecs * kScan + t % kScan;
+      if (i < end) {
+        const uint4 u[1] = {load_once(body + i)};
+        if (largest<T>(u) >= bound) each<T>(u[0], [&](int e, float x) { keep(x, head + i * kE + e); });
       }
     }
   }
   __syncthreads();
-  if (owners > kOwners || sm.n > kFound) {
+  if (owners > kScan || sm.n > kFound) {
     // many equal values, or all tokens that are not masked within few threads: the k-th largest
     // exactly, then of those that equal it the first ones, bit by bit
     int turn = 0;
@@ -357,14 +357,22 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
   }
   const int n = min(sm.n, kFound);
   const int64_t out = (int64_t)row * a.chunks + chunk;
-  if (tid < n) {
-    const BeamItem it = sm.found[tid];
+  int share = 1;  // lanes that share a candidate
+  while (share < 32 && 2 * share * n <= kScan) share <<= 1;
+  {
+    const int i = tid / share;
+    BeamItem it{};
     int rank = 0;
-    for (int s = 0; s < n; s++) {
-      const BeamItem o = sm.found[s];
-      rank += o.logit > it.logit || (o.logit == it.logit && o.token < it.token);
+    if (i < n) {
+      it = sm.found[i];
+#pragma unroll 4
+      for (int s = tid & (share - 1); s < n; s += share) {
+        const BeamItem o = sm.found[s];
+        rank += o.logit > it.logit || (o.logit == it.logit && o.token < it.token);
+      }
     }
-    if (rank < a.k) a.lists[out * a.k + rank] = it;
+    for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+    if (i < n && (tid & (share - 1)) == 0 && rank < a.k) a.lists[out * a.k + rank] = it;
   }
   if (tid == 0) {
     sum = sm.sum[0];
@@ -376,14 +384,15 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
 
 // ---------------------------------------------------------------- join
 // A candidate's place: `total` orders first (larger is better), `rest` breaks ties (smaller is better: row,
-// then larger logit, then token).  Where there is no candidate, `total` is 0 and `rest` the place's own index.
+// then larger logit, then token).  Where there is no candidate, `total` is below 2^32 and the place's own.
 struct __align__(16) Place {
   uint64_t total, rest;
+  __device__ bool real() const { return total >> 32; }
 };
 __device__ __forceinline__ bool before(const Place& a, const Place& b) {
   return a.total > b.total || (a.total == b.total && a.rest < b.rest);
 }
-__device__ __forceinline__ Place no_place(int i) { return Place{0, (uint64_t)i}; }
+__device__ __forceinline__ Place no_place(int i) { return Place{(uint64_t)i, 0}; }
 __device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
 // `quarter`: a fourth of the total, which no finite score and logits make overflow.
 __device__ __forceinline__ Place place(const Two& quarter, int beam, float logit, int token) {
@@ -397,12 +406,19 @@ __device__ void sort_places(Place* p, int n) {
   if (n <= kRanked) {  // by the number of those before; adjacent lanes share an element
     const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
     Place mine;
-    int rank = 0;
+    int rank = 0, same = 0;
     if (i < n) {
       mine = p[i];
 #pragma unroll 4
-      for (int j = part; j < n; j += share) rank += before(p[j], mine);
+      for (int j = part; j < n; j += share) {
+        const uint64_t t = p[j].total;
+        rank += t > mine.total;
+        same += t == mine.total;
+      }
     }
+    for (int d = 1; d < share; d <<= 1) same += __shfl_xor_sync(~0u, same, d);
+    if (same > 1)  // (itself, and equal totals)
+      for (int j = part; j < n; j += share) rank += p[j].total == mine.total && p[j].rest < mine.rest;
     for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     __syncthreads();
     if (i < n && part == 0) p[rank] = mine;
@@ -447,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a, int32_
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int first = blockIdx.x * a.beams, k = a.k, lists = a.beams * a.chunks;
   int32_t* sizes = reinterpret_cast<int32_t*>(items + lists * k);
-  if (tid == 0) n_open = n_found = 0, least = Place{0, ~0ull};
+  if (tid == 0) n_open = n_found = 0, least = Place{1ull << 32, 0};  // (behind every candidate)
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
   int lanes = 1;
   while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a, int32_
       pool[i] = l < lists && at < sizes[l] ? item(l, at) : no_place(i);
     }
     sort_places(pool, heads);
-    if (tid == 0 && pool[k - 1].total) least = pool[k - 1];
+    if (tid == 0 && pool[k - 1].real()) least = pool[k - 1];
     __syncthreads();
     for (int l = tid; l < lists; l += kThreads)
       if (sizes[l] > 0 && !before(least, item(l, 0))) open[atomicAdd(&n_open, 1)] = l;
@@ -587,7 +603,9 @@ cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaSt
   a.stats = static_cast<BeamStat*>(workspace);
   a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
   auto scan = type == 0 ? scan_kernel<__nv_bfloat16> : type == 1 ? scan_kernel<__half> : scan_kernel<float>;
-  cudaError_t e = launch_early(scan, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, 0, 1, stream, a);
+  const size_t tops = sizeof(float) * kScan * ((cut.vecs + kTile - 1) / kTile);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(scan), sizeof(float) * kMostVecs / kVecs);
+  if (e == cudaSuccess) e = launch_early(scan, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, tops, 1, stream, a);
   if (e != cudaSuccess) return e;
   const int lists = a.beams * a.chunks;
   const int pool = lists * a.k <= kAll ? pow2_from(lists * a.k) : std::max(pow2_from(lists * depth(a.k, lists)), pow2_from(std::min(lists, a.k) * a.k));
