@@ -14,8 +14,7 @@ namespace fp4idx {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kRanked = 256;  // up to here places are sorted by counting
-constexpr int kAll = 128;     // up to here a join sorts all of a group's candidates at once
+constexpr int kAll = 128;  // up to here a join sorts all of a group's candidates at once
 constexpr float kInf = __builtin_huge_valf();
 
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
@@ -281,7 +280,7 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
 #pragma unroll 4
     for (int s = tid & (span - 1); s < segments; s += span) {
       const float q = sm.segment[s];
-      rank += q > u || (q == u && s < i);
+      rank += (int)(q > u) | ((int)(q == u) & (int)(s < i));
     }
     for (int d = 1; d < span; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     if (rank == a.k - 1 && (tid & (span - 1)) == 0) sm.bound = u;
@@ -368,60 +367,51 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
 #pragma unroll 4
       for (int s = tid & (share - 1); s < n; s += share) {
         const BeamItem o = sm.found[s];
-        rank += o.logit > it.logit || (o.logit == it.logit && o.token < it.token);
+        rank += (int)(o.logit > it.logit) | ((int)(o.logit == it.logit) & (int)(o.token < it.token));
       }
     }
     for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     if (i < n && (tid & (share - 1)) == 0 && rank < a.k) a.lists[out * a.k + rank] = it;
   }
-  if (tid == 0) {
-    sum = sm.sum[0];
-    for (int w = 1; w < kScanWarps; w++) sum = sum + sm.sum[w];
+  if (warp == kScanWarps - 1) {
+    sum = sm.sum[lane & (kScanWarps - 1)];
+#pragma unroll 1
+    for (int d = 1; d < kScanWarps; d <<= 1) sum = sum + xor_lane(sum, d);
     // (of a NaN or an infinity the second float is no number)
-    a.stats[out] = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
+    if (lane == 0) a.stats[out] = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
   }
 }
 
 // ---------------------------------------------------------------- join
-// A candidate's place: `total` orders first (larger is better), `rest` breaks ties (smaller is better: row,
-// then larger logit, then token).  Where there is no candidate, `total` is below 2^32 and the place's own.
-struct __align__(16) Place {
-  uint64_t total, rest;
-  __device__ bool real() const { return total >> 32; }
-};
-__device__ __forceinline__ bool before(const Place& a, const Place& b) {
-  return a.total > b.total || (a.total == b.total && a.rest < b.rest);
-}
-__device__ __forceinline__ Place no_place(int i) { return Place{(uint64_t)i, 0}; }
 __device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
-// `quarter`: a fourth of the total, which no finite score and logits make overflow.
-__device__ __forceinline__ Place place(const Two& quarter, int beam, float logit, int token) {
-  return Place{(uint64_t)ordered(quarter.hi) << 32 | ordered(quarter.lo),
-               (uint64_t)beam << 52 | (uint64_t)~ordered(logit) << 20 | (uint32_t)token};
-}
 
-// Descending order; n is a power of two.  No two places are equal.
-__device__ void sort_places(Place* p, int n) {
-  __syncthreads();
-  if (n <= kRanked) {  // by the number of those before; adjacent lanes share an element
+// A group's candidates lie in shared memory list after list (beam after beam, chunk after chunk, each in order), k
+// places each, kMostItems in all.  Their keys are in the order of the totals (larger is better): the first of its
+// two floats, all but the last 13 bits of the second, and, so that no two keys are equal and the lower index (the lower
+// row, then the lower token) comes first among equal totals, the index counted down.  What is no candidate has
+// a key below 2^32.
+constexpr int kIndexBits = 13, kMostItems = 1 << kIndexBits;
+__device__ __forceinline__ uint64_t key_of(const Two& total, int i) {
+  const uint64_t t = (uint64_t)ordered(total.hi) << 32 | ordered(total.lo);
+  return (t >> kIndexBits << kIndexBits) | (kMostItems - 1 - i);
+}
+__device__ __forceinline__ int index_of(uint64_t key) { return kMostItems - 1 - (int)(key & (kMostItems - 1)); }
+// Descending order.  Up to kThreads (a power of two) by counting those above each, adjacent lanes sharing one; more
+// of them (a power of two) in a sorting network.
+__device__ __forceinline__ void sort_keys(uint64_t* keys, int n) {
+  if (n <= kThreads) {
     const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
-    Place mine;
-    int rank = 0, same = 0;
+    uint64_t key = 0;
+    int rank = 0;
     if (i < n) {
-      mine = p[i];
-#pragma unroll 4
-      for (int j = part; j < n; j += share) {
-        const uint64_t t = p[j].total;
-        rank += t > mine.total;
-        same += t == mine.total;
-      }
+      key = keys[i];
+#pragma unroll 8
+      for (int j = part; j < n; j += share) rank += keys[j] > key;
     }
-    for (int d = 1; d < share; d <<= 1) same += __shfl_xor_sync(~0u, same, d);
-    if (same > 1)  // (itself, and equal totals)
-      for (int j = part; j < n; j += share) rank += p[j].total == mine.total && p[j].rest < mine.rest;
+#pragma unroll 1
     for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     __syncthreads();
-    if (i < n && part == 0) p[rank] = mine;
+    if (part == 0 && i < n) keys[rank] = key;
     __syncthreads();
     return;
   }
@@ -429,8 +419,8 @@ __device__ void sort_places(Place* p, int n) {
     for (int d = size >> 1; d; d >>= 1) {
       for (int i = threadIdx.x; i < n / 2; i += kThreads) {
         const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-        const Place u = p[lo], v = p[hi];
-        if (before(v, u) == ((lo & size) == 0)) p[lo] = v, p[hi] = u;
+        const uint64_t u = keys[lo], v = keys[hi];
+        if ((v > u) == ((lo & size) == 0)) keys[lo] = v, keys[hi] = u;
       }
       __syncthreads();
     }
@@ -440,126 +430,116 @@ __host__ __device__ inline int pow2_from(int n) {
   while (p < n) p <<= 1;
   return p;
 }
-
 // Some 4 k candidates, and k at the least, make the bound of a join.
 __host__ __device__ inline int depth(int k, int lists) {
   const int d = (4 * k + lists - 1) / lists;
   return d < k ? d : k;
 }
+// Places of the list of candidates that are sorted (with room for those that fill it up to a power of two).
+__host__ __device__ inline int sorted_most(int k, int lists) {
+  const int all = lists * k;
+  return all <= kAll ? pow2_from(all) : pow2_from(lists < k ? all : k * k);
+}
 
-// The lists of a group are read once, next to the rows' sums; what follows stays in shared memory.
-__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a, int32_t pool_size) {
+// One CTA a group.
+__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  Place* pool = reinterpret_cast<Place*>(smem);
-  BeamItem* items = reinterpret_cast<BeamItem*>(pool + pool_size);
   // lse = top + rest, kept apart: next to a large top the sum's logarithm would be lost
-  __shared__ float tops[FP4IDX_BEAM_MAX_BEAMS];
+  __shared__ float tops[FP4IDX_BEAM_MAX_BEAMS], score[FP4IDX_BEAM_MAX_BEAMS];
   __shared__ Two rest[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ float score[FP4IDX_BEAM_MAX_BEAMS];
   __shared__ int32_t kind[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ int32_t open[FP4IDX_BEAM_MAX_K];  // lists that hold a candidate
-  __shared__ int32_t n_open, n_found;
-  __shared__ Place least;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int first = blockIdx.x * a.beams, k = a.k, lists = a.beams * a.chunks;
-  int32_t* sizes = reinterpret_cast<int32_t*>(items + lists * k);
-  if (tid == 0) n_open = n_found = 0, least = Place{1ull << 32, 0};  // (behind every candidate)
+  __shared__ int32_t n_found;
+  const int tid = threadIdx.x;
+  const int first = blockIdx.x * a.beams, k = a.k, lists = a.beams * a.chunks, all = lists * k, per_beam = a.chunks * k;
+  uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
+  int32_t* tokens = reinterpret_cast<int32_t*>(keys + all);
+  int32_t* sizes = tokens + all;
+  uint64_t* sorted = keys + (all * 3 + lists + 1) / 2;
+  if (tid == 0) n_found = 0;
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
   int lanes = 1;
   while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // (of rows without lists this reads what the workspace held; it is not looked at)
-  const BeamItem* from = a.lists + (int64_t)first * a.chunks * k;
-  for (int i = tid; i < lists * k; i += kThreads) items[i] = from[i];
   for (int b0 = 0; b0 < a.beams; b0 += kThreads / lanes) {
     const int b = b0 + tid / lanes, c0 = tid & (lanes - 1);
     const bool live = b < a.beams;
-    const float s = live ? a.scores[first + b] : -kInf;
     const BeamStat* st = a.stats + (int64_t)(first + b) * a.chunks;
-    Kind what = live ? kind_of(a, first + b, s, c0 == 0) : kNone;
-    Two total{0.f, 0.f};
-    float top = -kInf;
-    if (what == kTokens)
-      for (int c = c0; c < a.chunks; c += lanes) top = fmaxf(top, st[c].top);
+    // (a row without lists has what the workspace held; it is not looked at)
+    BeamStat mine{-kInf, 0.f, 0.f, 0};
+    if (live && c0 < a.chunks) mine = st[c0];
+    const float sc = live ? a.scores[first + b] : -kInf;
+    Kind what = live ? kind_of(a, first + b, sc, c0 == 0) : kNone;
+    float top = mine.top;
+    for (int q = c0 + lanes; q < a.chunks && live; q += lanes) top = fmaxf(top, st[q].top);
     for (int d = lanes >> 1; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    if (what == kTokens)
-      for (int c = c0; c < a.chunks; c += lanes) {
-        const BeamStat t = st[c];
-        const float w = exp2_approx((t.top - Running::ref(top)) * kLog2e);  // (one for the chunk of the largest)
-        total = total + Two{t.sum * w, t.sum_low * w};
-      }
+    Two total{0.f, 0.f};
+    for (int q = c0; q < a.chunks && live; q += lanes) {
+      const BeamStat t = q == c0 ? mine : st[q];
+      const float w = exp2_approx((t.top - Running::ref(top)) * kLog2e);  // (one for the chunk of the largest)
+      total = total + Two{t.sum * w, t.sum_low * w};
+      sizes[b * a.chunks + q] = what == kTokens ? t.count : what == kEnd && q == 0;
+    }
+#pragma unroll 1
     for (int d = lanes >> 1; d; d >>= 1) total = total + xor_lane(total, d);
-    if (what == kTokens) {
-      if (!(total.hi < kInf)) {  // a logit is NaN or +inf
-        if (c0 == 0) record_error(a.status, FP4IDX_ERR_BAD_VALUE);
-        what = kNone;
-      } else if (total.hi == 0.f) {
-        what = kNone;
-      } else {
-        total = log_of(total);
-      }
+    if (what == kTokens && !(total.hi < kInf)) {  // a logit is NaN or +inf
+      if (c0 == 0) record_error(a.status, FP4IDX_ERR_BAD_VALUE);
+      what = kNone;
     }
-    if (live) {
-      for (int c = c0; c < a.chunks; c += lanes) sizes[b * a.chunks + c] = what == kTokens ? st[c].count : what == kEnd && c == 0;
-      if (c0 == 0) kind[b] = what, score[b] = s, tops[b] = top, rest[b] = total;
-    }
+    if (what == kTokens && total.hi == 0.f) what = kNone;
+    if (what == kTokens) total = log_of(total);
+    if (live && c0 == 0) kind[b] = what, score[b] = sc, tops[b] = top, rest[b] = total;
   }
   __syncthreads();
-  // the i-th candidate of list l (list l = beam * chunks + chunk)
-  auto item = [&](int l, int i) {
-    const int b = l / a.chunks;
-    const float s = score[b] * 0.25f;
-    if (kind[b] == kEnd) return place(Two{s, 0.f}, b, 0.f, a.end_token);
-    const BeamItem it = items[l * k + i];
-    return place(sum_of(it.logit * 0.25f, tops[b] * -0.25f) + -scaled(rest[b], 0.25f) + s, b, it.logit, it.token);
-  };
-  if (lists * k <= kAll) {
-    const int all = pow2_from(lists * k);
-    for (int i = tid; i < all; i += kThreads) {
-      const int l = i / k, at = i - l * k;
-      const bool live = l < lists && at < sizes[l];
-      pool[i] = live ? item(l, at) : no_place(i);
-      if (live) atomicAdd(&n_found, 1);
+  const BeamItem* from = a.lists + (int64_t)first * per_beam;
+  for (int i = tid; i < all; i += kThreads) {
+    const int l = i / k, b = i / per_beam;
+    uint64_t key = (1 << 16) + i;
+    BeamItem it = from[i];
+    if (kind[b] != kNone && i - l * k < sizes[l]) {
+      // a fourth of the total: no finite score and logits make it overflow
+      Two t{score[b] * 0.25f, 0.f};
+      if (kind[b] == kEnd) it.token = a.end_token;
+      else t = sum_of(it.logit * 0.25f, tops[b] * -0.25f) + -scaled(rest[b], 0.25f) + t;
+      key = key_of(t, i);
     }
-    sort_places(pool, all);
-  } else {
-    // a bound: the k-th best of each list's first `deep` candidates.  At most k lists begin with one that is
-    // no worse (or fewer than k candidates are all there are).
-    const int deep = depth(k, lists), heads = pow2_from(lists * deep);
-    for (int i = tid; i < heads; i += kThreads) {
-      const int l = i / deep, at = i - l * deep;
-      pool[i] = l < lists && at < sizes[l] ? item(l, at) : no_place(i);
-    }
-    sort_places(pool, heads);
-    if (tid == 0 && pool[k - 1].real()) least = pool[k - 1];
-    __syncthreads();
-    for (int l = tid; l < lists; l += kThreads)
-      if (sizes[l] > 0 && !before(least, item(l, 0))) open[atomicAdd(&n_open, 1)] = l;
-    __syncthreads();
-    for (int o = warp; o < n_open; o += kWarps) {
-      const int l = open[o], n = sizes[l];
-      for (int i = lane; i < n; i += 32) {
-        const Place p = item(l, i);
-        if (!before(least, p)) pool[atomicAdd(&n_found, 1)] = p;
-      }
-    }
-    __syncthreads();
-    const int padded = pow2_from(n_found);
-    for (int i = n_found + tid; i < padded; i += kThreads) pool[i] = no_place(i);
-    sort_places(pool, padded);
+    keys[i] = key;
+    tokens[i] = it.token;
   }
-  const int found = n_found;
+  __syncthreads();
+  int n = all;
+  if (all > kAll) {
+    // a bound: the k-th best of each list's first `deep` candidates.  At most k lists begin with one that is
+    // no worse, or fewer than k candidates are all there are.
+    const int deep = depth(k, lists), heads = lists * deep, m = pow2_from(heads);
+    for (int i = tid; i < m; i += kThreads) sorted[i] = i < heads ? keys[i / deep * k + i % deep] : i;
+    __syncthreads();
+    sort_keys(sorted, m);
+    const uint64_t bound = sorted[k - 1];
+    __syncthreads();
+    for (int i = tid; i < all; i += kThreads) {
+      const uint64_t key = keys[i];
+      if (key >> 32 && key >= bound) sorted[atomicAdd(&n_found, 1)] = key;
+    }
+    __syncthreads();
+    n = n_found;
+  } else {
+    for (int i = tid; i < n; i += kThreads) sorted[i] = keys[i];
+  }
+  const int m = pow2_from(n);
+  for (int i = n + tid; i < m; i += kThreads) sorted[i] = i;
+  __syncthreads();
+  sort_keys(sorted, m);
   for (int i = tid; i < k; i += kThreads) {
     const int64_t o = (int64_t)blockIdx.x * k + i;
     float total = -kInf;
     int row = -1, token = -1, ended = 0;
-    if (i < found) {
-      const Place p = pool[i];
-      total = 4.f * unordered((uint32_t)(p.total >> 32));
-      const int b = (int)(p.rest >> 52);
+    const uint64_t key = i < m ? sorted[i] : 0;
+    if (key >> 32) {
+      const int at = index_of(key), b = at / per_beam;
+      total = 4.f * unordered((uint32_t)(key >> 32));
       row = first + b;
-      token = (int)(p.rest & 0xFFFFF);
+      token = tokens[at];
       ended = kind[b] == kEnd || token == a.end_token;
     }
     a.out_scores[o] = total;
@@ -569,9 +549,8 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a, int32_
   }
 }
 
-// CTAs of a scan that run at once, the least and the most vectors of a row that one of them takes, and the candidates
-// that a join keeps in shared memory.
-constexpr int kCtas = 304, kLeastVecs = kScan, kMostVecs = 32 * kVecs * kScan, kMostItems = 8192;
+// CTAs of a scan that run at once, and the least and the most vectors of a row that one of them takes.
+constexpr int kCtas = 304, kLeastVecs = kScan, kMostVecs = 32 * kVecs * kScan;
 struct Cut {
   int32_t chunks, vecs;
   Cut(int64_t n_rows, int32_t beams, int32_t k, int32_t vocab, int elems) {
@@ -607,12 +586,12 @@ cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaSt
   cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(scan), sizeof(float) * kMostVecs / kVecs);
   if (e == cudaSuccess) e = launch_early(scan, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, tops, 1, stream, a);
   if (e != cudaSuccess) return e;
-  const int lists = a.beams * a.chunks;
-  const int pool = lists * a.k <= kAll ? pow2_from(lists * a.k) : std::max(pow2_from(lists * depth(a.k, lists)), pow2_from(std::min(lists, a.k) * a.k));
-  const size_t smem = sizeof(Place) * pool + (size_t)lists * (a.k * sizeof(BeamItem) + 4);
-  e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 160 * 1024);
+  const int lists = a.beams * a.chunks, all = lists * a.k;
+  const int sorted = std::max(all > kAll ? pow2_from(lists * depth(a.k, lists)) : 0, sorted_most(a.k, lists));
+  const size_t smem = sizeof(uint64_t) * ((all * 3 + lists + 1) / 2 + sorted);
+  e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
   if (e != cudaSuccess) return e;
-  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, smem, 1, stream, a, pool);
+  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, smem, 1, stream, a);
 }
 
 }  // namespace fp4idx
