@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 
 #include "beam.cuh"
+#include "mma_bf16.cuh"
 
 namespace fp4idx {
 namespace {
@@ -61,12 +62,13 @@ __device__ __forceinline__ Two log_of(const Two& v) {
 // What a row contributes: nothing (dead, or its score is no number), its tokens, or its end.
 enum Kind : int32_t { kNone, kTokens, kEnd };
 __device__ __forceinline__ Kind kind_of(const BeamArgs& a, int row, float score, bool report) {
+  const bool done = a.done && a.done[row];
   if (score == -kInf) return kNone;
   if (!(score < kInf)) {  // NaN or +inf
     if (report) record_error(a.status, FP4IDX_ERR_BAD_VALUE);
     return kNone;
   }
-  return a.done && a.done[row] ? kEnd : kTokens;
+  return done ? kEnd : kTokens;
 }
 
 // ---------------------------------------------------------------- scan
@@ -219,18 +221,21 @@ __device__ __forceinline__ int block_sum(int v, int32_t* count, int slot) {
   return all;
 }
 
-// A row's tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a
-// chunk takes `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.
-template <class T>
-__global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
+// One chunk: its list and its sums go to `list` and `stat` (nothing, if the row has no tokens to offer).  A row's
+// tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a chunk takes
+// `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.  `tops` has a float for each tile
+// of each thread; `ready` is called by all threads before anything is written.
+template <class T, class Ready>
+__device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk, ScanShared& sm, float* tops, BeamItem* list,
+                                           BeamStat* stat, Ready&& ready) {
   constexpr int kE = 16 / sizeof(T);
-  __shared__ ScanShared sm;
-  extern __shared__ float tops[];  // the largest of each thread's tiles
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = blockIdx.x / a.chunks, chunk = blockIdx.x - row * a.chunks;
   if (tid == 0) sm.owners = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (kind_of(a, row, a.scores[row], false) != kTokens) return;
+  if (kind_of(a, row, a.scores[row], false) != kTokens) {
+    ready();
+    return;
+  }
   const T* x = static_cast<const T*>(a.logits) + row * a.stride;
   const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
   const int vecs = (a.vocab - head) / kE, rest = head + vecs * kE;
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
     __syncthreads();
   }
   const int n = min(sm.n, kFound);
-  const int64_t out = (int64_t)row * a.chunks + chunk;
+  ready();
   int share = 1;  // lanes that share a candidate
   while (share < 32 && 2 * share * n <= kScan) share <<= 1;
   {
@@ -371,15 +376,24 @@ __global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
       }
     }
     for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
-    if (i < n && (tid & (share - 1)) == 0 && rank < a.k) a.lists[out * a.k + rank] = it;
+    if (i < n && (tid & (share - 1)) == 0 && rank < a.k) list[rank] = it;
   }
   if (warp == kScanWarps - 1) {
     sum = sm.sum[lane & (kScanWarps - 1)];
 #pragma unroll 1
     for (int d = 1; d < kScanWarps; d <<= 1) sum = sum + xor_lane(sum, d);
     // (of a NaN or an infinity the second float is no number)
-    if (lane == 0) a.stats[out] = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
+    if (lane == 0) *stat = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
   }
+}
+
+template <class T>
+__global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ ScanShared sm;
+  const int row = blockIdx.x / a.chunks;
+  scan_chunk<T>(a, row, blockIdx.x - row * a.chunks, sm, reinterpret_cast<float*>(smem), a.lists + (int64_t)blockIdx.x * a.k,
+                a.stats + blockIdx.x, [] {});
 }
 
 // ---------------------------------------------------------------- join
@@ -441,30 +455,35 @@ __host__ __device__ inline int sorted_most(int k, int lists) {
   return all <= kAll ? pow2_from(all) : pow2_from(lists < k ? all : k * k);
 }
 
-// One CTA a group.
-__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];
+struct JoinShared {
   // lse = top + rest, kept apart: next to a large top the sum's logarithm would be lost
-  __shared__ float tops[FP4IDX_BEAM_MAX_BEAMS], score[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ Two rest[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ int32_t kind[FP4IDX_BEAM_MAX_BEAMS];
-  __shared__ int32_t n_found;
+  float tops[FP4IDX_BEAM_MAX_BEAMS], score[FP4IDX_BEAM_MAX_BEAMS];
+  Two rest[FP4IDX_BEAM_MAX_BEAMS];
+  int32_t kind[FP4IDX_BEAM_MAX_BEAMS];
+  int32_t n_found;
+};
+__host__ __device__ inline size_t join_bytes(int k, int lists) {
+  const int all = lists * k, heads = all > kAll ? pow2_from(lists * depth(k, lists)) : 0, most = sorted_most(k, lists);
+  return sizeof(uint64_t) * ((all * 3 + lists + 1) / 2 + (heads > most ? heads : most));
+}
+
+// One group, by one CTA, from its rows' lists and sums; `smem` has join_bytes.
+__device__ __forceinline__ void join_group(const BeamArgs& a, int group, const BeamStat* stats, const BeamItem* from,
+                                           JoinShared& sm, uint8_t* smem) {
   const int tid = threadIdx.x;
-  const int first = blockIdx.x * a.beams, k = a.k, lists = a.beams * a.chunks, all = lists * k, per_beam = a.chunks * k;
+  const int first = group * a.beams, k = a.k, lists = a.beams * a.chunks, all = lists * k, per_beam = a.chunks * k;
   uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
   int32_t* tokens = reinterpret_cast<int32_t*>(keys + all);
   int32_t* sizes = tokens + all;
   uint64_t* sorted = keys + (all * 3 + lists + 1) / 2;
-  if (tid == 0) n_found = 0;
+  if (tid == 0) sm.n_found = 0;
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
   int lanes = 1;
   while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   for (int b0 = 0; b0 < a.beams; b0 += kThreads / lanes) {
     const int b = b0 + tid / lanes, c0 = tid & (lanes - 1);
     const bool live = b < a.beams;
-    const BeamStat* st = a.stats + (int64_t)(first + b) * a.chunks;
+    const BeamStat* st = stats + b * a.chunks;
     // (a row without lists has what the workspace held; it is not looked at)
     BeamStat mine{-kInf, 0.f, 0.f, 0};
     if (live && c0 < a.chunks) mine = st[c0];
@@ -488,19 +507,18 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     }
     if (what == kTokens && total.hi == 0.f) what = kNone;
     if (what == kTokens) total = log_of(total);
-    if (live && c0 == 0) kind[b] = what, score[b] = sc, tops[b] = top, rest[b] = total;
+    if (live && c0 == 0) sm.kind[b] = what, sm.score[b] = sc, sm.tops[b] = top, sm.rest[b] = total;
   }
   __syncthreads();
-  const BeamItem* from = a.lists + (int64_t)first * per_beam;
   for (int i = tid; i < all; i += kThreads) {
     const int l = i / k, b = i / per_beam;
     uint64_t key = (1 << 16) + i;
     BeamItem it = from[i];
-    if (kind[b] != kNone && i - l * k < sizes[l]) {
+    if (sm.kind[b] != kNone && i - l * k < sizes[l]) {
       // a fourth of the total: no finite score and logits make it overflow
-      Two t{score[b] * 0.25f, 0.f};
-      if (kind[b] == kEnd) it.token = a.end_token;
-      else t = sum_of(it.logit * 0.25f, tops[b] * -0.25f) + -scaled(rest[b], 0.25f) + t;
+      Two t{sm.score[b] * 0.25f, 0.f};
+      if (sm.kind[b] == kEnd) it.token = a.end_token;
+      else t = sum_of(it.logit * 0.25f, sm.tops[b] * -0.25f) + -scaled(sm.rest[b], 0.25f) + t;
       key = key_of(t, i);
     }
     keys[i] = key;
@@ -519,10 +537,10 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
     __syncthreads();
     for (int i = tid; i < all; i += kThreads) {
       const uint64_t key = keys[i];
-      if (key >> 32 && key >= bound) sorted[atomicAdd(&n_found, 1)] = key;
+      if (key >> 32 && key >= bound) sorted[atomicAdd(&sm.n_found, 1)] = key;
     }
     __syncthreads();
-    n = n_found;
+    n = sm.n_found;
   } else {
     for (int i = tid; i < n; i += kThreads) sorted[i] = keys[i];
   }
@@ -531,7 +549,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
   __syncthreads();
   sort_keys(sorted, m);
   for (int i = tid; i < k; i += kThreads) {
-    const int64_t o = (int64_t)blockIdx.x * k + i;
+    const int64_t o = (int64_t)group * k + i;
     float total = -kInf;
     int row = -1, token = -1, ended = 0;
     const uint64_t key = i < m ? sorted[i] : 0;
@@ -540,13 +558,52 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
       total = 4.f * unordered((uint32_t)(key >> 32));
       row = first + b;
       token = tokens[at];
-      ended = kind[b] == kEnd || token == a.end_token;
+      ended = sm.kind[b] == kEnd || token == a.end_token;
     }
     a.out_scores[o] = total;
     a.out_rows[o] = row;
     a.out_tokens[o] = token;
     if (a.done_out) a.done_out[o] = ended;
   }
+}
+
+__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ JoinShared sm;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t list = (int64_t)blockIdx.x * a.beams * a.chunks;
+  join_group(a, blockIdx.x, a.stats + list, a.lists + list * a.k, sm, smem);
+}
+
+// ---------------------------------------------------------------- both in one launch
+// A cluster has a group's chunks; their lists and sums go straight to the shared memory of its first CTA, which joins
+// them.
+__host__ __device__ inline size_t lists_bytes(int k, int lists) { return lists * (sizeof(BeamStat) + k * sizeof(BeamItem)); }
+template <class T>
+__device__ __forceinline__ T* in_first_cta(T* p) {
+  uint64_t r;
+  asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)));
+  return reinterpret_cast<T*>(r);
+}
+template <class T>
+__global__ void __launch_bounds__(kScan, 2) select_kernel(const BeamArgs a) {
+  static_assert(kScan == kThreads, "one CTA does both");
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ ScanShared scan;
+  __shared__ JoinShared join;
+  const int lists = a.beams * a.chunks, group = blockIdx.x / lists, list = blockIdx.x - group * lists;
+  BeamStat* stats = reinterpret_cast<BeamStat*>(smem);
+  BeamItem* items = reinterpret_cast<BeamItem*>(stats + lists);
+  uint8_t* own = smem + lists_bytes(a.k, lists);
+  // (the first CTA has to be there before it is written to)
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int beam = list / a.chunks;
+  scan_chunk<T>(a, group * a.beams + beam, list - beam * a.chunks, scan, reinterpret_cast<float*>(own),
+                in_first_cta(items + list * a.k), in_first_cta(stats + list),
+                [] { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); });
+  mma::cluster_sync();
+  if (list == 0) join_group(a, group, stats, items, join, own);
 }
 
 // CTAs of a scan that run at once, and the least and the most vectors of a row that one of them takes.
@@ -563,6 +620,47 @@ struct Cut {
   }
 };
 
+// Chunks of a row in a cluster of a group: no more CTAs than run at once, or one.
+constexpr int kMaxCluster = 16, kSlack = 8192;
+constexpr size_t kSelectSmem = 100 * 1024;
+int32_t cluster_chunks(int64_t n_rows, int32_t beams) {
+  return (int32_t)std::min<int64_t>(kMaxCluster / beams, std::max<int64_t>(1, kCtas / n_rows));
+}
+
+template <class T>
+cudaError_t launch_typed(BeamArgs a, cudaStream_t stream) {
+  const Cut cut(a.n_rows, a.beams, a.k, a.vocab, 16 / sizeof(T));
+  auto tops = [](int32_t vecs) { return sizeof(float) * kScan * ((vecs + kTile - 1) / kTile); };
+  // One launch where a group's rows fit a cluster, and its CTAs have little more to read than in a wave of all SMs
+  const int32_t each = cluster_chunks(a.n_rows, a.beams);
+  if (each > 0) {
+    const int64_t all = std::max<int64_t>(1, a.vocab / (16 / sizeof(T)));
+    const int64_t vecs = std::max<int64_t>(kLeastVecs, ((all + each - 1) / each + 31) / 32 * 32);
+    if (vecs <= std::min<int64_t>(cut.vecs + kSlack, kMostVecs)) {
+      a.chunk_vecs = (int32_t)vecs;
+      a.chunks = (int32_t)((all + vecs - 1) / vecs);
+      const int lists = a.beams * a.chunks;
+      const size_t smem = lists_bytes(a.k, lists) + std::max(tops(a.chunk_vecs), join_bytes(a.k, lists));
+      const void* f = reinterpret_cast<const void*>(select_kernel<T>);
+      cudaError_t e = set_smem_attr_once(f, kSelectSmem);
+      int fit = 1;
+      if (e == cudaSuccess && lists > 8) e = resident_clusters(f, lists, kScan, kSelectSmem, &fit);
+      if (e != cudaSuccess) return e;
+      if (fit > 0)
+        return launch_early(select_kernel<T>, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, smem, lists, stream, a);
+    }
+  }
+  a.chunks = cut.chunks;
+  a.chunk_vecs = cut.vecs;
+  a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
+  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(scan_kernel<T>), sizeof(float) * kMostVecs / kVecs);
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
+  if (e != cudaSuccess) return e;
+  e = launch_early(scan_kernel<T>, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, tops(a.chunk_vecs), 1, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, join_bytes(a.k, a.beams * a.chunks), 1, stream, a);
+}
+
 }  // namespace
 
 size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k) {
@@ -576,22 +674,10 @@ size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k) {
 }
 
 cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaStream_t stream) {
-  const Cut cut(a.n_rows, a.beams, a.k, a.vocab, type == 2 ? 4 : 8);
-  a.chunks = cut.chunks;
-  a.chunk_vecs = cut.vecs;
   a.stats = static_cast<BeamStat*>(workspace);
-  a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
-  auto scan = type == 0 ? scan_kernel<__nv_bfloat16> : type == 1 ? scan_kernel<__half> : scan_kernel<float>;
-  const size_t tops = sizeof(float) * kScan * ((cut.vecs + kTile - 1) / kTile);
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(scan), sizeof(float) * kMostVecs / kVecs);
-  if (e == cudaSuccess) e = launch_early(scan, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, tops, 1, stream, a);
-  if (e != cudaSuccess) return e;
-  const int lists = a.beams * a.chunks, all = lists * a.k;
-  const int sorted = std::max(all > kAll ? pow2_from(lists * depth(a.k, lists)) : 0, sorted_most(a.k, lists));
-  const size_t smem = sizeof(uint64_t) * ((all * 3 + lists + 1) / 2 + sorted);
-  e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
-  if (e != cudaSuccess) return e;
-  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, smem, 1, stream, a);
+  return type == 0   ? launch_typed<__nv_bfloat16>(a, stream)
+         : type == 1 ? launch_typed<__half>(a, stream)
+                     : launch_typed<float>(a, stream);
 }
 
 }  // namespace fp4idx
