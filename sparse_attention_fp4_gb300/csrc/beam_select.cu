@@ -14,7 +14,7 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kJoin = 512;
 constexpr int kAll = 128;  // up to here a join sorts all of a group's candidates at once
 constexpr float kInf = __builtin_huge_valf();
 
@@ -72,10 +72,7 @@ __device__ __forceinline__ Kind kind_of(const BeamArgs& a, int row, float score,
 }
 
 // ---------------------------------------------------------------- scan
-constexpr int kScan = 512, kScanWarps = kScan / 32;
 constexpr int kVecs = 4;          // vectors (16 bytes of logits) that a thread takes at once
-constexpr int kFound = kScan;     // candidates of a chunk before the last ranking
-constexpr int kTile = kVecs * kScan;
 constexpr int kSegments = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -200,12 +197,14 @@ struct Running {
   }
 };
 
+template <int kThreads>
 struct ScanShared {
+  static constexpr int kFound = kThreads;  // candidates of a chunk before the last ranking
   float segment[kSegments];
-  float top[kScanWarps];
-  Two sum[kScanWarps];
+  float top[kThreads / 32];
+  Two sum[kThreads / 32];
   BeamItem found[kFound];
-  int32_t owner[kScan];  // thread + tile * kScan
+  int32_t owner[kThreads];  // thread + tile * kThreads
   int32_t owners, n, count[2];
   float bound;
 };
@@ -225,17 +224,14 @@ __device__ __forceinline__ int block_sum(int v, int32_t* count, int slot) {
 // tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a chunk takes
 // `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.  `tops` has a float for each tile
 // of each thread; `ready` is called by all threads before anything is written.
-template <class T, class Ready>
-__device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk, ScanShared& sm, float* tops, BeamItem* list,
+template <class T, int kThreads, class Ready>
+__device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk, ScanShared<kThreads>& sm, float* tops, BeamItem* list,
                                            BeamStat* stat, Ready&& ready) {
-  constexpr int kE = 16 / sizeof(T);
+  constexpr int kE = 16 / sizeof(T), kWarps = kThreads / 32, kTile = kVecs * kThreads, kFound = ScanShared<kThreads>::kFound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sm.owners = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (kind_of(a, row, a.scores[row], false) != kTokens) {
-    ready();
-    return;
-  }
+  if (kind_of(a, row, a.scores[row], false) != kTokens) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.stride;
   const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
   const int vecs = (a.vocab - head) / kE, rest = head + vecs * kE;
@@ -248,21 +244,21 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   auto load = [&](int i, uint4 (&v)[kVecs]) {
 #pragma unroll
     for (int j = 0; j < kVecs; j++)
-      v[j] = i + j * kScan < end ? load_once(body + i + j * kScan) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
+      v[j] = i + j * kThreads < end ? load_once(body + i + j * kThreads) : make_uint4(Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked, Elems<T>::kMasked);
   };
   uint4 v[2][kVecs];
   load(first + tid, v[0]);
-  for (int i = first + tid, t = tid; i < end; i += 2 * kTile, t += 2 * kScan) {
+  for (int i = first + tid, t = tid; i < end; i += 2 * kTile, t += 2 * kThreads) {
     load(i + kTile, v[1]);
     tops[t] = run.add<T>(v[0]);
     load(i + 2 * kTile, v[0]);
-    if (i + kTile < end) tops[t + kScan] = run.add<T>(v[1]);
+    if (i + kTile < end) tops[t + kThreads] = run.add<T>(v[1]);
   }
   // (earlier, the join's CTAs would take the places of CTAs of this scan that have not begun)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (edge >= 0) run.add(to_float(x[edge]));
-  // the largest of all, and of segments (of eight threads; four for long lists)
-  const int span = a.k > 32 ? 4 : 8, segments = kScan / span;
+  // the largest of all, and of segments (of adjacent threads, of fewer for long lists)
+  const int segments = a.k > 32 ? kSegments : kSegments / 2, span = kThreads / segments;
   float top = run.top;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -272,7 +268,7 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   if (lane == 0) sm.top[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kScanWarps; w++) top = fmaxf(top, sm.top[w]);
+  for (int w = 0; w < kWarps; w++) top = fmaxf(top, sm.top[w]);
   Two sum{run.rescaled(Running::ref(top)), 0.f};
 #pragma unroll
   for (int d = 16; d; d >>= 1) sum = sum + xor_lane(sum, d);
@@ -300,17 +296,17 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
     }
   };
   if (run.top >= bound && run.top > -kInf)
-    for (int t = tid, i = first + tid; i < end; t += kScan, i += kTile)
+    for (int t = tid, i = first + tid; i < end; t += kThreads, i += kTile)
       if (tops[t] >= bound && tops[t] > -kInf) {
         const int o = atomicAdd(&sm.owners, 1);
-        if (o < kScan) sm.owner[o] = t;
+        if (o < kThreads) sm.owner[o] = t;
       }
   if (edge >= 0) keep(to_float(x[edge]), edge);
   __syncthreads();
   const int owners = sm.owners;
-  if (owners <= kScan) {
-    for (int w = tid; w < owners * kVecs && *(volatile int32_t*)&sm.n <= kFound; w += kScan) {
-      const int t = sm.owner[w / kVecs], i = first + t / kScan * kTile + w % kVecs * kScan + t % kScan;
+  if (owners <= kThreads) {
+    for (int w = tid; w < owners * kVecs && *(volatile int32_t*)&sm.n <= kFound; w += kThreads) {
+      const int t = sm.owner[w / kVecs], i = first + t / kThreads * kTile + w % kVecs * kThreads + t % kThreads;
       if (i < end) {
         const uint4 u[1] = {load_once(body + i)};
         if (largest<T>(u) >= bound) each<T>(u[0], [&](int e, float x) { keep(x, head + i * kE + e); });
@@ -318,12 +314,12 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
     }
   }
   __syncthreads();
-  if (owners > kScan || sm.n > kFound) {
+  if (owners > kThreads || sm.n > kFound) {
     // many equal values, or all tokens that are not masked within few threads: the k-th largest
     // exactly, then of those that equal it the first ones, bit by bit
     int turn = 0;
     auto all_of = [&](auto&& f) {
-      for (int v = first + tid; v < end; v += kScan) each<T>(body[v], [&](int e, float u) { f(ordered(u), u, head + v * kE + e); });
+      for (int v = first + tid; v < end; v += kThreads) each<T>(body[v], [&](int e, float u) { f(ordered(u), u, head + v * kE + e); });
       if (edge >= 0) f(ordered(to_float(x[edge])), to_float(x[edge]), edge);
     };
     auto count = [&](auto&& f) {
@@ -362,7 +358,7 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   const int n = min(sm.n, kFound);
   ready();
   int share = 1;  // lanes that share a candidate
-  while (share < 32 && 2 * share * n <= kScan) share <<= 1;
+  while (share < 32 && 2 * share * n <= kThreads) share <<= 1;
   {
     const int i = tid / share;
     BeamItem it{};
@@ -378,19 +374,19 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
     for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
     if (i < n && (tid & (share - 1)) == 0 && rank < a.k) list[rank] = it;
   }
-  if (warp == kScanWarps - 1) {
-    sum = sm.sum[lane & (kScanWarps - 1)];
+  if (warp == kWarps - 1) {
+    sum = sm.sum[lane & (kWarps - 1)];
 #pragma unroll 1
-    for (int d = 1; d < kScanWarps; d <<= 1) sum = sum + xor_lane(sum, d);
+    for (int d = 1; d < kWarps; d <<= 1) sum = sum + xor_lane(sum, d);
     // (of a NaN or an infinity the second float is no number)
     if (lane == 0) *stat = BeamStat{top, sum.hi, sum.hi < kInf ? sum.lo : 0.f, min(n, a.k)};
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kScan, 2) scan_kernel(const BeamArgs a) {
+template <class T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) scan_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ ScanShared sm;
+  __shared__ ScanShared<kThreads> sm;
   const int row = blockIdx.x / a.chunks;
   scan_chunk<T>(a, row, blockIdx.x - row * a.chunks, sm, reinterpret_cast<float*>(smem), a.lists + (int64_t)blockIdx.x * a.k,
                 a.stats + blockIdx.x, [] {});
@@ -412,6 +408,7 @@ __device__ __forceinline__ uint64_t key_of(const Two& total, int i) {
 __device__ __forceinline__ int index_of(uint64_t key) { return kMostItems - 1 - (int)(key & (kMostItems - 1)); }
 // Descending order.  Up to kThreads (a power of two) by counting those above each, adjacent lanes sharing one; more
 // of them (a power of two) in a sorting network.
+template <int kThreads>
 __device__ __forceinline__ void sort_keys(uint64_t* keys, int n) {
   if (n <= kThreads) {
     const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
@@ -468,6 +465,7 @@ __host__ __device__ inline size_t join_bytes(int k, int lists) {
 }
 
 // One group, by one CTA, from its rows' lists and sums; `smem` has join_bytes.
+template <int kThreads>
 __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const BeamStat* stats, const BeamItem* from,
                                            JoinShared& sm, uint8_t* smem) {
   const int tid = threadIdx.x;
@@ -532,7 +530,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     const int deep = depth(k, lists), heads = lists * deep, m = pow2_from(heads);
     for (int i = tid; i < m; i += kThreads) sorted[i] = i < heads ? keys[i / deep * k + i % deep] : i;
     __syncthreads();
-    sort_keys(sorted, m);
+    sort_keys<kThreads>(sorted, m);
     const uint64_t bound = sorted[k - 1];
     __syncthreads();
     for (int i = tid; i < all; i += kThreads) {
@@ -547,7 +545,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   const int m = pow2_from(n);
   for (int i = n + tid; i < m; i += kThreads) sorted[i] = i;
   __syncthreads();
-  sort_keys(sorted, m);
+  sort_keys<kThreads>(sorted, m);
   for (int i = tid; i < k; i += kThreads) {
     const int64_t o = (int64_t)group * k + i;
     float total = -kInf;
@@ -567,13 +565,13 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   }
 }
 
-__global__ void __launch_bounds__(kThreads) join_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kJoin) join_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ JoinShared sm;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t list = (int64_t)blockIdx.x * a.beams * a.chunks;
-  join_group(a, blockIdx.x, a.stats + list, a.lists + list * a.k, sm, smem);
+  join_group<kJoin>(a, blockIdx.x, a.stats + list, a.lists + list * a.k, sm, smem);
 }
 
 // ---------------------------------------------------------------- both in one launch
@@ -586,11 +584,10 @@ __device__ __forceinline__ T* in_first_cta(T* p) {
   asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)));
   return reinterpret_cast<T*>(r);
 }
-template <class T>
-__global__ void __launch_bounds__(kScan, 2) select_kernel(const BeamArgs a) {
-  static_assert(kScan == kThreads, "one CTA does both");
+template <class T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ ScanShared scan;
+  __shared__ ScanShared<kThreads> scan;
   __shared__ JoinShared join;
   const int lists = a.beams * a.chunks, group = blockIdx.x / lists, list = blockIdx.x - group * lists;
   BeamStat* stats = reinterpret_cast<BeamStat*>(smem);
@@ -599,20 +596,36 @@ __global__ void __launch_bounds__(kScan, 2) select_kernel(const BeamArgs a) {
   // (the first CTA has to be there before it is written to)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   const int beam = list / a.chunks;
+  bool waited = false;
+  auto wait = [&] {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    waited = true;
+  };
   scan_chunk<T>(a, group * a.beams + beam, list - beam * a.chunks, scan, reinterpret_cast<float*>(own),
-                in_first_cta(items + list * a.k), in_first_cta(stats + list),
-                [] { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); });
-  mma::cluster_sync();
-  if (list == 0) join_group(a, group, stats, items, join, own);
+                in_first_cta(items + list * a.k), in_first_cta(stats + list), wait);
+  if (!waited) {  // (a row that has nothing to offer)
+    if (list != 0) return;
+    wait();
+  }
+  // (only the first CTA waits: the others make room, and a barrier does not wait for threads that have ended)
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if (list != 0) return;
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  join_group<kThreads>(a, group, stats, items, join, own);
 }
 
-// CTAs of a scan that run at once, and the least and the most vectors of a row that one of them takes.
-constexpr int kCtas = 304, kLeastVecs = kScan, kMostVecs = 32 * kVecs * kScan;
+// Up to kWave chunks CTAs of 512 threads take one each, all at once; above that CTAs of 256 threads, so that more chunks
+// overlap: what a CTA does besides reading takes some 5 us, of latency.
+constexpr int kWave = 304;
+// The least and the most vectors of a row that one CTA takes, what it takes to spare the join lists, and the lists that
+// a join has then.
+constexpr int kLeastVecs = 512, kMostVecs = 65536, kShortVecs = 4096, kLists = 32;
 struct Cut {
   int32_t chunks, vecs;
   Cut(int64_t n_rows, int32_t beams, int32_t k, int32_t vocab, int elems) {
     const int64_t all = std::max(1, vocab / elems);
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(kCtas / n_rows, kMostItems / (beams * k)));
+    const int64_t few = std::max<int64_t>(kLists / beams, all / kShortVecs);
+    const int64_t want = std::max<int64_t>(1, std::min({kWave / n_rows, (int64_t)(kMostItems / (beams * k)), few}));
     int64_t each = std::max<int64_t>(kLeastVecs, (all + want - 1) / want);
     each = std::min<int64_t>((each + 31) / 32 * 32, kMostVecs);
     vecs = (int32_t)each;
@@ -621,44 +634,49 @@ struct Cut {
 };
 
 // Chunks of a row in a cluster of a group: no more CTAs than run at once, or one.
-constexpr int kMaxCluster = 16, kSlack = 8192;
+constexpr int kMaxCluster = 8, kSlack = 8192;
 constexpr size_t kSelectSmem = 100 * 1024;
 int32_t cluster_chunks(int64_t n_rows, int32_t beams) {
-  return (int32_t)std::min<int64_t>(kMaxCluster / beams, std::max<int64_t>(1, kCtas / n_rows));
+  return (int32_t)std::min<int64_t>(kMaxCluster / beams, std::max<int64_t>(1, kWave / n_rows));
+}
+
+template <class T, int kThreads>
+cudaError_t launch_scan(const BeamArgs& a, bool cluster, cudaStream_t stream) {
+  const int lists = a.beams * a.chunks;
+  const dim3 grid((unsigned)(a.n_rows * (int64_t)a.chunks));
+  const size_t tops = sizeof(float) * kThreads * ((a.chunk_vecs + kVecs * kThreads - 1) / (kVecs * kThreads));
+  cudaError_t e;
+  if (cluster) {
+    e = set_smem_attr_once(reinterpret_cast<const void*>(select_kernel<T, kThreads>), kSelectSmem);
+    if (e != cudaSuccess) return e;
+    return launch_early(select_kernel<T, kThreads>, grid, kThreads, lists_bytes(a.k, lists) + std::max(tops, join_bytes(a.k, lists)),
+                        lists, stream, a);
+  }
+  e = set_smem_attr_once(reinterpret_cast<const void*>(scan_kernel<T, kThreads>), sizeof(float) * kMostVecs / kVecs);
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
+  if (e == cudaSuccess) e = launch_early(scan_kernel<T, kThreads>, grid, kThreads, tops, 1, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kJoin, join_bytes(a.k, lists), 1, stream, a);
 }
 
 template <class T>
 cudaError_t launch_typed(BeamArgs a, cudaStream_t stream) {
   const Cut cut(a.n_rows, a.beams, a.k, a.vocab, 16 / sizeof(T));
-  auto tops = [](int32_t vecs) { return sizeof(float) * kScan * ((vecs + kTile - 1) / kTile); };
-  // One launch where a group's rows fit a cluster, and its CTAs have little more to read than in a wave of all SMs
-  const int32_t each = cluster_chunks(a.n_rows, a.beams);
-  if (each > 0) {
-    const int64_t all = std::max<int64_t>(1, a.vocab / (16 / sizeof(T)));
-    const int64_t vecs = std::max<int64_t>(kLeastVecs, ((all + each - 1) / each + 31) / 32 * 32);
-    if (vecs <= std::min<int64_t>(cut.vecs + kSlack, kMostVecs)) {
-      a.chunk_vecs = (int32_t)vecs;
-      a.chunks = (int32_t)((all + vecs - 1) / vecs);
-      const int lists = a.beams * a.chunks;
-      const size_t smem = lists_bytes(a.k, lists) + std::max(tops(a.chunk_vecs), join_bytes(a.k, lists));
-      const void* f = reinterpret_cast<const void*>(select_kernel<T>);
-      cudaError_t e = set_smem_attr_once(f, kSelectSmem);
-      int fit = 1;
-      if (e == cudaSuccess && lists > 8) e = resident_clusters(f, lists, kScan, kSelectSmem, &fit);
-      if (e != cudaSuccess) return e;
-      if (fit > 0)
-        return launch_early(select_kernel<T>, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, smem, lists, stream, a);
-    }
-  }
   a.chunks = cut.chunks;
   a.chunk_vecs = cut.vecs;
+  // one launch where a group's rows fit a cluster, and its CTAs have little more to read each
+  const int64_t each = cluster_chunks(a.n_rows, a.beams), all = std::max<int64_t>(1, a.vocab / (16 / sizeof(T)));
+  bool cluster = false;
+  if (each > 0) {
+    const int64_t vecs = std::max<int64_t>(kLeastVecs, ((all + each - 1) / each + 31) / 32 * 32);
+    cluster = vecs <= std::min(cut.vecs + kSlack, kMostVecs);
+    if (cluster) {
+      a.chunk_vecs = (int32_t)vecs;
+      a.chunks = (int32_t)((all + vecs - 1) / vecs);
+    }
+  }
   a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
-  cudaError_t e = set_smem_attr_once(reinterpret_cast<const void*>(scan_kernel<T>), sizeof(float) * kMostVecs / kVecs);
-  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
-  if (e != cudaSuccess) return e;
-  e = launch_early(scan_kernel<T>, dim3((unsigned)(a.n_rows * (int64_t)a.chunks)), kScan, tops(a.chunk_vecs), 1, stream, a);
-  if (e != cudaSuccess) return e;
-  return launch_early(join_kernel, dim3(a.n_rows / a.beams), kThreads, join_bytes(a.k, a.beams * a.chunks), 1, stream, a);
+  return (int64_t)a.n_rows * a.chunks <= kWave ? launch_scan<T, 512>(a, cluster, stream) : launch_scan<T, 256>(a, cluster, stream);
 }
 
 }  // namespace
@@ -668,7 +686,7 @@ size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k) {
   int64_t most = 1;
   for (int elems : {4, 8}) {
     const int64_t all = std::max(1, vocab / elems), least = (all + kMostVecs - 1) / kMostVecs;
-    most = std::max(most, std::min(n_rows * ((all + kLeastVecs - 1) / kLeastVecs), std::max<int64_t>(kCtas, n_rows * least)));
+    most = std::max(most, std::min(n_rows * ((all + kLeastVecs - 1) / kLeastVecs), std::max<int64_t>(kWave, n_rows * least)));
   }
   return (size_t)most * (sizeof(BeamStat) + k * sizeof(BeamItem));
 }
