@@ -76,7 +76,7 @@ extern "C" {
 #define FP4IDX_BEAM_MAX_K 64
 #define FP4IDX_BEAM_MAX_VOCAB (1 << 19)
 #define FP4IDX_BEAM_MAX_ROWS (1 << 20)
-#define FP4IDX_FORK_MAX_ROWS 16384          /* rows of a page table, old and new */
+#define FP4IDX_FORK_MAX_ROWS 8192           /* rows of a page table, old and new */
 #define FP4IDX_MAX_POOL_PAGES (1 << 23)     /* fork and compaction: pages of a pool */
 #define FP4IDX_COPY_MAX_REGIONS 256         /* caches of one fp4idx_copy_pages call */
 #define FP4IDX_TOPK_NOALLOC_MAX_BYTES (16u * 1024u * 1024u) /* fixed scratch of fp4idx_topk_noalloc */
@@ -609,7 +609,7 @@ int fp4idx_beam_select(const void* logits, int32_t logits_type, int64_t logits_s
  * this call; what is missing is taken from free_pages at *free_head on, what is left over
  * is written just below *free_head.
  *   page_table  [n_old, max_pages] int32, cached_lens [n_old] int32, ratio 1..64
- *   parents     [n_new] int32;  n_old, n_new <= 16384
+ *   parents     [n_new] int32;  n_old, n_new <= 8192
  *   num_pages   pages of the pool (1..2^23); ids of the table and the list lie below it
  *   pinned      [ceil(num_pages/32)] uint32 bit patterns, nullable: bit p % 32 of word p / 32
  *               is set for a page that something else holds too (a prefix cache); it is

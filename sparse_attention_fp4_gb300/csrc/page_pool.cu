@@ -1,10 +1,12 @@
 // The page pool: page tables forked (shared, copied on write, freed) and compacted.
 //
-// Both kernels are one cluster of CTAs with one bit a page of the pool in shared memory, the bits
-// of adjacent pages dealt out over the CTAs (CTA c holds words [c << shift, (c + 1) << shift)).  Rows of
-// the tables are read by all CTAs; a page is marked where its bit lives, through distributed
-// shared memory.  Lists in ascending order of ids are then popcounts, one scan a CTA and one
-// exchange of the CTAs' sums.  Nothing is left in device memory from call to call.
+// Each kernel is one cluster of CTAs with bits for the pages of the pool in shared memory.  All CTAs read rows of the
+// table and mark pages; then CTA c has words [c << shift, (c + 1) << shift) of the marks, and lists of pages in
+// ascending order are popcounts, one scan a CTA and one exchange of the CTAs' sums.  Nothing is left in device
+// memory from call to call.  Where they fit, every CTA marks a full set of bits of its own, and the
+// sets are merged through distributed shared memory (a mark in another CTA's memory costs some four cycles of an
+// SM: 130,000 of them took 16 us of a compaction); larger pools are marked where the bits live.
+// Both are bound by latency: dependent loads, barriers of the cluster.
 #include <algorithm>
 
 #include "beam.cuh"
@@ -15,225 +17,237 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 16;
-constexpr int kStep = 128;  // columns that a warp takes at once
-constexpr int32_t kNone = INT32_MAX;
+constexpr int kLane = 4, kStep = 32 * kLane;  // columns that a lane, a warp takes at once
+constexpr uint32_t kHalf = 1u << 30;          // beside a row's pages: its last one is partly filled
+constexpr size_t kMaxSmem = 225 * 1024;
 
-struct Cluster {
-  int rank, ctas, shift;  // shift: log2 of the words of bits a CTA holds
-  uint32_t bits;          // shared-memory address of this CTA's words
+struct Marks {
+  int rank, ctas, shift;
+  bool full;     // every CTA has all the words
+  uint32_t* own;  // `sets` sets of words
 
-  __device__ uint32_t word(int32_t page) const {
-    const uint32_t w = (uint32_t)page >> 5;
-    return mma::map_shared(bits + ((w & ((1u << shift) - 1)) << 2), w >> shift);
-  }
-  __device__ void set(int32_t page) const {
-    asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(word(page)), "r"(1u << (page & 31)) : "memory");
-  }
-  __device__ void clear(int32_t page) const {
-    asm volatile("red.relaxed.cluster.shared::cluster.and.b32 [%0], %1;" ::"r"(word(page)), "r"(~(1u << (page & 31))) : "memory");
-  }
-  __device__ bool test(int32_t page) const {
-    uint32_t v;
-    asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(word(page)) : "memory");
-    return v >> (page & 31) & 1u;
-  }
-};
-
-// Sums over the CTA's threads (exclusive, and the total) and over the cluster's CTAs.
-struct Scan {
-  int32_t warp[kWarps];
-  int32_t total;
-};
-__device__ __forceinline__ int32_t exclusive(int32_t v, Scan& sm, int32_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int32_t s = v;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int32_t u = __shfl_up_sync(~0u, s, d);
-    if (lane >= d) s += u;
-  }
-  __syncthreads();  // (an earlier scan has been read)
-  if (lane == 31) sm.warp[warp] = s;
-  __syncthreads();
-  if (warp == 0) {
-    int32_t w = sm.warp[lane];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int32_t u = __shfl_up_sync(~0u, w, d);
-      if (lane >= d) w += u;
+  __device__ int words() const { return full ? ctas << shift : 1 << shift; }
+  __device__ int first() const { return full ? rank << shift : 0; }  // of this CTA's share in `own`
+  __device__ void set(int32_t page, int set) const {
+    uint32_t w = (uint32_t)page >> 5;
+    if (full) {
+      atomicOr(own + set * words() + w, 1u << (page & 31));
+    } else {
+      const uint32_t at = set * words() + (w & ((1u << shift) - 1));
+      asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(mma::map_shared(ptx::smem_addr(own + at), w >> shift)),
+                   "r"(1u << (page & 31))
+                   : "memory");
     }
-    sm.warp[lane] = w;
   }
+  // Word w of this CTA's share, of all CTAs' marks.
+  __device__ uint32_t merged(int w, int set) const {
+    const uint32_t* at = own + set * words() + first() + w;
+    if (!full || ctas == 1) return *at;
+    uint32_t v[kMaxCtas], all = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxCtas; c++) {
+      v[c] = 0;
+      if (c < ctas)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[c]) : "r"(mma::map_shared(ptx::smem_addr(at), c)) : "memory");
+    }
+#pragma unroll
+    for (int c = 0; c < kMaxCtas; c++) all |= v[c];
+    return all;
+  }
+};
+
+// The sum of the warps' values before this one, and of all; every lane gives its warp's.
+__device__ __forceinline__ int32_t before_warp(int32_t v, int32_t* table, int32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();  // (an earlier table has been read)
+  if (lane == 0) table[warp] = v;
   __syncthreads();
-  *total = sm.warp[kWarps - 1];
-  return s - v + (warp ? sm.warp[warp - 1] : 0);
+  const int32_t u = table[lane];
+  *total = __reduce_add_sync(~0u, u);
+  return __reduce_add_sync(~0u, lane < warp ? u : 0);
 }
 // Every CTA's value in all CTAs' tables; read them after the next cluster barrier.
-__device__ __forceinline__ void publish(const Cluster& cl, int32_t* table, int32_t v) {
-  if ((int)threadIdx.x < cl.ctas)
-    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mma::map_shared(ptx::smem_addr(table + cl.rank), threadIdx.x)), "r"(v)
+__device__ __forceinline__ void publish(const Marks& m, int32_t* table, int32_t v) {
+  if ((int)threadIdx.x < m.ctas)
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mma::map_shared(ptx::smem_addr(table + m.rank), threadIdx.x)), "r"(v)
                  : "memory");
 }
-__device__ __forceinline__ int32_t before_me(const Cluster& cl, const int32_t* table, int32_t* total) {
-  int32_t mine = 0, all = 0;
-  for (int c = 0; c < cl.ctas; c++) {
-    if (c == cl.rank) mine = all;
-    all += table[c];
-  }
-  *total = all;
-  return mine;
+__device__ __forceinline__ int32_t before_cta(const Marks& m, const int32_t* table, int32_t* total) {
+  const int lane = threadIdx.x & 31;
+  const int32_t u = lane < m.ctas ? table[lane] : 0;
+  *total = __reduce_add_sync(~0u, u);
+  return __reduce_add_sync(~0u, lane < m.rank ? u : 0);
 }
 
-// Pages of a row of `len` tokens, -1 if its length is negative or needs more than the table's columns.
+// Pages of a row of `len` tokens, with kHalf where the last is partly filled; -1 if its length is
+// negative or needs more than the table's columns.
 __device__ __forceinline__ int32_t pages_of(int32_t len, int32_t ratio, int32_t max_pages) {
-  const int32_t n = len / ratio / kPage + (len / ratio % kPage != 0);
-  return len < 0 || n > max_pages ? -1 : n;
+  const int32_t e = len / ratio, half = e % kPage != 0, n = e / kPage + half;
+  return len < 0 || n > max_pages ? -1 : n | (half ? (int32_t)kHalf : 0);
 }
+__device__ __forceinline__ int32_t count_of(int32_t pages) { return pages < 0 ? 0 : pages & ~kHalf; }
 
-// This thread's share of the CTA's words: `each` words from first on.
-struct Share {
+// This warp's words of the CTA's share.
+struct Run {
   int32_t first, last;
-  __device__ Share(const Cluster& cl) {
-    const int32_t words = 1 << cl.shift, each = (words + kThreads - 1) / kThreads;
-    first = min(words, (int)threadIdx.x * each);
+  __device__ explicit Run(const Marks& m) {
+    const int32_t words = 1 << m.shift, each = (words + kWarps - 1) / kWarps, warp = threadIdx.x >> 5;
+    first = min(words, warp * each);
     last = min(words, first + each);
   }
 };
+// f(place, page) for the set bits of a word, from place `at` on, each by its lane; returns the next place.
+template <class F>
+__device__ __forceinline__ int32_t list_bits(uint32_t bits, int32_t page0, int32_t at, F&& f) {
+  const int lane = threadIdx.x & 31;
+  if (bits >> lane & 1) f(at + __popc(bits & ((1u << lane) - 1)), page0 + lane);
+  return at + __popc(bits);
+}
+// Bits of the word that starts at page `p0` for pages in [0, n).
+__device__ __forceinline__ uint32_t below(int64_t p0, int32_t n) {
+  const int64_t k = n - p0;
+  return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
+}
+
+// f(row, first column) for the blocks of kStep columns of a table, a warp each.
+template <class F>
+__device__ __forceinline__ void each_block(const Marks& m, int32_t rows, int32_t max_pages, F&& f) {
+  const uint32_t blocks = (max_pages + kStep - 1) / kStep, all = rows * blocks, step = m.ctas * kWarps;
+  for (uint32_t u = m.rank * kWarps + (threadIdx.x >> 5); u < all; u += step) {
+    const uint32_t r = u / blocks;
+    f((int)r, (int)(u - r * blocks) * kStep);
+    if (all - u <= step) break;  // (u + step may not fit)
+  }
+}
+// A lane's entries of a block of a row with n pages, -1 behind them.
+__device__ __forceinline__ void load_block(const int32_t* row, int c0, int32_t n, int32_t (&page)[kLane]) {
+#pragma unroll
+  for (int j = 0; j < kLane; j++) {
+    const int c = c0 + j * 32 + (threadIdx.x & 31);
+    page[j] = c < n ? row[c] : -1;
+  }
+}
+// Marks a row's block; ids outside the pool are reported.
+__device__ __forceinline__ void mark_block(const Marks& m, const int32_t* row, int c0, int32_t n, int set, int32_t num_pages,
+                                           int32_t* status) {
+  if (c0 >= n) return;
+  int32_t page[kLane];
+  load_block(row, c0, n, page);
+#pragma unroll
+  for (int j = 0; j < kLane; j++) {
+    if ((uint32_t)page[j] < (uint32_t)num_pages) m.set(page[j], set);
+    else if (c0 + j * 32 + (int)(threadIdx.x & 31) < n) record_error(status, FP4IDX_ERR_BAD_PAGE);
+  }
+}
 
 // ---------------------------------------------------------------- fork
-struct ForkTables {
-  Scan scan;
-  int32_t freed[kMaxCtas];
-};
+constexpr int32_t kNoRow = INT32_MAX;
 
-__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int shift) {
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int shift, bool full) {
   extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ ForkTables sm;
+  __shared__ int32_t table[kWarps], freed[kMaxCtas];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* bits = smem;
-  int32_t* first = reinterpret_cast<int32_t*>(smem + (1 << shift));  // an old row's first new row
-  int32_t* copies = first + a.n_old;                                 // the new rows that get a page
-  const Cluster cl{(int)blockIdx.x, (int)gridDim.x, shift, ptx::smem_addr(bits)};
-  const bool lead = cl.rank == 0;
-  for (int i = tid; i < 1 << shift; i += kThreads) bits[i] = 0;
-  for (int i = tid; i < a.n_old; i += kThreads) first[i] = kNone;
+  const Marks m{(int)blockIdx.x, (int)gridDim.x, shift, full, smem};
+  constexpr int kGone = 0, kStays = 1;  // pages of rows from which none, or one at the least goes on
+  const int words = m.words();
+  int32_t* first = reinterpret_cast<int32_t*>(smem + 2 * words);  // an old row's first new row
+  int32_t* pages = first + a.n_old;
+  int16_t* parent = reinterpret_cast<int16_t*>(pages + a.n_old);
+  int16_t* copies = parent + a.n_new;  // the new rows that get a page of their own
+  const bool lead = m.rank == 0;
+  for (int i = tid; i < 2 * words; i += kThreads) smem[i] = 0;
+  for (int i = tid; i < a.n_old; i += kThreads) first[i] = kNoRow;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
+  for (int i = tid; i < a.n_old; i += kThreads) {
+    pages[i] = pages_of(a.cached[i], a.ratio, a.max_pages);
+    if (pages[i] < 0 && lead) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+  }
   for (int i = tid; i < a.n_new; i += kThreads) {
     const int32_t p = a.parents[i];
-    if (p >= 0 && p < a.n_old) atomicMin(&first[p], i);
+    const bool good = p >= 0 && p < a.n_old;
+    if (good) atomicMin(&first[p], i);
     else if (p != -1 && lead) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+    parent[i] = good ? (int16_t)p : (int16_t)-1;
   }
-  mma::cluster_sync();
+  if (full) __syncthreads();
+  else mma::cluster_sync();  // (all CTAs' words are clear)
 
-  // the half-filled page of new row i's parent (-1: it has none), and whether i gets one of its own
-  auto half_page = [&](int p, int32_t len, int32_t* col) {
-    const int32_t e = len / a.ratio;
-    *col = e / kPage;
-    return e % kPage ? a.page_table[(int64_t)p * a.max_pages + *col] : -1;
-  };
+  // whether new row i gets a page of its own for the partly filled `page` of its parent
   auto own_page = [&](int i, int p, int32_t page) {
     if ((uint32_t)page >= (uint32_t)a.num_pages) return false;
     return first[p] != i || (a.pinned && (a.pinned[page >> 5] >> (page & 31) & 1));
   };
-  const int blocks = (a.max_pages + kStep - 1) / kStep, warps = cl.ctas * kWarps, at = cl.rank * kWarps + warp;
-  // pages of the rows from which none goes on
-  for (int64_t u = at; u < (int64_t)a.n_old * blocks; u += warps) {
-    const int r = (int)(u / blocks), c0 = (int)(u - (int64_t)r * blocks) * kStep;
-    if (first[r] != kNone) continue;
-    const int32_t n = pages_of(a.cached[r], a.ratio, a.max_pages);
-    for (int c = c0 + lane; c < min(n, c0 + kStep); c += 32) {
-      const int32_t page = a.page_table[(int64_t)r * a.max_pages + c];
-      if ((uint32_t)page < (uint32_t)a.num_pages) cl.set(page);
-      else record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-    }
-    if (n < 0 && lane == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-  }
+  each_block(m, a.n_old, a.max_pages, [&](int r, int c0) {
+    mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(pages[r]), first[r] == kNoRow ? kGone : kStays,
+               a.num_pages, a.status);
+  });
   // the new rows, but for the pages that this call gives them
-  for (int64_t u = at; u < (int64_t)a.n_new * blocks; u += warps) {
-    const int i = (int)(u / blocks), c0 = (int)(u - (int64_t)i * blocks) * kStep, p = a.parents[i];
-    int32_t n = 0, len = 0, skip = -1;
-    if (p >= 0 && p < a.n_old) {
-      len = a.cached[p];
-      n = pages_of(len, a.ratio, a.max_pages);
-      if (n < 0) {
-        if (lane == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-        n = len = 0;
-      }
-      int32_t col;
-      if (n > 0 && own_page(i, p, half_page(p, len, &col))) skip = col;
+  each_block(m, a.n_new, a.max_pages, [&](int i, int c0) {
+    const int p = parent[i];
+    const int32_t has = p < 0 ? 0 : pages[p], n = count_of(has);
+    int32_t page[kLane];
+    load_block(a.page_table + (int64_t)p * a.max_pages, c0, n, page);
+#pragma unroll
+    for (int j = 0; j < kLane; j++) {
+      const int c = c0 + j * 32 + lane;
+      const bool given = has > 0 && (has & kHalf) && c == n - 1 && own_page(i, p, page[j]);
+      if (c < a.max_pages && !given) a.table_out[(int64_t)i * a.max_pages + c] = page[j];
     }
-    for (int c = c0 + lane; c < min(a.max_pages, c0 + kStep); c += 32)
-      if (c != skip) a.table_out[(int64_t)i * a.max_pages + c] = c < n ? a.page_table[(int64_t)p * a.max_pages + c] : -1;
-    if (c0 == 0 && lane == 0) a.cached_out[i] = len;
-  }
-  mma::cluster_sync();
-  // ... that the other rows hold too
-  for (int64_t u = at; u < (int64_t)a.n_old * blocks; u += warps) {
-    const int r = (int)(u / blocks), c0 = (int)(u - (int64_t)r * blocks) * kStep;
-    if (first[r] == kNone) continue;
-    const int32_t n = pages_of(a.cached[r], a.ratio, a.max_pages);
-    for (int c = c0 + lane; c < min(n, c0 + kStep); c += 32) {
-      const int32_t page = a.page_table[(int64_t)r * a.max_pages + c];
-      if ((uint32_t)page >= (uint32_t)a.num_pages) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-      else if (cl.test(page)) cl.clear(page);
-    }
-  }
+    if (c0 == 0 && lane == 0) a.cached_out[i] = has < 0 || p < 0 ? 0 : a.cached[p];
+  });
   // the rows that get a page, in order (every CTA for itself)
   int32_t n_copies = 0, n_rows = 0;
   for (int base = 0; base < a.n_new; base += kThreads) {
     const int i = base + tid;
-    bool goes = false, mine = false;
-    if (i < a.n_new) {
-      const int32_t p = a.parents[i];
-      if (p >= 0 && p < a.n_old) {
-        const int32_t len = a.cached[p];
-        goes = pages_of(len, a.ratio, a.max_pages) >= 0;
-        int32_t col;
-        mine = goes && own_page(i, p, half_page(p, len, &col));
-      }
-    }
+    const int p = i < a.n_new ? parent[i] : -1;
+    const int32_t has = p < 0 ? -1 : pages[p];
+    const bool mine = has > 0 && (has & kHalf) && own_page(i, p, a.page_table[(int64_t)p * a.max_pages + count_of(has) - 1]);
+    const uint32_t set = __ballot_sync(~0u, mine);
     int32_t n;
-    const int32_t c = n_copies + exclusive(mine, sm.scan, &n);
-    if (mine) copies[c] = i;
+    const int32_t c = n_copies + before_warp(__popc(set), table, &n) + __popc(set & ((1u << lane) - 1));
+    if (mine) copies[c] = (int16_t)i;
     n_copies += n;
-    n_rows += __syncthreads_count(goes);
+    n_rows += __syncthreads_count(has >= 0);
   }
   mma::cluster_sync();
-  // the pages that came back
-  const Share share(cl);
-  const int32_t w0 = cl.rank << shift;
+  // the pages that come back: this CTA's share, in place of its marks
+  const Run run(m);
+  const int32_t w0 = m.rank << shift;
+  uint32_t* back = smem + m.first();
   int32_t mine = 0;
-  for (int w = share.first; w < share.last; w++) {
-    uint32_t v = bits[w];
+  for (int w = run.first + lane; w < run.last; w += 32) {
+    uint32_t v = m.merged(w, kGone);
+    if (v) v &= ~m.merged(w, kStays);
     if (v && a.pinned) v &= ~a.pinned[w0 + w];
-    bits[w] = v;
+    back[w] = v;
     mine += __popc(v);
   }
   int32_t freed_here, n_freed;
-  int32_t f = exclusive(mine, sm.scan, &freed_here);
-  publish(cl, sm.freed, freed_here);
+  int32_t f = before_warp(__reduce_add_sync(~0u, mine), table, &freed_here);
+  publish(m, freed, freed_here);
   mma::cluster_sync();
-  f += before_me(cl, sm.freed, &n_freed);
+  f += before_cta(m, freed, &n_freed);
   const int32_t head_in = a.free_head ? *a.free_head : 0;
   const bool good_head = head_in >= 0 && head_in <= a.n_free;
   const int32_t head = good_head ? head_in : 0, avail = good_head ? a.n_free - head : 0;
   const int32_t n_given = (int32_t)min((int64_t)n_copies, (int64_t)n_freed + avail);
   const int32_t left = max(0, n_freed - n_copies), listed = min(left, head), lost = left - listed;
   auto give = [&](int c, int32_t page) {
-    const int i = copies[c], p = a.parents[i];
-    int32_t col;
-    a.copy_src[c] = half_page(p, a.cached[p], &col);
+    const int i = copies[c], p = parent[i];
+    const int64_t col = count_of(pages[p]) - 1;
+    a.copy_src[c] = a.page_table[(int64_t)p * a.max_pages + col];
     a.copy_dst[c] = page;
     a.table_out[(int64_t)i * a.max_pages + col] = page;
   };
-  for (int w = share.first; w < share.last; w++)
-    for (uint32_t v = bits[w]; v; v &= v - 1, f++) {
-      const int32_t page = (w0 + w) * 32 + __ffs(v) - 1;
-      if (f < n_copies) give(f, page);
-      else if (f - n_copies >= lost) a.free_pages[head - listed + (f - n_copies - lost)] = page;
-    }
+  for (int w = run.first; w < run.last; w++) {
+    if (back[w] == 0) continue;
+    f = list_bits(back[w], (w0 + w) * 32, f, [&](int32_t at, int32_t page) {
+      if (at < n_copies) give(at, page);
+      else if (at - n_copies >= lost) a.free_pages[head - listed + (at - n_copies - lost)] = page;
+    });
+  }
   if (!lead) return;
   for (int c = n_freed + tid; c < n_given; c += kThreads) {
     const int32_t page = a.free_pages[head + (c - n_freed)];
@@ -256,125 +270,124 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
 }
 
 // ---------------------------------------------------------------- compaction
-struct CompactTables {
-  Scan scan;
-  int32_t used[kMaxCtas], holes[kMaxCtas], movers[kMaxCtas], spare[kMaxCtas], end[kMaxCtas];
-};
-
-// Bits of the word that starts at page `p0` for pages in [0, n).
-__device__ __forceinline__ uint32_t below(int64_t p0, int32_t n) {
-  const int64_t k = n - p0;
-  return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
-}
-
-__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a, int shift) {
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs a, int shift, bool full) {
   extern __shared__ __align__(16) uint32_t smem[];
-  __shared__ CompactTables sm;
+  __shared__ int32_t table[kWarps], used_by[kMaxCtas], holes_by[kMaxCtas], movers_by[kMaxCtas], spare_by[kMaxCtas], end_by[kMaxCtas];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t* bits = smem;
-  const Cluster cl{(int)blockIdx.x, (int)gridDim.x, shift, ptx::smem_addr(bits)};
-  const bool lead = cl.rank == 0;
-  const int32_t w0 = cl.rank << shift;
-  const Share share(cl);
+  const Marks m{(int)blockIdx.x, (int)gridDim.x, shift, full, smem};
+  const bool lead = m.rank == 0;
+  for (int i = tid; i < m.words(); i += kThreads) smem[i] = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto pins = [&](int w) { return a.pinned && (int64_t)(w0 + w) * 32 < a.num_pages ? a.pinned[w0 + w] : 0u; };
-  for (int i = tid; i < 1 << shift; i += kThreads) bits[i] = pins(i) & below((int64_t)(w0 + i) * 32, a.num_pages);
-  mma::cluster_sync();
-  const int blocks = (a.max_pages + kStep - 1) / kStep, warps = cl.ctas * kWarps, at = cl.rank * kWarps + warp;
-  for (int64_t u = at; u < (int64_t)a.n_seqs * blocks; u += warps) {
-    const int r = (int)(u / blocks), c0 = (int)(u - (int64_t)r * blocks) * kStep;
+  if (full) __syncthreads();
+  else mma::cluster_sync();
+  each_block(m, a.n_seqs, a.max_pages, [&](int r, int c0) {
     const int32_t n = pages_of(a.cached[r], a.ratio, a.max_pages);
-    for (int c = c0 + lane; c < min(n, c0 + kStep); c += 32) {
-      const int32_t page = a.page_table[(int64_t)r * a.max_pages + c];
-      if ((uint32_t)page < (uint32_t)a.num_pages) cl.set(page);
-      else record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-    }
     if (n < 0 && lane == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+    mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(n), 0, a.num_pages, a.status);
+  });
+  mma::cluster_sync();
+  // this CTA's share of the pages in use, in place of its marks
+  const Run run(m);
+  const int32_t w0 = m.rank << shift;
+  uint32_t* bits = smem + m.first();
+  auto page0 = [&](int w) { return (int64_t)(w0 + w) * 32; };
+  auto pins = [&](int w) { return a.pinned && page0(w) < a.num_pages ? a.pinned[w0 + w] & below(page0(w), a.num_pages) : 0u; };
+  int32_t n = 0, here, used;
+  for (int w = run.first + lane; w < run.last; w += 32) {
+    const uint32_t v = m.merged(w, 0) | pins(w);
+    bits[w] = v;
+    n += __popc(v);
   }
+  before_warp(__reduce_add_sync(~0u, n), table, &here);
+  publish(m, used_by, here);
   mma::cluster_sync();
-  int32_t v = 0, here, used;
-  for (int w = share.first; w < share.last; w++) v += __popc(bits[w]);
-  exclusive(v, sm.scan, &here);
-  publish(cl, sm.used, here);
-  mma::cluster_sync();
-  before_me(cl, sm.used, &used);
+  before_cta(m, used_by, &used);
   // ids below `used` that are free, and pages from there on that may move
-  auto holes = [&](int w) { return ~bits[w] & below((int64_t)(w0 + w) * 32, used); };
-  auto movers = [&](int w) { return bits[w] & ~below((int64_t)(w0 + w) * 32, used) & ~pins(w); };
-  int32_t nh = 0, nm = 0, here_h, here_m, all_h, all_m;
-  for (int w = share.first; w < share.last; w++) nh += __popc(holes(w)), nm += __popc(movers(w));
-  int32_t h = exclusive(nh, sm.scan, &here_h);
-  int32_t m = exclusive(nm, sm.scan, &here_m);
-  publish(cl, sm.holes, here_h);
-  publish(cl, sm.movers, here_m);
+  auto holes = [&](int w) { return ~bits[w] & below(page0(w), used); };
+  auto movers = [&](int w) {
+    const uint32_t v = bits[w] & ~below(page0(w), used);
+    return v ? v & ~pins(w) : 0u;
+  };
+  int32_t nh = 0, nm = 0, here_h, here_m, all_m, unused;
+  for (int w = run.first + lane; w < run.last; w += 32) nh += __popc(holes(w)), nm += __popc(movers(w));
+  int32_t h = before_warp(__reduce_add_sync(~0u, nh), table, &here_h);
+  int32_t v = before_warp(__reduce_add_sync(~0u, nm), table, &here_m);
+  publish(m, holes_by, here_h);
+  publish(m, movers_by, here_m);
   mma::cluster_sync();
-  h += before_me(cl, sm.holes, &all_h);
-  m += before_me(cl, sm.movers, &all_m);
+  h += before_cta(m, holes_by, &unused);
+  v += before_cta(m, movers_by, &all_m);
   const int32_t moves = min(all_m, a.max_moves);  // (there are at least as many holes as movers)
-  int32_t last = 0, free_here = 0;
-  const int32_t m0 = m;
-  for (int w = share.first; w < share.last; w++) {
-    const int32_t p0 = (w0 + w) * 32;
+  const int32_t first_mover = v;
+  int32_t last = 0, spare = 0;
+  for (int w = run.first; w < run.last; w++) {
+    const int32_t p0 = (int32_t)page0(w);
+    const uint32_t open = holes(w), from = movers(w);
     uint32_t now = bits[w];
-    for (uint32_t x = holes(w); x; x &= x - 1, h++)
-      if (h < moves) {
-        a.move_dst[h] = p0 + __ffs(x) - 1;
-        now |= x & -x;
-      }
-    for (uint32_t x = movers(w); x; x &= x - 1, m++)
-      if (m < moves) {
-        a.move_src[m] = p0 + __ffs(x) - 1;
-        now &= ~(x & -x);
-      }
-    bits[w] = now;
+    if (open) {
+      bool fills = false;
+      h = list_bits(open, p0, h, [&](int32_t at, int32_t page) {
+        fills = at < moves;
+        if (fills) a.move_dst[at] = page;
+      });
+      now |= __ballot_sync(~0u, fills);
+    }
+    if (from) {
+      bool goes = false;
+      v = list_bits(from, p0, v, [&](int32_t at, int32_t page) {
+        goes = at < moves;
+        if (goes) a.move_src[at] = page;
+      });
+      now &= ~__ballot_sync(~0u, goes);
+    }
+    __syncwarp();
+    if (lane == 0) bits[w] = now;
     if (now) last = p0 + 32 - __clz(now);
-    free_here += __popc(~now & below(p0, a.num_pages));
+    spare += __popc(~now & below(p0, a.num_pages));
   }
-  int32_t spare, all_spare;
-  int32_t f = exclusive(free_here, sm.scan, &spare);
-  for (int d = 16; d; d >>= 1) last = max(last, __shfl_xor_sync(~0u, last, d));
+  int32_t here_spare, all_spare;
+  int32_t f = before_warp(spare, table, &here_spare);
+  publish(m, spare_by, here_spare);
   __syncthreads();
-  if (lane == 0) sm.scan.warp[warp] = last;
+  if (lane == 0) table[warp] = last;
   __syncthreads();
-  int32_t end = 0;
-  for (int w = 0; w < kWarps; w++) end = max(end, sm.scan.warp[w]);
-  publish(cl, sm.spare, spare);
-  publish(cl, sm.end, end);
+  publish(m, end_by, (int32_t)__reduce_max_sync(~0u, (uint32_t)table[lane]));
   mma::cluster_sync();
-  f += before_me(cl, sm.spare, &all_spare);
-  for (int c = 0; c < cl.ctas; c++) end = max(end, sm.end[c]);
-  // where the moved pages went
-  for (int m1 = m0; m1 < min(m, moves); m1++) a.remap[a.move_src[m1]] = a.move_dst[m1];
-  // the free list
+  f += before_cta(m, spare_by, &all_spare);
+  const int32_t end = (int32_t)__reduce_max_sync(~0u, lane < m.ctas ? (uint32_t)end_by[lane] : 0u);
+  // where the pages from `used` on are now: those of this CTA's share that move, and those that stay
+  for (int i = first_mover + lane; i < min(v, moves); i += 32) a.remap[a.move_src[i]] = a.move_dst[i];
   const int32_t listed = min(all_spare, a.n_free), lost = all_spare - listed, head = a.n_free - listed;
-  for (int w = share.first; w < share.last; w++)
-    for (uint32_t x = ~bits[w] & below((int64_t)(w0 + w) * 32, a.num_pages); x; x &= x - 1, f++)
-      if (f >= lost) a.free_pages[head + f - lost] = (w0 + w) * 32 + __ffs(x) - 1;
+  for (int w = run.first; w < run.last; w++) {
+    const uint32_t now = bits[w], stay = now & ~below(page0(w), used);
+    if (stay >> lane & 1) a.remap[page0(w) + lane] = (int32_t)page0(w) + lane;
+    f = list_bits(~now & below(page0(w), a.num_pages), (int32_t)page0(w), f, [&](int32_t at, int32_t page) {
+      if (at >= lost) a.free_pages[head + at - lost] = page;
+    });
+  }
   mma::cluster_sync();
-  for (int64_t u = at; u < (int64_t)a.n_seqs * blocks; u += warps) {
-    const int r = (int)(u / blocks), c0 = (int)(u - (int64_t)r * blocks) * kStep;
-    const int32_t n = pages_of(a.cached[r], a.ratio, a.max_pages);
-    for (int c = c0 + lane; c < min(a.max_pages, c0 + kStep); c += 32) {
-      int32_t page = -1;
-      if (c < n) {
-        page = a.page_table[(int64_t)r * a.max_pages + c];
-        if (page >= used && page < a.num_pages && !cl.test(page)) page = a.remap[page];
-      }
-      a.table_out[(int64_t)r * a.max_pages + c] = page;
+  each_block(m, a.n_seqs, a.max_pages, [&](int r, int c0) {
+    int32_t page[kLane];
+    load_block(a.page_table + (int64_t)r * a.max_pages, c0, count_of(pages_of(a.cached[r], a.ratio, a.max_pages)), page);
+#pragma unroll
+    for (int j = 0; j < kLane; j++)
+      if (page[j] >= used && page[j] < a.num_pages) page[j] = a.remap[page[j]];
+#pragma unroll
+    for (int j = 0; j < kLane; j++) {
+      const int c = c0 + j * 32 + lane;
+      if (c < a.max_pages) a.table_out[(int64_t)r * a.max_pages + c] = page[j];
     }
+  });
+  if (!lead) return;
+  for (int c = moves + tid; c < a.max_moves; c += kThreads) a.move_src[c] = a.move_dst[c] = -1;
+  if (tid == 0) {
+    if (lost > 0) record_error(a.status, FP4IDX_ERR_CAPACITY);
+    a.counts[0] = moves;
+    a.counts[1] = used;
+    a.counts[2] = end;
+    a.counts[3] = head;
   }
-  if (lead) {
-    for (int c = moves + tid; c < a.max_moves; c += kThreads) a.move_src[c] = a.move_dst[c] = -1;
-    if (tid == 0) {
-      if (lost > 0) record_error(a.status, FP4IDX_ERR_CAPACITY);
-      a.counts[0] = moves;
-      a.counts[1] = used;
-      a.counts[2] = end;
-      a.counts[3] = head;
-    }
-  }
-  mma::cluster_sync();  // no CTA ends while another reads its bits
 }
 
 int log2_from(int64_t n) {
@@ -383,35 +396,44 @@ int log2_from(int64_t n) {
   return s;
 }
 
-// CTAs of a call
-int ctas_of(int64_t entries, int64_t pool) { return entries > 16384 || pool > (1 << 18) ? kMaxCtas : 1; }
+// CTAs of a call: one for every so many entries of its tables
+constexpr int64_t kEntries = 2048;
+
+int ctas_of(int64_t entries, int64_t pool) {
+  if (pool > (1 << 19)) return kMaxCtas;
+  int c = 1;
+  while (c < kMaxCtas && c * kEntries < entries) c *= 2;
+  return c;
+}
 
 template <class A>
-cudaError_t launch(void (*kernel)(A, int), const A& a, int ctas, int64_t rows, cudaStream_t stream) {
+cudaError_t launch(void (*kernel)(A, int, bool), const A& a, int sets, int64_t entries, size_t rows, cudaStream_t stream) {
   const int64_t words = ((int64_t)a.num_pages + 31) / 32;
+  const int ctas = ctas_of(entries, a.num_pages);
   const int shift = log2_from((words + ctas - 1) / ctas);
-  const size_t smem = 4 * (((size_t)1 << shift) + rows);
+  const size_t part = 4 * ((size_t)sets << shift);
+  const bool full = part * ctas + rows <= kMaxSmem;
+  const size_t smem = (full ? part * ctas : part) + rows;
   const void* f = reinterpret_cast<const void*>(kernel);
-  cudaError_t e = set_smem_attr_once(f, 220 * 1024);
+  cudaError_t e = set_smem_attr_once(f, kMaxSmem);
   if (e != cudaSuccess) return e;
   if (ctas > 8) {
     int fit = 0;  // (asks for clusters above the portable size)
-    e = resident_clusters(f, ctas, kThreads, 220 * 1024, &fit);
+    e = resident_clusters(f, ctas, kThreads, kMaxSmem, &fit);
     if (e != cudaSuccess) return e;
     if (fit < 1) return cudaErrorInvalidClusterSize;
   }
-  return launch_early(kernel, dim3(ctas), kThreads, smem, ctas, stream, a, shift);
+  return launch_early(kernel, dim3(ctas), kThreads, smem, ctas, stream, a, shift, full);
 }
 
 }  // namespace
 
 cudaError_t launch_fork_pages(const ForkArgs& a, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.n_old + a.n_new;
-  return launch(fork_kernel, a, ctas_of(rows * a.max_pages, a.num_pages), rows, stream);
+  return launch(fork_kernel, a, 2, ((int64_t)a.n_old + a.n_new) * a.max_pages, 8 * (size_t)a.n_old + 4 * (size_t)a.n_new, stream);
 }
 
 cudaError_t launch_compact_pages(const CompactArgs& a, cudaStream_t stream) {
-  return launch(compact_kernel, a, ctas_of((int64_t)a.n_seqs * a.max_pages, a.num_pages), 0, stream);
+  return launch(compact_kernel, a, 1, (int64_t)a.n_seqs * a.max_pages, 0, stream);
 }
 
 }  // namespace fp4idx

@@ -62,7 +62,7 @@ def test_fork_pages(lib):
         assert f(**{name: None}) == INVALID, name
     for name in ("table", "cached", "parents", "pinned", "free", "head", "table_out", "cached_out", "src", "dst", "counts", "status"):
         assert f(**{name: M2}) == INVALID, name
-    for kw in (dict(n_old=16385), dict(n_new=16385), dict(pool=(1 << 23) + 1), dict(max_pages=1 << 26), dict(n_free=1 << 31)):
+    for kw in (dict(n_old=8193), dict(n_new=8193), dict(pool=(1 << 23) + 1), dict(max_pages=1 << 26), dict(n_free=1 << 31)):
         assert f(**kw) == UNSUPPORTED, kw
 
 

@@ -97,7 +97,7 @@ def test_fork_of_many_rows(rows):
 
 
 def test_fork_of_the_most_rows():
-    rows = 16384
+    rows = 8192
     table, cached, ids = state(8, rows, 2, 1, rows * 3 + 5)
     check_fork(table, cached, 1, pick(1, rows, rows, 0.1), rows * 3 + 5, [-9] * rows * 2 + ids, rows * 2)
 
