@@ -55,9 +55,10 @@ cudaError_t launch_compact_pages(const CompactArgs& a, cudaStream_t stream);
 struct Regions {
   uint8_t* base[FP4IDX_COPY_MAX_REGIONS];
   int32_t vecs[FP4IDX_COPY_MAX_REGIONS];  // 16-byte pieces of a page
+  int32_t each[FP4IDX_COPY_MAX_REGIONS], first[FP4IDX_COPY_MAX_REGIONS];  // filled in by the launcher
   int32_t n;
 };
 cudaError_t launch_move_pages(const int32_t* src, const int32_t* dst, int64_t n_copies, const int32_t* count,
-                              const Regions& regions, int64_t num_pages, int32_t* status, cudaStream_t stream);
+                              Regions& regions, int64_t num_pages, int32_t* status, cudaStream_t stream);
 
 }  // namespace fp4idx

@@ -17,7 +17,7 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxCtas = 16;
-constexpr int kLane = 4, kStep = 32 * kLane;  // columns that a lane, a warp takes at once
+constexpr int kLane = 8, kStep = 32 * kLane;  // columns that a lane, a warp takes at once
 constexpr uint32_t kHalf = 1u << 30;          // beside a row's pages: its last one is partly filled
 constexpr size_t kMaxSmem = 225 * 1024;
 
@@ -47,8 +47,11 @@ struct Marks {
 #pragma unroll
     for (int c = 0; c < kMaxCtas; c++) {
       v[c] = 0;
-      if (c < ctas)
-        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[c]) : "r"(mma::map_shared(ptx::smem_addr(at), c)) : "memory");
+      if (c < ctas)  // (each CTA begins with itself, so that they do not all read the same one)
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(v[c])
+                     : "r"(mma::map_shared(ptx::smem_addr(at), (rank + c) & (ctas - 1)))
+                     : "memory");
     }
 #pragma unroll
     for (int c = 0; c < kMaxCtas; c++) all |= v[c];
@@ -109,14 +112,27 @@ __device__ __forceinline__ uint32_t below(int64_t p0, int32_t n) {
   return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
 }
 
-// f(row, first column) for the blocks of kStep columns of a table, a warp each.
-template <class F>
-__device__ __forceinline__ void each_block(const Marks& m, int32_t rows, int32_t max_pages, F&& f) {
+// f(row, first column, of(row)) for the blocks of kStep columns of a table, a warp each; of(row) is called a block ahead.
+// `back`: the warps in reverse order, so that two short tables are read by different warps.
+template <class Of, class F>
+__device__ __forceinline__ void each_block(const Marks& m, bool back, int32_t rows, int32_t max_pages, Of&& of, F&& f) {
   const uint32_t blocks = (max_pages + kStep - 1) / kStep, all = rows * blocks, step = m.ctas * kWarps;
-  for (uint32_t u = m.rank * kWarps + (threadIdx.x >> 5); u < all; u += step) {
-    const uint32_t r = u / blocks;
-    f((int)r, (int)(u - r * blocks) * kStep);
-    if (all - u <= step) break;  // (u + step may not fit)
+  const uint32_t at = m.rank * kWarps + (threadIdx.x >> 5);
+  uint32_t u = back ? step - 1 - at : at;
+  if (u >= all) return;
+  uint32_t r = u / blocks;
+  int32_t value = of((int)r);
+  while (true) {
+    const uint32_t c0 = (u - r * blocks) * kStep, here = r;
+    const int32_t now = value;
+    const bool more = all - u > step;
+    if (more) {
+      u += step;
+      r = u / blocks;
+      value = of((int)r);
+    }
+    f((int)here, (int)c0, now);
+    if (!more) return;
   }
 }
 // A lane's entries of a block of a row with n pages, -1 behind them.
@@ -159,6 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
   for (int i = tid; i < a.n_old; i += kThreads) first[i] = kNoRow;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int32_t head_in = a.free_head ? *a.free_head : 0;
   __syncthreads();
   for (int i = tid; i < a.n_old; i += kThreads) {
     pages[i] = pages_of(a.cached[i], a.ratio, a.max_pages);
@@ -179,13 +196,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
     if ((uint32_t)page >= (uint32_t)a.num_pages) return false;
     return first[p] != i || (a.pinned && (a.pinned[page >> 5] >> (page & 31) & 1));
   };
-  each_block(m, a.n_old, a.max_pages, [&](int r, int c0) {
-    mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(pages[r]), first[r] == kNoRow ? kGone : kStays,
-               a.num_pages, a.status);
+  each_block(m, false, a.n_old, a.max_pages, [&](int r) { return pages[r]; }, [&](int r, int c0, int32_t has) {
+    mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(has), first[r] == kNoRow ? kGone : kStays, a.num_pages,
+               a.status);
   });
   // the new rows, but for the pages that this call gives them
-  each_block(m, a.n_new, a.max_pages, [&](int i, int c0) {
-    const int p = parent[i];
+  each_block(m, true, a.n_new, a.max_pages, [&](int i) { return (int32_t)parent[i]; }, [&](int i, int c0, int32_t p) {
     const int32_t has = p < 0 ? 0 : pages[p], n = count_of(has);
     int32_t page[kLane];
     load_block(a.page_table + (int64_t)p * a.max_pages, c0, n, page);
@@ -229,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
   publish(m, freed, freed_here);
   mma::cluster_sync();
   f += before_cta(m, freed, &n_freed);
-  const int32_t head_in = a.free_head ? *a.free_head : 0;
   const bool good_head = head_in >= 0 && head_in <= a.n_free;
   const int32_t head = good_head ? head_in : 0, avail = good_head ? a.n_free - head : 0;
   const int32_t n_given = (int32_t)min((int64_t)n_copies, (int64_t)n_freed + avail);
@@ -281,8 +296,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (full) __syncthreads();
   else mma::cluster_sync();
-  each_block(m, a.n_seqs, a.max_pages, [&](int r, int c0) {
-    const int32_t n = pages_of(a.cached[r], a.ratio, a.max_pages);
+  auto len_of = [&](int r) { return a.cached[r]; };
+  each_block(m, false, a.n_seqs, a.max_pages, len_of, [&](int r, int c0, int32_t len) {
+    const int32_t n = pages_of(len, a.ratio, a.max_pages);
     if (n < 0 && lane == 0) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
     mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(n), 0, a.num_pages, a.status);
   });
@@ -367,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
     });
   }
   mma::cluster_sync();
-  each_block(m, a.n_seqs, a.max_pages, [&](int r, int c0) {
+  each_block(m, false, a.n_seqs, a.max_pages, len_of, [&](int r, int c0, int32_t len) {
     int32_t page[kLane];
-    load_block(a.page_table + (int64_t)r * a.max_pages, c0, count_of(pages_of(a.cached[r], a.ratio, a.max_pages)), page);
+    load_block(a.page_table + (int64_t)r * a.max_pages, c0, count_of(pages_of(len, a.ratio, a.max_pages)), page);
 #pragma unroll
     for (int j = 0; j < kLane; j++)
       if (page[j] >= used && page[j] < a.num_pages) page[j] = a.remap[page[j]];

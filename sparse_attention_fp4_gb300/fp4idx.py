@@ -10,8 +10,8 @@ fallback.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
+from array import array
 
 import torch
 
@@ -651,15 +651,14 @@ def copy_pages(src, dst, caches, count=None, status=None, stream=None):
     dev, on = _here(stream)
     n, m = src.numel(), len(caches)
     pages = caches[0].shape[0] if m else 0
-    base, size = (_vp * m)(), (_i64 * m)()
-    for i, c in enumerate(caches):
-        if c.get_device() != dev or not c.is_contiguous() or c.dim() < 1 or c.shape[0] != pages:
+    for c in caches:
+        if c.get_device() != dev or not c.is_contiguous() or c.shape[0] != pages:
             raise ValueError("caches must be contiguous CUDA tensors on the current device, of one number of pages")
-        base[i] = c.data_ptr()
-        size[i] = math.prod(c.shape[1:]) * c.element_size()
+    each = pages or 1
+    base, size = array("Q", [c.data_ptr() for c in caches]), array("q", [c.nbytes // each for c in caches])
     rc = _lib.fp4idx_copy_pages(
         _addr(src, "src", _I32, 0, dev), _addr(dst, "dst", _I32, n, dev), n,
-        None if count is None else _addr(count, "count", _I32, 1, dev), base, size, m, pages,
+        None if count is None else _addr(count, "count", _I32, 1, dev), base.buffer_info()[0], size.buffer_info()[0], m, pages,
         None if status is None else _addr(status, "status", _I32, 1, dev), on)
     _check("fp4idx_copy_pages", rc)
 
