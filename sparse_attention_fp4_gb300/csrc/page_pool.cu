@@ -39,23 +39,28 @@ struct Marks {
                    : "memory");
     }
   }
-  // Word w of this CTA's share, of all CTAs' marks.
-  __device__ uint32_t merged(int w, int set) const {
-    const uint32_t* at = own + set * words() + first() + w;
-    if (!full || ctas == 1) return *at;
-    uint32_t v[kMaxCtas], all = 0;
+  // Word w of this CTA's share, of all CTAs' marks, in each of `kSets` sets.
+  template <int kSets>
+  __device__ void merged(int w, uint32_t (&all)[kSets]) const {
+    uint32_t v[kSets][kMaxCtas];
 #pragma unroll
-    for (int c = 0; c < kMaxCtas; c++) {
-      v[c] = 0;
-      if (c < ctas)  // (each CTA begins with itself, so that they do not all read the same one)
-        asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                     : "=r"(v[c])
-                     : "r"(mma::map_shared(ptx::smem_addr(at), (rank + c) & (ctas - 1)))
-                     : "memory");
+    for (int s = 0; s < kSets; s++)
+#pragma unroll
+      for (int c = 0; c < kMaxCtas; c++) {
+        const uint32_t* at = own + s * words() + first() + w;
+        v[s][c] = c == 0 ? *at : 0;
+        if (c > 0 && full && c < ctas)  // (each CTA begins behind itself, so that they do not all read the same one)
+          asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                       : "=r"(v[s][c])
+                       : "r"(mma::map_shared(ptx::smem_addr(at), (rank + c) & (ctas - 1)))
+                       : "memory");
+      }
+#pragma unroll
+    for (int s = 0; s < kSets; s++) {
+      all[s] = 0;
+#pragma unroll
+      for (int c = 0; c < kMaxCtas; c++) all[s] |= v[s][c];
     }
-#pragma unroll
-    for (int c = 0; c < kMaxCtas; c++) all |= v[c];
-    return all;
   }
 };
 
@@ -99,16 +104,9 @@ struct Run {
     last = min(words, first + each);
   }
 };
-// f(place, page) for the set bits of a word, from place `at` on, each by its lane; returns the next place.
-template <class F>
-__device__ __forceinline__ int32_t list_bits(uint32_t bits, int32_t page0, int32_t at, F&& f) {
-  const int lane = threadIdx.x & 31;
-  if (bits >> lane & 1) f(at + __popc(bits & ((1u << lane) - 1)), page0 + lane);
-  return at + __popc(bits);
-}
 // Bits of the word that starts at page `p0` for pages in [0, n).
-__device__ __forceinline__ uint32_t below(int64_t p0, int32_t n) {
-  const int64_t k = n - p0;
+__device__ __forceinline__ uint32_t below(int32_t p0, int32_t n) {
+  const int32_t k = n - p0;
   return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u;
 }
 
@@ -177,16 +175,18 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int32_t head_in = a.free_head ? *a.free_head : 0;
   __syncthreads();
-  for (int i = tid; i < a.n_old; i += kThreads) {
-    pages[i] = pages_of(a.cached[i], a.ratio, a.max_pages);
-    if (pages[i] < 0 && lead) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
-  }
-  for (int i = tid; i < a.n_new; i += kThreads) {
-    const int32_t p = a.parents[i];
-    const bool good = p >= 0 && p < a.n_old;
-    if (good) atomicMin(&first[p], i);
-    else if (p != -1 && lead) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
-    parent[i] = good ? (int16_t)p : (int16_t)-1;
+  for (int i = tid; i < max(a.n_old, a.n_new); i += kThreads) {
+    const int32_t len = i < a.n_old ? a.cached[i] : 0, p = i < a.n_new ? a.parents[i] : -1;
+    if (i < a.n_old) {
+      pages[i] = pages_of(len, a.ratio, a.max_pages);
+      if (pages[i] < 0 && lead) record_error(a.status, FP4IDX_ERR_BAD_LENGTH);
+    }
+    if (i < a.n_new) {
+      const bool good = p >= 0 && p < a.n_old;
+      if (good) atomicMin(&first[p], i);
+      else if (p != -1 && lead) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+      parent[i] = good ? (int16_t)p : (int16_t)-1;
+    }
   }
   if (full) __syncthreads();
   else mma::cluster_sync();  // (all CTAs' words are clear)
@@ -232,14 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
   const Run run(m);
   const int32_t w0 = m.rank << shift;
   uint32_t* back = smem + m.first();
-  int32_t mine = 0;
-  for (int w = run.first + lane; w < run.last; w += 32) {
-    uint32_t v = m.merged(w, kGone);
-    if (v) v &= ~m.merged(w, kStays);
-    if (v && a.pinned) v &= ~a.pinned[w0 + w];
-    back[w] = v;
-    mine += __popc(v);
+  for (int w = tid; w < 1 << shift; w += kThreads) {
+    const uint32_t pin = a.pinned && w0 + w < (a.num_pages + 31) / 32 ? a.pinned[w0 + w] : 0u;
+    uint32_t held[2];
+    m.merged(w, held);
+    back[w] = held[kGone] & ~held[kStays] & ~pin;
   }
+  __syncthreads();
+  int32_t mine = 0;
+  for (int w = run.first + lane; w < run.last; w += 32) mine += __popc(back[w]);
   int32_t freed_here, n_freed;
   int32_t f = before_warp(__reduce_add_sync(~0u, mine), table, &freed_here);
   publish(m, freed, freed_here);
@@ -249,24 +250,31 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const ForkArgs a, int
   const int32_t head = good_head ? head_in : 0, avail = good_head ? a.n_free - head : 0;
   const int32_t n_given = (int32_t)min((int64_t)n_copies, (int64_t)n_freed + avail);
   const int32_t left = max(0, n_freed - n_copies), listed = min(left, head), lost = left - listed;
-  auto give = [&](int c, int32_t page) {
+  auto give = [&](int c, int32_t page) {  // copy_dst[c] is written
     const int i = copies[c], p = parent[i];
     const int64_t col = count_of(pages[p]) - 1;
     a.copy_src[c] = a.page_table[(int64_t)p * a.max_pages + col];
-    a.copy_dst[c] = page;
     a.table_out[(int64_t)i * a.max_pages + col] = page;
   };
+  int32_t unused;
+  const int32_t first_here = before_cta(m, freed, &unused);
   for (int w = run.first; w < run.last; w++) {
-    if (back[w] == 0) continue;
-    f = list_bits(back[w], (w0 + w) * 32, f, [&](int32_t at, int32_t page) {
-      if (at < n_copies) give(at, page);
+    const uint32_t v = back[w];
+    if (v == 0) continue;
+    if (v >> lane & 1) {
+      const int32_t at = f + __popc(v & ((1u << lane) - 1)), page = (w0 + w) * 32 + lane;
+      if (at < n_copies) a.copy_dst[at] = page;
       else if (at - n_copies >= lost) a.free_pages[head - listed + (at - n_copies - lost)] = page;
-    });
+    }
+    f += __popc(v);
   }
+  __syncthreads();
+  for (int c = first_here + tid; c < min(first_here + freed_here, n_copies); c += kThreads) give(c, a.copy_dst[c]);
   if (!lead) return;
   for (int c = n_freed + tid; c < n_given; c += kThreads) {
     const int32_t page = a.free_pages[head + (c - n_freed)];
     if ((uint32_t)page >= (uint32_t)a.num_pages) record_error(a.status, FP4IDX_ERR_BAD_PAGE);
+    a.copy_dst[c] = page;
     give(c, page);
   }
   for (int c = n_given + warp; c < n_copies; c += kWarps) {
@@ -303,28 +311,29 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
     mark_block(m, a.page_table + (int64_t)r * a.max_pages, c0, count_of(n), 0, a.num_pages, a.status);
   });
   mma::cluster_sync();
-  // this CTA's share of the pages in use, in place of its marks
+  // this CTA's share of the pages in use, in place of its marks, and of those that may move
   const Run run(m);
   const int32_t w0 = m.rank << shift;
-  uint32_t* bits = smem + m.first();
-  auto page0 = [&](int w) { return (int64_t)(w0 + w) * 32; };
+  uint32_t *bits = smem + m.first(), *free_to_move = smem + m.words();
+  auto page0 = [&](int w) { return (w0 + w) * 32; };
   auto pins = [&](int w) { return a.pinned && page0(w) < a.num_pages ? a.pinned[w0 + w] & below(page0(w), a.num_pages) : 0u; };
-  int32_t n = 0, here, used;
-  for (int w = run.first + lane; w < run.last; w += 32) {
-    const uint32_t v = m.merged(w, 0) | pins(w);
-    bits[w] = v;
-    n += __popc(v);
+  for (int w = tid; w < 1 << shift; w += kThreads) {
+    const uint32_t pin = pins(w);
+    uint32_t held[1];
+    m.merged(w, held);
+    bits[w] = held[0] | pin;
+    free_to_move[w] = held[0] & ~pin;
   }
+  __syncthreads();
+  int32_t n = 0, here, used;
+  for (int w = run.first + lane; w < run.last; w += 32) n += __popc(bits[w]);
   before_warp(__reduce_add_sync(~0u, n), table, &here);
   publish(m, used_by, here);
   mma::cluster_sync();
   before_cta(m, used_by, &used);
   // ids below `used` that are free, and pages from there on that may move
   auto holes = [&](int w) { return ~bits[w] & below(page0(w), used); };
-  auto movers = [&](int w) {
-    const uint32_t v = bits[w] & ~below(page0(w), used);
-    return v ? v & ~pins(w) : 0u;
-  };
+  auto movers = [&](int w) { return free_to_move[w] & ~below(page0(w), used); };
   int32_t nh = 0, nm = 0, here_h, here_m, all_m, unused;
   for (int w = run.first + lane; w < run.last; w += 32) nh += __popc(holes(w)), nm += __popc(movers(w));
   int32_t h = before_warp(__reduce_add_sync(~0u, nh), table, &here_h);
@@ -336,25 +345,23 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   v += before_cta(m, movers_by, &all_m);
   const int32_t moves = min(all_m, a.max_moves);  // (there are at least as many holes as movers)
   const int32_t first_mover = v;
+  const uint32_t before = (1u << lane) - 1;
   int32_t last = 0, spare = 0;
   for (int w = run.first; w < run.last; w++) {
-    const int32_t p0 = (int32_t)page0(w);
-    const uint32_t open = holes(w), from = movers(w);
+    const int32_t p0 = page0(w);
     uint32_t now = bits[w];
-    if (open) {
-      bool fills = false;
-      h = list_bits(open, p0, h, [&](int32_t at, int32_t page) {
-        fills = at < moves;
-        if (fills) a.move_dst[at] = page;
-      });
+    if (p0 < used && h < moves) {
+      const uint32_t open = holes(w);
+      const bool fills = (open >> lane & 1) && h + __popc(open & before) < moves;
+      if (fills) a.move_dst[h + __popc(open & before)] = p0 + lane;
+      h += __popc(open);
       now |= __ballot_sync(~0u, fills);
     }
-    if (from) {
-      bool goes = false;
-      v = list_bits(from, p0, v, [&](int32_t at, int32_t page) {
-        goes = at < moves;
-        if (goes) a.move_src[at] = page;
-      });
+    if (p0 + 32 > used && v < moves) {
+      const uint32_t from = movers(w);
+      const bool goes = (from >> lane & 1) && v + __popc(from & before) < moves;
+      if (goes) a.move_src[v + __popc(from & before)] = p0 + lane;
+      v += __popc(from);
       now &= ~__ballot_sync(~0u, goes);
     }
     __syncwarp();
@@ -375,12 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   // where the pages from `used` on are now: those of this CTA's share that move, and those that stay
   for (int i = first_mover + lane; i < min(v, moves); i += 32) a.remap[a.move_src[i]] = a.move_dst[i];
   const int32_t listed = min(all_spare, a.n_free), lost = all_spare - listed, head = a.n_free - listed;
+  int32_t* free_at = a.free_pages + (head - lost);
   for (int w = run.first; w < run.last; w++) {
-    const uint32_t now = bits[w], stay = now & ~below(page0(w), used);
-    if (stay >> lane & 1) a.remap[page0(w) + lane] = (int32_t)page0(w) + lane;
-    f = list_bits(~now & below(page0(w), a.num_pages), (int32_t)page0(w), f, [&](int32_t at, int32_t page) {
-      if (at >= lost) a.free_pages[head + at - lost] = page;
-    });
+    const int32_t p0 = page0(w);
+    const uint32_t now = bits[w], open = ~now & below(p0, a.num_pages);
+    if (p0 + 32 > used && (now & ~below(p0, used)) >> lane & 1) a.remap[p0 + lane] = p0 + lane;
+    const int32_t at = f + __popc(open & before);
+    if ((open >> lane & 1) && at >= lost) free_at[at] = p0 + lane;
+    f += __popc(open);
   }
   mma::cluster_sync();
   each_block(m, false, a.n_seqs, a.max_pages, len_of, [&](int r, int c0, int32_t len) {
@@ -423,11 +432,13 @@ int ctas_of(int64_t entries, int64_t pool) {
 }
 
 template <class A>
-cudaError_t launch(void (*kernel)(A, int, bool), const A& a, int sets, int64_t entries, size_t rows, cudaStream_t stream) {
+cudaError_t launch(void (*kernel)(A, int, bool), const A& a, int sets, int share, int64_t entries, size_t rows,
+                   cudaStream_t stream) {
   const int64_t words = ((int64_t)a.num_pages + 31) / 32;
   const int ctas = ctas_of(entries, a.num_pages);
   const int shift = log2_from((words + ctas - 1) / ctas);
   const size_t part = 4 * ((size_t)sets << shift);
+  rows += share * ((size_t)4 << shift);
   const bool full = part * ctas + rows <= kMaxSmem;
   const size_t smem = (full ? part * ctas : part) + rows;
   const void* f = reinterpret_cast<const void*>(kernel);
@@ -445,11 +456,11 @@ cudaError_t launch(void (*kernel)(A, int, bool), const A& a, int sets, int64_t e
 }  // namespace
 
 cudaError_t launch_fork_pages(const ForkArgs& a, cudaStream_t stream) {
-  return launch(fork_kernel, a, 2, ((int64_t)a.n_old + a.n_new) * a.max_pages, 8 * (size_t)a.n_old + 4 * (size_t)a.n_new, stream);
+  return launch(fork_kernel, a, 2, 0, ((int64_t)a.n_old + a.n_new) * a.max_pages, 8 * (size_t)a.n_old + 4 * (size_t)a.n_new, stream);
 }
 
 cudaError_t launch_compact_pages(const CompactArgs& a, cudaStream_t stream) {
-  return launch(compact_kernel, a, 1, (int64_t)a.n_seqs * a.max_pages, 0, stream);
+  return launch(compact_kernel, a, 1, 1, (int64_t)a.n_seqs * a.max_pages, 0, stream);
 }
 
 }  // namespace fp4idx
