@@ -14,7 +14,8 @@
 namespace fp4idx {
 namespace {
 
-constexpr int kJoin = 512;
+constexpr int kJoin = 1024;
+constexpr int kEarly = 2;  // candidates a thread
 constexpr int kAll = 128;  // up to here a join sorts all of a group's candidates at once
 constexpr float kInf = __builtin_huge_valf();
 
@@ -475,6 +476,10 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   int32_t* sizes = tokens + all;
   uint64_t* sorted = keys + (all * 3 + lists + 1) / 2;
   if (tid == 0) sm.n_found = 0;
+  BeamItem early[kEarly];  // on their way while the rows' sums are joined
+#pragma unroll
+  for (int j = 0; j < kEarly; j++)
+    if (tid + j * kThreads < all) early[j] = from[tid + j * kThreads];
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
   int lanes = 1;
   while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
@@ -508,10 +513,9 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     if (live && c0 == 0) sm.kind[b] = what, sm.score[b] = sc, sm.tops[b] = top, sm.rest[b] = total;
   }
   __syncthreads();
-  for (int i = tid; i < all; i += kThreads) {
+  auto put = [&](int i, BeamItem it) {
     const int l = i / k, b = i / per_beam;
     uint64_t key = (1 << 16) + i;
-    BeamItem it = from[i];
     if (sm.kind[b] != kNone && i - l * k < sizes[l]) {
       // a fourth of the total: no finite score and logits make it overflow
       Two t{sm.score[b] * 0.25f, 0.f};
@@ -521,7 +525,11 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     }
     keys[i] = key;
     tokens[i] = it.token;
-  }
+  };
+#pragma unroll
+  for (int j = 0; j < kEarly; j++)
+    if (tid + j * kThreads < all) put(tid + j * kThreads, early[j]);
+  for (int i = tid + kEarly * kThreads; i < all; i += kThreads) put(i, from[i]);
   __syncthreads();
   int n = all;
   if (all > kAll) {
