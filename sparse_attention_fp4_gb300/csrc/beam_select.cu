@@ -153,6 +153,43 @@ __device__ __forceinline__ uint32_t ordered(float v) {
   return (uint32_t)i ^ (i < 0 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+__device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
+__host__ __device__ inline int pow2_from(int n) {
+  int p = 1;
+  while (p < n) p <<= 1;
+  return p;
+}
+// Descending order; no two keys are equal.  Up to kThreads (a power of two) by counting those above each, adjacent lanes sharing one; more
+// of them (a power of two) in a sorting network.
+template <int kThreads>
+__device__ __forceinline__ void sort_keys(uint64_t* keys, int n) {
+  if (n <= kThreads) {
+    const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
+    uint64_t key = 0;
+    int rank = 0;
+    if (i < n) {
+      key = keys[i];
+#pragma unroll 8
+      for (int j = part; j < n; j += share) rank += keys[j] > key;
+    }
+#pragma unroll 1
+    for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+    __syncthreads();
+    if (part == 0 && i < n) keys[rank] = key;
+    __syncthreads();
+    return;
+  }
+  for (int size = 2; size <= n; size <<= 1)
+    for (int d = size >> 1; d; d >>= 1) {
+      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+        const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
+        const uint64_t u = keys[lo], v = keys[hi];
+        if ((v > u) == ((lo & size) == 0)) keys[lo] = v, keys[hi] = u;
+      }
+      __syncthreads();
+    }
+}
+
 // The largest of what a thread has read, and the sum of exp(value - largest): 2^((value - largest) log2 e).
 struct Running {
   float top = -kInf, sum = 0.f;
@@ -200,11 +237,11 @@ struct Running {
 
 template <int kThreads>
 struct ScanShared {
-  static constexpr int kFound = kThreads;  // candidates of a chunk before the last ranking
+  static constexpr int kFound = 2048;  // candidates of a chunk that are sorted
   float segment[kSegments];
   float top[kThreads / 32];
   Two sum[kThreads / 32];
-  BeamItem found[kFound];
+  uint64_t found[kFound];  // ordered logit, then the token counted down
   int32_t owner[kThreads];  // thread + tile * kThreads
   int32_t owners, n, count[2];
   float bound;
@@ -290,11 +327,12 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   __syncthreads();
   // the tiles with a candidate are read once more, a vector a thread
   const float bound = sm.bound;
+  auto add = [&](uint32_t o, int token) {
+    const int at = atomicAdd(&sm.n, 1);
+    if (at < kFound) sm.found[at] = (uint64_t)o << 32 | (0xFFFFFFFFu - token);
+  };
   auto keep = [&](float u, int token) {
-    if (u >= bound && u > -kInf) {
-      const int at = atomicAdd(&sm.n, 1);
-      if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token};
-    }
+    if (u >= bound && u > -kInf) add(ordered(u), token);
   };
   if (run.top >= bound && run.top > -kInf)
     for (int t = tid, i = first + tid; i < end; t += kThreads, i += kTile)
@@ -316,16 +354,16 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   }
   __syncthreads();
   if (owners > kThreads || sm.n > kFound) {
-    // many equal values, or all tokens that are not masked within few threads: the k-th largest
-    // exactly, then of those that equal it the first ones, bit by bit
+    // many equal values, or many tokens in few threads: the k-th largest exactly, then of those that equal it
+    // the first ones, bit by bit
     int turn = 0;
     auto all_of = [&](auto&& f) {
-      for (int v = first + tid; v < end; v += kThreads) each<T>(body[v], [&](int e, float u) { f(ordered(u), u, head + v * kE + e); });
-      if (edge >= 0) f(ordered(to_float(x[edge])), to_float(x[edge]), edge);
+      for (int v = first + tid; v < end; v += kThreads) each<T>(body[v], [&](int e, float u) { f(ordered(u), head + v * kE + e); });
+      if (edge >= 0) f(ordered(to_float(x[edge])), edge);
     };
     auto count = [&](auto&& f) {
       int n = 0;
-      all_of([&](uint32_t o, float, int token) { n += f(o, token); });
+      all_of([&](uint32_t o, int token) { n += f(o, token); });
       n = block_sum(n, sm.count, turn);
       turn ^= 1;
       return n;
@@ -348,32 +386,20 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
     }
     if (tid == 0) sm.n = 0;
     __syncthreads();
-    all_of([&](uint32_t o, float u, int token) {
-      if (o > kth || (o == kth && token <= last)) {
-        const int at = atomicAdd(&sm.n, 1);
-        if (at < kFound) sm.found[at] = BeamItem{u + 0.f, token};
-      }
+    all_of([&](uint32_t o, int token) {
+      if (o > kth || (o == kth && token <= last)) add(o, token);
     });
     __syncthreads();
   }
   const int n = min(sm.n, kFound);
   ready();
-  int share = 1;  // lanes that share a candidate
-  while (share < 32 && 2 * share * n <= kThreads) share <<= 1;
-  {
-    const int i = tid / share;
-    BeamItem it{};
-    int rank = 0;
-    if (i < n) {
-      it = sm.found[i];
-#pragma unroll 4
-      for (int s = tid & (share - 1); s < n; s += share) {
-        const BeamItem o = sm.found[s];
-        rank += (int)(o.logit > it.logit) | ((int)(o.logit == it.logit) & (int)(o.token < it.token));
-      }
-    }
-    for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
-    if (i < n && (tid & (share - 1)) == 0 && rank < a.k) list[rank] = it;
+  const int padded = pow2_from(n);
+  for (int i = n + tid; i < padded; i += kThreads) sm.found[i] = i;
+  __syncthreads();
+  sort_keys<kThreads>(sm.found, padded);
+  for (int i = tid; i < min(n, a.k); i += kThreads) {
+    const uint64_t key = sm.found[i];
+    list[i] = BeamItem{unordered((uint32_t)(key >> 32)), (int32_t)(0xFFFFFFFFu - (uint32_t)key)};
   }
   if (warp == kWarps - 1) {
     sum = sm.sum[lane & (kWarps - 1)];
@@ -394,8 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scan_kernel(const B
 }
 
 // ---------------------------------------------------------------- join
-__device__ __forceinline__ float unordered(uint32_t o) { return __uint_as_float(o >> 31 ? o ^ 0x80000000u : ~o); }
-
 // A group's candidates lie in shared memory list after list (beam after beam, chunk after chunk, each in order), k
 // places each, kMostItems in all.  Their keys are in the order of the totals (larger is better): the first of its
 // two floats, all but the last 13 bits of the second, and, so that no two keys are equal and the lower index (the lower
@@ -407,41 +431,6 @@ __device__ __forceinline__ uint64_t key_of(const Two& total, int i) {
   return (t >> kIndexBits << kIndexBits) | (kMostItems - 1 - i);
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return kMostItems - 1 - (int)(key & (kMostItems - 1)); }
-// Descending order.  Up to kThreads (a power of two) by counting those above each, adjacent lanes sharing one; more
-// of them (a power of two) in a sorting network.
-template <int kThreads>
-__device__ __forceinline__ void sort_keys(uint64_t* keys, int n) {
-  if (n <= kThreads) {
-    const int share = min(32, kThreads / n), part = threadIdx.x & (share - 1), i = threadIdx.x / share;
-    uint64_t key = 0;
-    int rank = 0;
-    if (i < n) {
-      key = keys[i];
-#pragma unroll 8
-      for (int j = part; j < n; j += share) rank += keys[j] > key;
-    }
-#pragma unroll 1
-    for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
-    __syncthreads();
-    if (part == 0 && i < n) keys[rank] = key;
-    __syncthreads();
-    return;
-  }
-  for (int size = 2; size <= n; size <<= 1)
-    for (int d = size >> 1; d; d >>= 1) {
-      for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-        const int lo = 2 * i - (i & (d - 1)), hi = lo + d;
-        const uint64_t u = keys[lo], v = keys[hi];
-        if ((v > u) == ((lo & size) == 0)) keys[lo] = v, keys[hi] = u;
-      }
-      __syncthreads();
-    }
-}
-__host__ __device__ inline int pow2_from(int n) {
-  int p = 1;
-  while (p < n) p <<= 1;
-  return p;
-}
 // Some 4 k candidates, and k at the least, make the bound of a join.
 __host__ __device__ inline int depth(int k, int lists) {
   const int d = (4 * k + lists - 1) / lists;
