@@ -611,9 +611,12 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
   join_group<kThreads>(a, group, stats, items, join, own);
 }
 
-// Up to kWave chunks CTAs of 512 threads take one each, all at once; above that CTAs of 256 threads, so that more chunks
-// overlap: what a CTA does besides reading takes some 5 us, of latency.
-constexpr int kWave = 304;
+// What a CTA does besides reading takes some 5 us of latency, so chunks should run at once.  Up to kWave of
+// them CTAs of 512 threads take one each; above that CTAs of 256 threads (400 rows of 131,072 tokens 29 us against 37,
+// 100 x 6 of 65,537 31 against 36; 256 rows of 131,072 are as fast either way), and 128 for rows of up to kSmallVecs
+// vectors (1,024 rows of 10,000 tokens 17 us against 23, 1,488 rows of 842 with lists of 31 23 against 80; of 4,000
+// vectors 19 either way).
+constexpr int kWave = 304, kSmallVecs = 2048;
 // The least and the most vectors of a row that one CTA takes, what it takes to spare the join lists, and the lists that
 // a join has then.
 constexpr int kLeastVecs = 512, kMostVecs = 65536, kShortVecs = 4096, kLists = 32;
@@ -673,7 +676,8 @@ cudaError_t launch_typed(BeamArgs a, cudaStream_t stream) {
     }
   }
   a.lists = reinterpret_cast<BeamItem*>(a.stats + (int64_t)a.n_rows * a.chunks);
-  return (int64_t)a.n_rows * a.chunks <= kWave ? launch_scan<T, 512>(a, cluster, stream) : launch_scan<T, 256>(a, cluster, stream);
+  if ((int64_t)a.n_rows * a.chunks <= kWave) return launch_scan<T, 512>(a, cluster, stream);
+  return a.chunk_vecs > kSmallVecs ? launch_scan<T, 256>(a, cluster, stream) : launch_scan<T, 128>(a, cluster, stream);
 }
 
 }  // namespace
