@@ -436,22 +436,19 @@ __host__ __device__ inline int depth(int k, int lists) {
   const int d = (4 * k + lists - 1) / lists;
   return d < k ? d : k;
 }
-// Places of the list of candidates that are sorted (with room for those that fill it up to a power of two).
-__host__ __device__ inline int sorted_most(int k, int lists) {
-  const int all = lists * k;
-  return all <= kAll ? pow2_from(all) : pow2_from(lists < k ? all : k * k);
-}
-
 struct JoinShared {
   // lse = top + rest, kept apart: next to a large top the sum's logarithm would be lost
   float tops[FP4IDX_BEAM_MAX_BEAMS], score[FP4IDX_BEAM_MAX_BEAMS];
   Two rest[FP4IDX_BEAM_MAX_BEAMS];
   int32_t kind[FP4IDX_BEAM_MAX_BEAMS];
   int32_t n_found;
+  uint32_t bound;
 };
+// Where, in units of 8 bytes, the sorted keys begin (16-byte aligned): behind the keys, the tokens and the lists' sizes.
+__host__ __device__ inline int sorted_at(int all, int lists) { return ((3 * all + lists + 1) / 2 + 1) & ~1; }
 __host__ __device__ inline size_t join_bytes(int k, int lists) {
-  const int all = lists * k, heads = all > kAll ? pow2_from(lists * depth(k, lists)) : 0, most = sorted_most(k, lists);
-  return sizeof(uint64_t) * ((all * 3 + lists + 1) / 2 + (heads > most ? heads : most));
+  const int all = lists * k;
+  return sizeof(uint64_t) * (sorted_at(all, lists) + pow2_from(all));
 }
 
 // One group, by one CTA, from its rows' lists and sums; `smem` has join_bytes.
@@ -463,7 +460,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   uint64_t* keys = reinterpret_cast<uint64_t*>(smem);
   int32_t* tokens = reinterpret_cast<int32_t*>(keys + all);
   int32_t* sizes = tokens + all;
-  uint64_t* sorted = keys + (all * 3 + lists + 1) / 2;
+  uint64_t* sorted = keys + sorted_at(all, lists);
   if (tid == 0) sm.n_found = 0;
   BeamItem early[kEarly];  // on their way while the rows' sums are joined
 #pragma unroll
@@ -522,17 +519,32 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   __syncthreads();
   int n = all;
   if (all > kAll) {
-    // a bound: the k-th best of each list's first `deep` candidates.  At most k lists begin with one that is
-    // no worse, or fewer than k candidates are all there are.
-    const int deep = depth(k, lists), heads = lists * deep, m = pow2_from(heads);
-    for (int i = tid; i < m; i += kThreads) sorted[i] = i < heads ? keys[i / deep * k + i % deep] : i;
+    // a bound: the k-th best of each list's first `deep` candidates, by the upper bits of their totals (the index
+    // in the others makes them differ); whatever is no worse in these bits stays
+    const int deep = depth(k, lists), heads = lists * deep, m = pow2_from(heads), bits = 31 - __clz(m);
+    uint32_t* upper = reinterpret_cast<uint32_t*>(sorted);
+    for (int i = tid; i < m; i += kThreads) {
+      const uint32_t hi = i < heads ? (uint32_t)(keys[i / deep * k + i % deep] >> 32) : 0u;
+      upper[i] = (hi >> bits << bits) | (m - 1 - i);
+    }
     __syncthreads();
-    sort_keys<kThreads>(sorted, m);
-    const uint64_t bound = sorted[k - 1];
+    const int share = max(1, min(min(32, kThreads / m), m / 4)), part = tid & (share - 1);
+    for (int i = tid / share; i < m; i += kThreads / share) {  // (whole warps: m is 32 at the least)
+      const uint32_t mine = upper[i];
+      int rank = 0;
+#pragma unroll 4
+      for (int j = 4 * part; j < m; j += 4 * share) {
+        const uint4 q = *reinterpret_cast<const uint4*>(upper + j);
+        rank += (q.x > mine) + (q.y > mine) + (q.z > mine) + (q.w > mine);
+      }
+      for (int d = 1; d < share; d <<= 1) rank += __shfl_xor_sync(~0u, rank, d);
+      if (rank == k - 1 && part == 0) sm.bound = max(1u, mine >> bits << bits);
+    }
     __syncthreads();
+    const uint32_t bound = sm.bound;
     for (int i = tid; i < all; i += kThreads) {
       const uint64_t key = keys[i];
-      if (key >> 32 && key >= bound) sorted[atomicAdd(&sm.n_found, 1)] = key;
+      if ((uint32_t)(key >> 32) >= bound) sorted[atomicAdd(&sm.n_found, 1)] = key;
     }
     __syncthreads();
     n = sm.n_found;
@@ -574,7 +586,9 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const BeamArgs a) {
 // ---------------------------------------------------------------- both in one launch
 // A cluster has a group's chunks; their lists and sums go straight to the shared memory of its first CTA, which joins
 // them.
-__host__ __device__ inline size_t lists_bytes(int k, int lists) { return lists * (sizeof(BeamStat) + k * sizeof(BeamItem)); }
+__host__ __device__ inline size_t lists_bytes(int k, int lists) {
+  return (lists * (sizeof(BeamStat) + k * sizeof(BeamItem)) + 15) / 16 * 16;
+}
 template <class T>
 __device__ __forceinline__ T* in_first_cta(T* p) {
   uint64_t r;
@@ -653,7 +667,7 @@ cudaError_t launch_scan(const BeamArgs& a, bool cluster, cudaStream_t stream) {
                         lists, stream, a);
   }
   e = set_smem_attr_once(reinterpret_cast<const void*>(scan_kernel<T, kThreads>), sizeof(float) * kMostVecs / kVecs);
-  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 136 * 1024);
+  if (e == cudaSuccess) e = set_smem_attr_once(reinterpret_cast<const void*>(join_kernel), 168 * 1024);
   if (e == cudaSuccess) e = launch_early(scan_kernel<T, kThreads>, grid, kThreads, tops, 1, stream, a);
   if (e != cudaSuccess) return e;
   return launch_early(join_kernel, dim3(a.n_rows / a.beams), kJoin, join_bytes(a.k, lists), 1, stream, a);
