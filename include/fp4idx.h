@@ -566,8 +566,8 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
  * Rows g*n_beams .. g*n_beams + n_beams - 1 are the beams of group (request) g:
  *   total[r,v] = scores[r] + (logits[r,v] - log sum_u exp(logits[r,u]))
  * and a finished row (done[r] != 0) has the one candidate (end_token, scores[r]); its
- * logits are not read.  Per group the k largest totals, in descending order; equal totals:
- * the lower row, then the larger logit, then the lower token.
+ * logits are not read.  Per group the k largest totals, in descending order; of equal
+ * totals the lower row comes first, then the lower token.
  *   logits      [n_rows, vocab] of type logits_type (0 bf16, 1 fp16, 2 fp32), row r at
  *               element r*logits_stride; aligned to its element type; a token is ruled out
  *               by -inf
@@ -581,8 +581,10 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
  *               where a group has no candidate left
  *   done_out    [n_rows/n_beams, k] int32, nullable (written): 1 where the row was finished
  *               or the token is end_token, else 0
- * Sums are fp32 within 16,384 tokens and fp64 above; totals are compared in fp64, so that
- * totals of different rows closer than about 1e-7 may change places.  A row whose scores or
+ * Exponentials and a thread's share of their sum are fp32, what is added up above that, and
+ * the totals, has some 36 bits or more.  Totals of different rows closer than about 1e-7 of the
+ * logarithm of the sum may change places; within a row the order is that of the logits (but for
+ * logits of one row so close that their totals agree to 36 bits).  A row whose score or
  * logits hold a NaN or +inf has no candidate (BAD_VALUE).  The outputs must not overlap one
  * another or the inputs.  workspace: fp4idx_beam_select_workspace_bytes(n_rows, vocab, k)
  * bytes, 16-byte aligned, nothing in it needs to be initialised; calls that may overlap need

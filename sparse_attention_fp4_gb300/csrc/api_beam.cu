@@ -85,7 +85,7 @@ int fp4idx_copy_pages(const int32_t* src, const int32_t* dst, int64_t n_copies, 
   if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4) || !aligned(status_dev, 4)) return FP4IDX_ERR_INVALID_ARG;
   fp4idx::Regions r{};
   for (int32_t c = 0; c < n_regions; c++) {
-    if (!regions[c] || !aligned(regions[c], 16) || page_bytes[c] < 16 || page_bytes[c] % 16 != 0)
+    if ((!regions[c] && num_pages > 0) || !aligned(regions[c], 16) || page_bytes[c] < 16 || page_bytes[c] % 16 != 0)
       return FP4IDX_ERR_INVALID_ARG;
     if (page_bytes[c] > (1 << 30)) return FP4IDX_ERR_UNSUPPORTED;
     r.base[c] = static_cast<uint8_t*>(regions[c]);

@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from array import array
 
@@ -654,8 +655,8 @@ def copy_pages(src, dst, caches, count=None, status=None, stream=None):
     for c in caches:
         if c.get_device() != dev or not c.is_contiguous() or c.shape[0] != pages:
             raise ValueError("caches must be contiguous CUDA tensors on the current device, of one number of pages")
-    each = pages or 1
-    base, size = array("Q", [c.data_ptr() for c in caches]), array("q", [c.nbytes // each for c in caches])
+    base = array("Q", [c.data_ptr() for c in caches])
+    size = array("q", [c.nbytes // pages if pages else math.prod(c.shape[1:]) * c.element_size() for c in caches])
     rc = _lib.fp4idx_copy_pages(
         _addr(src, "src", _I32, 0, dev), _addr(dst, "dst", _I32, n, dev), n,
         None if count is None else _addr(count, "count", _I32, 1, dev), base.buffer_info()[0], size.buffer_info()[0], m, pages,

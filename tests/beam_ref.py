@@ -35,14 +35,15 @@ def totals(logits, scores, beams, done=None, end=-1):
 
 
 def check_select(got, logits, scores, beams, k, done=None, end=-1):
-    """got: scores, rows, tokens (and done_out) as [groups, k] arrays.  A total is off by lse's error and one
-    rounding to fp32: sums of fp32 exponentials, each within 2 units of 2^-23 (and the rounding of its
-    argument, at most 2^-24 of a difference d where it weighs exp(-d), below 2^-24), over at most 64 + 16
-    additions in fp32: 2^-22 + 2^-24 + 80 * 2^-24 < 6e-6 of the sum, so of lse.  Candidates whose totals are closer than
-    twice that may change places (within a row the order is exact)."""
+    """got: scores, rows, tokens (and done_out) as [groups, k] arrays.  A total is off by one rounding to fp32 and by lse's
+    error, in units of 2^-24 of the sum of exponentials: 4 of an exponential (2^-22), 4 of its argument (two
+    roundings of a number t that weighs 2^-t), 10 additions within a tile; per tile of its thread (of 2,048 logits of a
+    row at the least, 64 at the most) one addition and, where its largest rises, a factor within 5; 2 for joining
+    threads and chunks, the logarithm and the totals (some 36 bits or more).  Candidates whose totals are closer
+    than twice that may change places (within a row the order is exact)."""
     out_s, out_r, out_t, out_d = got
     want = totals(logits, scores, beams, done, end)
-    eps = 6e-6
+    eps = (20 + 6 * min(64, -(-logits.shape[1] // 2048))) * 2.0 ** -24
     for g, w in enumerate(want):
         n = min(k, len(w))
         assert (out_r[g, n:] == -1).all() and (out_t[g, n:] == -1).all() and (out_s[g, n:] == -np.inf).all(), g

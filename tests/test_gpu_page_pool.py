@@ -112,6 +112,15 @@ def test_fork_in_pools_of_any_size(pool):
     check_fork(table, [100, 128, 190, 64], 1, [0, 0, 0, -1], pool, [7] * 9 + ids[7:], 9)
 
 
+def test_fork_of_the_most_rows_in_the_largest_pool():
+    rows, pool = 8192, 1 << 23
+    table, cached, ids = state(9, rows, 2, 1, rows * 3)
+    far = lambda p: pool - 1 - 331 * p if p >= 0 else p  # noqa: E731
+    table = [[far(p) if 0 <= p < rows * 3 else p for p in t] for t in table]
+    got = check_fork(table, cached, 1, pick(2, rows, rows, 0.1), pool, [-9] * rows * 2 + [far(p) for p in ids], rows * 2)
+    assert got["counts"][0] > 1000 and got["counts"][1] > 1000
+
+
 def test_fork_identity_and_release():
     """Rows that go on from themselves cost nothing; a batch that ends gives every page back."""
     table, cached, ids = state(3, 12, 30, 1, 500)
@@ -400,6 +409,13 @@ def test_copy_streams_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(bool((w == raw(c)).all()) for w, c in zip(want, caches))
+
+
+def test_copy_without_pages_or_caches():
+    from sparse_attention_fp4_gb300 import fp4idx
+    fp4idx.copy_pages(i32([1]), i32([2]), [])
+    fp4idx.copy_pages(i32([]), i32([]), [torch.empty((0, 4, 64, 16), dtype=torch.uint8, device="cuda")])
+    fp4idx.copy_pages(i32([1]), i32([0]), [torch.empty((0, 4, 64, 16), dtype=torch.uint8, device="cuda")])
 
 
 def test_refusals_of_the_binding():
