@@ -346,29 +346,37 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   const int32_t moves = min(all_m, a.max_moves);  // (there are at least as many holes as movers)
   const int32_t first_mover = v;
   const uint32_t before = (1u << lane) - 1;
-  int32_t last = 0, spare = 0;
-  for (int w = run.first; w < run.last; w++) {
+  for (int w = run.first; w < run.last && h < moves; w++) {
     const int32_t p0 = page0(w);
-    uint32_t now = bits[w];
-    if (p0 < used && h < moves) {
-      const uint32_t open = holes(w);
-      const bool fills = (open >> lane & 1) && h + __popc(open & before) < moves;
-      if (fills) a.move_dst[h + __popc(open & before)] = p0 + lane;
-      h += __popc(open);
-      now |= __ballot_sync(~0u, fills);
-    }
-    if (p0 + 32 > used && v < moves) {
-      const uint32_t from = movers(w);
-      const bool goes = (from >> lane & 1) && v + __popc(from & before) < moves;
-      if (goes) a.move_src[v + __popc(from & before)] = p0 + lane;
-      v += __popc(from);
-      now &= ~__ballot_sync(~0u, goes);
-    }
-    __syncwarp();
-    if (lane == 0) bits[w] = now;
-    if (now) last = p0 + 32 - __clz(now);
-    spare += __popc(~now & below(p0, a.num_pages));
+    if (p0 >= used) break;
+    const uint32_t open = holes(w);
+    if (open == 0) continue;
+    const int32_t at = h + __popc(open & before);
+    const bool fills = (open >> lane & 1) && at < moves;
+    if (fills) a.move_dst[at] = p0 + lane;
+    h += __popc(open);
+    const uint32_t filled = __ballot_sync(~0u, fills);
+    if (lane == 0) bits[w] |= filled;
   }
+  for (int w = run.first; w < run.last && v < moves; w++) {
+    const int32_t p0 = page0(w);
+    const uint32_t from = movers(w);
+    if (from == 0) continue;
+    const int32_t at = v + __popc(from & before);
+    const bool goes = (from >> lane & 1) && at < moves;
+    if (goes) a.move_src[at] = p0 + lane;
+    v += __popc(from);
+    const uint32_t gone = __ballot_sync(~0u, goes);
+    if (lane == 0) bits[w] &= ~gone;
+  }
+  __syncwarp();
+  int32_t last = 0, spare = 0;
+  for (int w = run.first + lane; w < run.last; w += 32) {
+    if (bits[w]) last = page0(w) + 32 - __clz(bits[w]);
+    spare += __popc(~bits[w] & below(page0(w), a.num_pages));
+  }
+  spare = __reduce_add_sync(~0u, spare);
+  last = (int32_t)__reduce_max_sync(~0u, (uint32_t)last);
   int32_t here_spare, all_spare;
   int32_t f = before_warp(spare, table, &here_spare);
   publish(m, spare_by, here_spare);
@@ -386,10 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
   for (int w = run.first; w < run.last; w++) {
     const int32_t p0 = page0(w);
     const uint32_t now = bits[w], open = ~now & below(p0, a.num_pages);
-    if (p0 + 32 > used && (now & ~below(p0, used)) >> lane & 1) a.remap[p0 + lane] = p0 + lane;
-    const int32_t at = f + __popc(open & before);
+    if (now && p0 + 32 > used && (now & ~below(p0, used)) >> lane & 1) a.remap[p0 + lane] = p0 + lane;
+    if (open == 0) continue;
+    const int32_t at = f + (open == ~0u ? lane : __popc(open & before));
     if ((open >> lane & 1) && at >= lost) free_at[at] = p0 + lane;
-    f += __popc(open);
+    f += open == ~0u ? 32 : __popc(open);
   }
   mma::cluster_sync();
   each_block(m, false, a.n_seqs, a.max_pages, len_of, [&](int r, int c0, int32_t len) {
