@@ -75,6 +75,7 @@ __device__ __forceinline__ Kind kind_of(const BeamArgs& a, int row, float score,
 // ---------------------------------------------------------------- scan
 constexpr int kVecs = 4;          // vectors (16 bytes of logits) that a thread takes at once
 constexpr int kSegments = 128;
+constexpr int kWords = 4;  // words a thread reads again at once
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <class T>
@@ -325,7 +326,7 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
     if (rank == a.k - 1 && (tid & (span - 1)) == 0) sm.bound = u;
   }
   __syncthreads();
-  // the tiles with a candidate are read once more, a vector a thread
+  // the tiles with a candidate are read once more, a word a thread
   const float bound = sm.bound;
   auto add = [&](uint32_t o, int token) {
     const int at = atomicAdd(&sm.n, 1);
@@ -342,13 +343,28 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
       }
   if (edge >= 0) keep(to_float(x[edge]), edge);
   __syncthreads();
-  const int owners = sm.owners;
+  const int owners = sm.owners, words = owners * kVecs * 4;
   if (owners <= kThreads) {
-    for (int w = tid; w < owners * kVecs && *(volatile int32_t*)&sm.n <= kFound; w += kThreads) {
-      const int t = sm.owner[w / kVecs], i = first + t / kThreads * kTile + w % kVecs * kThreads + t % kThreads;
-      if (i < end) {
-        const uint4 u[1] = {load_once(body + i)};
-        if (largest<T>(u) >= bound) each<T>(u[0], [&](int e, float x) { keep(x, head + i * kE + e); });
+    for (int w = tid; w < words && *(volatile int32_t*)&sm.n <= kFound; w += kWords * kThreads) {
+      uint32_t u[kWords];
+      int at[kWords];  // the word's first token
+#pragma unroll
+      for (int j = 0; j < kWords; j++) {
+        const int o = w + j * kThreads, q = o / 4 % kVecs, t = o < words ? sm.owner[o / (4 * kVecs)] : 0;
+        const int i = first + t / kThreads * kTile + q * kThreads + t % kThreads;
+        const bool in = o < words && i < end;
+        at[j] = head + i * kE + o % 4 * (kE / 4);
+        u[j] = in ? reinterpret_cast<const volatile uint32_t*>(body + i)[o % 4] : Elems<T>::kMasked;
+      }
+#pragma unroll
+      for (int j = 0; j < kWords; j++) {
+        if constexpr (kE == 4) {
+          keep(__uint_as_float(u[j]), at[j]);
+        } else {
+          const float2 p = Elems<T>::pair(u[j]);
+          keep(p.x, at[j]);
+          keep(p.y, at[j] + 1);
+        }
       }
     }
   }
