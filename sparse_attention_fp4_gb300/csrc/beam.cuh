@@ -17,6 +17,17 @@ struct BeamItem {
   int32_t token;
 };
 
+// i / d by one product, for i and d below 2^16.
+struct Divisor {
+  int32_t d;
+  uint32_t inverse;
+  Divisor() = default;
+  explicit Divisor(int32_t n) : d(n), inverse(n == 1 ? 0 : 0xFFFFFFFFu / n + 1) {}
+#ifdef __CUDACC__
+  __device__ int under(int i) const { return d == 1 ? i : (int)__umulhi((uint32_t)i, inverse); }
+#endif
+};
+
 struct BeamArgs {
   const void* logits;
   const float* scores;
@@ -28,6 +39,8 @@ struct BeamArgs {
   int64_t stride;
   int32_t n_rows, vocab, beams, k, end_token;
   int32_t chunks, chunk_vecs;  // chunks of a row, and how many 16-byte vectors of logits one has
+  int32_t lanes;               // of a join, for a row's chunks
+  Divisor by_k, by_beam, by_deep;  // a list's candidates, a row's, those of a list that make a join's bound
 };
 size_t beam_select_workspace_bytes(int64_t n_rows, int32_t vocab, int32_t k);
 cudaError_t launch_beam_select(BeamArgs a, int32_t type, void* workspace, cudaStream_t stream);

@@ -448,7 +448,7 @@ __device__ __forceinline__ uint64_t key_of(const Two& total, int i) {
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return kMostItems - 1 - (int)(key & (kMostItems - 1)); }
 // Some 4 k candidates, and k at the least, make the bound of a join.
-__host__ __device__ inline int depth(int k, int lists) {
+inline int depth(int k, int lists) {
   const int d = (4 * k + lists - 1) / lists;
   return d < k ? d : k;
 }
@@ -483,8 +483,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   for (int j = 0; j < kEarly; j++)
     if (tid + j * kThreads < all) early[j] = from[tid + j * kThreads];
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
-  int lanes = 1;
-  while (lanes < 32 && lanes < a.chunks) lanes <<= 1;
+  const int lanes = a.lanes;
   for (int b0 = 0; b0 < a.beams; b0 += kThreads / lanes) {
     const int b = b0 + tid / lanes, c0 = tid & (lanes - 1);
     const bool live = b < a.beams;
@@ -516,7 +515,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   }
   __syncthreads();
   auto put = [&](int i, BeamItem it) {
-    const int l = i / k, b = i / per_beam;
+    const int l = a.by_k.under(i), b = a.by_beam.under(i);
     uint64_t key = (1 << 16) + i;
     if (sm.kind[b] != kNone && i - l * k < sizes[l]) {
       // a fourth of the total: no finite score and logits make it overflow
@@ -537,10 +536,11 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
   if (all > kAll) {
     // a bound: the k-th best of each list's first `deep` candidates, by the upper bits of their totals (the index
     // in the others makes them differ); whatever is no worse in these bits stays
-    const int deep = depth(k, lists), heads = lists * deep, m = pow2_from(heads), bits = 31 - __clz(m);
+    const int deep = a.by_deep.d, heads = lists * deep, m = pow2_from(heads), bits = 31 - __clz(m);
     uint32_t* upper = reinterpret_cast<uint32_t*>(sorted);
     for (int i = tid; i < m; i += kThreads) {
-      const uint32_t hi = i < heads ? (uint32_t)(keys[i / deep * k + i % deep] >> 32) : 0u;
+      const int l = a.by_deep.under(i);
+      const uint32_t hi = i < heads ? (uint32_t)(keys[l * k + (i - l * deep)] >> 32) : 0u;
       upper[i] = (hi >> bits << bits) | (m - 1 - i);
     }
     __syncthreads();
@@ -671,8 +671,12 @@ int32_t cluster_chunks(int64_t n_rows, int32_t beams) {
 }
 
 template <class T, int kThreads>
-cudaError_t launch_scan(const BeamArgs& a, bool cluster, cudaStream_t stream) {
+cudaError_t launch_scan(BeamArgs a, bool cluster, cudaStream_t stream) {
   const int lists = a.beams * a.chunks;
+  a.by_k = Divisor(a.k);
+  a.by_beam = Divisor(a.chunks * a.k);
+  a.by_deep = Divisor(depth(a.k, lists));
+  a.lanes = std::min(32, pow2_from(a.chunks));
   const dim3 grid((unsigned)(a.n_rows * (int64_t)a.chunks));
   const size_t tops = sizeof(float) * kThreads * ((a.chunk_vecs + kVecs * kThreads - 1) / (kVecs * kThreads));
   cudaError_t e;
