@@ -262,14 +262,16 @@ __device__ __forceinline__ int block_sum(int v, int32_t* count, int slot) {
 // One chunk: its list and its sums go to `list` and `stat` (nothing, if the row has no tokens to offer).  A row's
 // tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a chunk takes
 // `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.  `tops` has a float for each tile
-// of each thread; `ready` is called by all threads before anything is written.
-template <class T, int kThreads, class Ready>
+// of each thread; `begin` is called once what the launch before this one wrote may be read, `ready` by all threads before
+// anything is written.
+template <class T, int kThreads, class Begin, class Ready>
 __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk, ScanShared<kThreads>& sm, float* tops, BeamItem* list,
-                                           BeamStat* stat, Ready&& ready) {
+                                           BeamStat* stat, Begin&& begin, Ready&& ready) {
   constexpr int kE = 16 / sizeof(T), kWarps = kThreads / 32, kTile = kVecs * kThreads, kFound = ScanShared<kThreads>::kFound;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) sm.owners = sm.n = sm.count[0] = sm.count[1] = 0, sm.bound = -kInf;
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  begin();
   if (kind_of(a, row, a.scores[row], false) != kTokens) return;
   const T* x = static_cast<const T*>(a.logits) + row * a.stride;
   const int head = min(a.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) scan_kernel(const B
   __shared__ ScanShared<kThreads> sm;
   const int row = blockIdx.x / a.chunks;
   scan_chunk<T>(a, row, blockIdx.x - row * a.chunks, sm, reinterpret_cast<float*>(smem), a.lists + (int64_t)blockIdx.x * a.k,
-                a.stats + blockIdx.x, [] {});
+                a.stats + blockIdx.x, [] {}, [] {});
 }
 
 // ---------------------------------------------------------------- join
@@ -467,7 +469,16 @@ __host__ __device__ inline size_t join_bytes(int k, int lists) {
   return sizeof(uint64_t) * (sorted_at(all, lists) + pow2_from(all));
 }
 
-// One group, by one CTA, from its rows' lists and sums; `smem` has join_bytes.
+// The scores of a group's rows, and what they contribute, for the thread of each row.
+__device__ __forceinline__ void read_rows(const BeamArgs& a, int first, JoinShared& sm) {
+  for (int b = threadIdx.x; b < a.beams; b += blockDim.x) {
+    const float s = a.scores[first + b];
+    sm.kind[b] = kind_of(a, first + b, s, true);
+    sm.score[b] = s;
+  }
+}
+
+// One group, by one CTA, from its rows' lists and sums, once read_rows has been called; `smem` has join_bytes.
 template <int kThreads>
 __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const BeamStat* stats, const BeamItem* from,
                                            JoinShared& sm, uint8_t* smem) {
@@ -484,6 +495,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     if (tid + j * kThreads < all) early[j] = from[tid + j * kThreads];
   // a row's chunks over `lanes` adjacent lanes, all of the group's rows at once if they fit
   const int lanes = a.lanes;
+  __syncthreads();
   for (int b0 = 0; b0 < a.beams; b0 += kThreads / lanes) {
     const int b = b0 + tid / lanes, c0 = tid & (lanes - 1);
     const bool live = b < a.beams;
@@ -491,8 +503,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     // (a row without lists has what the workspace held; it is not looked at)
     BeamStat mine{-kInf, 0.f, 0.f, 0};
     if (live && c0 < a.chunks) mine = st[c0];
-    const float sc = live ? a.scores[first + b] : -kInf;
-    Kind what = live ? kind_of(a, first + b, sc, c0 == 0) : kNone;
+    int32_t what = live ? sm.kind[b] : kNone;
     float top = mine.top;
     for (int q = c0 + lanes; q < a.chunks && live; q += lanes) top = fmaxf(top, st[q].top);
     for (int d = lanes >> 1; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
@@ -511,7 +522,7 @@ __device__ __forceinline__ void join_group(const BeamArgs& a, int group, const B
     }
     if (what == kTokens && total.hi == 0.f) what = kNone;
     if (what == kTokens) total = log_of(total);
-    if (live && c0 == 0) sm.kind[b] = what, sm.score[b] = sc, sm.tops[b] = top, sm.rest[b] = total;
+    if (live && c0 == 0) sm.kind[b] = what, sm.tops[b] = top, sm.rest[b] = total;
   }
   __syncthreads();
   auto put = [&](int i, BeamItem it) {
@@ -596,6 +607,7 @@ __global__ void __launch_bounds__(kJoin) join_kernel(const BeamArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int64_t list = (int64_t)blockIdx.x * a.beams * a.chunks;
+  read_rows(a, blockIdx.x * a.beams, sm);
   join_group<kJoin>(a, blockIdx.x, a.stats + list, a.lists + list * a.k, sm, smem);
 }
 
@@ -628,8 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     waited = true;
   };
+  auto begin = [&] {
+    if (list == 0) read_rows(a, group * a.beams, join);
+  };
   scan_chunk<T>(a, group * a.beams + beam, list - beam * a.chunks, scan, reinterpret_cast<float*>(own),
-                in_first_cta(items + list * a.k), in_first_cta(stats + list), wait);
+                in_first_cta(items + list * a.k), in_first_cta(stats + list), begin, wait);
   if (!waited) {  // (a row that has nothing to offer)
     if (list != 0) return;
     wait();
