@@ -206,6 +206,66 @@ def test_a_row_is_the_same_in_any_batch(kind):
         assert abs(whole[0][r] - alone[0][0]).max() <= 1e-5
 
 
+def test_rows_past_32_bit_offsets():
+    from sparse_attention_fp4_gb300 import fp4idx
+    R, V = 8196, 1 << 18  # 2^31 + 2^20 logits
+    x = torch.zeros((R, V), dtype=BF16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    for r in (0, 8190, 8191, 8192, 8195):
+        x[r] = torch.randn(V, generator=g, device="cuda")
+    s = torch.full((R,), -1.0, device="cuda")
+    out = [torch.empty(R, dtype=d, device="cuda") for d in (FP32, torch.int32, torch.int32)]
+    ws = torch.empty(fp4idx.beam_select_workspace_bytes(R, V, 2), dtype=torch.uint8, device="cuda")
+    fp4idx.beam_select(x, s, 2, 2, ws, *out)
+    got = [o.cpu().numpy().reshape(-1, 2) for o in out]
+    for first in (0, 8190, 8192, 8194):
+        pair = x[first:first + 2].float().cpu().numpy()
+        mine = [v[first // 2:first // 2 + 1].copy() for v in got]
+        mine[1] -= first
+        ref.check_select(mine + [None], pair, np.float32([-1, -1]), 2, 2)
+    assert (got[2][1] == [0, 1]).all() and (got[1][1] == 2).all()  # rows of zeros
+
+
+@pytest.mark.parametrize("beams", [1, 64])
+def test_the_most_rows(beams):
+    from sparse_attention_fp4_gb300 import fp4idx
+    R, V, k = 1 << 20, 3, 1
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn((R, V), generator=g, device="cuda")
+    s = -torch.rand(R, generator=g, device="cuda")
+    out = [torch.empty(R // beams, dtype=d, device="cuda") for d in (FP32, torch.int32, torch.int32)]
+    ws = torch.empty(fp4idx.beam_select_workspace_bytes(R, V, k), dtype=torch.uint8, device="cuda")
+    fp4idx.beam_select(x, s, beams, k, ws, *out)
+    total = (s.double()[:, None] + torch.log_softmax(x.double(), 1)).view(R // beams, -1)
+    want, at = total.max(1)
+    assert float((out[0].double() - want).abs().max()) < 3e-6
+    first = torch.arange(R // beams, device="cuda") * beams
+    flat = (out[1] - first) * V + out[2]
+    assert bool(((flat >= 0) & (flat < beams * V)).all())
+    chosen = total.gather(1, flat.long()[:, None])[:, 0]
+    assert float((want - chosen).max()) < 3e-6  # the best, but for totals that close
+
+
+def test_two_streams_at_once():
+    from sparse_attention_fp4_gb300 import fp4idx
+    a, sa = rows(30, 64, 60000, BF16)
+    b, sb = rows(31, 40, 50001, FP32)
+    calls = []
+    for x, scores, beams, k in ((a, sa, 4, 8), (b, sb, 20, 20)):
+        n = x.shape[0] // beams * k
+        out = [torch.empty(n, dtype=d, device="cuda") for d in (FP32, torch.int32, torch.int32)]
+        ws = torch.empty(fp4idx.beam_select_workspace_bytes(*x.shape, k), dtype=torch.uint8, device="cuda")
+        calls.append((x, torch.tensor(scores, device="cuda"), beams, k, ws, out, scores))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for st, (x, s, beams, k, ws, out, _) in zip(streams, calls):
+            fp4idx.beam_select(x, s, beams, k, ws, *out, stream=st)
+    torch.cuda.synchronize()
+    for x, s, beams, k, ws, out, scores in calls:
+        ref.check_select([o.cpu().numpy().reshape(-1, k) for o in out] + [None], x.float().cpu().numpy(), np.float32(scores), beams, k)
+
+
 def test_streams_graph_and_repeats():
     from sparse_attention_fp4_gb300 import fp4idx
     x, scores = rows(17, 32, 30000, BF16)

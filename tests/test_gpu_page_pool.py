@@ -81,7 +81,7 @@ def pick(seed, rows, new, ended=0.0):
 
 @pytest.mark.parametrize("rows,most,ratio,new,ended", [
     (1, 1, 1, 1, 0), (1, 1, 64, 3, 0), (4, 3, 4, 4, 0), (4, 8, 1, 4, 0.3), (8, 5, 2, 8, 0), (3, 40, 1, 12, 0), (64, 20, 4, 64, 0.1),
-    (64, 130, 1, 64, 0), (5, 300, 1, 5, 0.5), (33, 129, 3, 70, 0.2), (1, 2000, 1, 4, 0), (200, 128, 1, 130, 0.4), (7, 9, 1, 0, 0)])
+    (64, 130, 1, 64, 0), (5, 300, 1, 5, 0.5), (33, 129, 3, 70, 0.2), (1, 2000, 1, 4, 0), (2, 30000, 1, 3, 0.3), (200, 128, 1, 130, 0.4), (7, 9, 1, 0, 0)])
 def test_fork(rows, most, ratio, new, ended):
     for seed in range(3):
         table, cached, ids = state(seed, rows, most, ratio, rows * most + new + 9, same=seed == 1)
@@ -359,6 +359,12 @@ def test_copy_many_regions():
     pool = 50
     ids = random.Random(1).sample(range(pool), 30)
     check_copy(ids[:15], ids[15:], caches_of(1, pool, ("payload", "scale", "tiny", "fp8") * 64))
+
+
+def test_copy_large_pages():
+    caches = [filled(8, 6, 3 << 20), filled(9, 6, 5, 4000016, dtype=torch.float32)]
+    assert raw(caches[1]).shape[1] % 16 == 0
+    check_copy([0, 3], [5, 1], caches)
 
 
 def test_copy_padding_count_and_bad_ids():
