@@ -670,14 +670,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
 // vectors 19 either way).
 constexpr int kWave = 304, kSmallVecs = 2048;
 // The least and the most vectors of a row that one CTA takes, what it takes to spare the join lists, and the lists that
-// a join has then (one request of 8 or 16 beams 13 and 15 us, with as many chunks as SMs 25 and 27).
-constexpr int kLeastVecs = 512, kMostVecs = 65536, kShortVecs = 4096, kLists = 32;
+// a join has then (one request of 8 or 16 beams 13 and 15 us, with as many chunks as SMs 25 and 27); the candidates of a
+// join that more chunks do not pass (22 rows of 246,505 with lists of 44 21.5 us, 27.2 with up to 8,192; 63 rows of 204,501
+// 23.4 and 26.0; 32 of 131,072 with lists of 64 24.9 and 23.0).
+constexpr int kLeastVecs = 512, kMostVecs = 65536, kShortVecs = 4096, kLists = 32, kFewItems = 2048;
 struct Cut {
   int32_t chunks, vecs;
   Cut(int64_t n_rows, int32_t beams, int32_t k, int32_t vocab, int elems) {
     const int64_t all = std::max(1, vocab / elems);
     const int64_t few = std::max<int64_t>(kLists / beams, all / kShortVecs);
-    const int64_t want = std::max<int64_t>(1, std::min({kWave / n_rows, (int64_t)(kMostItems / (beams * k)), few}));
+    const int64_t want = std::max<int64_t>(1, std::min({kWave / n_rows, (int64_t)(kFewItems / (beams * k)), few}));
     int64_t each = std::max<int64_t>(kLeastVecs, (all + want - 1) / want);
     each = std::min<int64_t>((each + 31) / 32 * 32, kMostVecs);
     vecs = (int32_t)each;
