@@ -2,8 +2,8 @@
 //
 // Bound by HBM.  A page is cut into windows of up to kMost 16-byte pieces a lane, and warps take windows, all in
 // flight at once: a warp's loads, then its stores, with the next window's page ids on their way.  Small
-// pages (256 bytes of scales) are a short window of their own.  20,000 index pages take 30.5 us (5.7 TB/s; a CTA a page
-// and cache 56), 4,001 latent pages 92 us (6.1 TB/s).
+// pages (256 bytes of scales) are a short window of their own.  20,000 index pages take 29.6 us (5.9 TB/s; a CTA a page
+// and cache 56), 4,001 latent pages 87 us (6.4 TB/s).
 #include <algorithm>
 
 #include "beam.cuh"
@@ -87,8 +87,11 @@ cudaError_t launch_move_pages(const int32_t* src, const int32_t* dst, int64_t n_
   int ctas = 0;
   const cudaError_t e = resident_ctas(reinterpret_cast<const void*>(move_pages_kernel), kThreads, 0, &ctas);
   if (e != cudaSuccess) return e;
+  // four times the CTAs that run at once: the later ones begin as others end (latent pages 92 us with as many as run at
+  // once, 87 with four times as many, 85 with a CTA for every eight windows; index pages 30.5, 29.6 and 31.5), and few are
+  // launched for nothing where *count is far below n_copies
   const int64_t need = (n_copies * windows + kWarps - 1) / kWarps;
-  return launch_early(move_pages_kernel, dim3((unsigned)std::min<int64_t>(need, ctas)), kThreads, 0, 1, stream, src, dst,
+  return launch_early(move_pages_kernel, dim3((unsigned)std::min<int64_t>(need, 4 * (int64_t)ctas)), kThreads, 0, 1, stream, src, dst,
                       (int32_t)n_copies, count, regions, (int32_t)windows, num_pages, status);
 }
 
