@@ -268,9 +268,10 @@ __device__ __forceinline__ int block_sum(int v, int32_t* count, int slot) {
 
 // One chunk: its list and its sums go to `list` and `stat` (nothing, if the row has no tokens to offer).  A row's
 // tokens: up to the first 16-byte boundary one by one (the head), then vectors, of which a chunk takes
-// `chunk_vecs`, then the rest (the tail).  The first chunk takes head and tail too.  `tops` has a float for each tile
-// of each thread; `begin` is called once what the launch before this one wrote may be read, `ready` by all threads before
-// anything is written.
+// `chunk_vecs`, then the rest (the tail).  The first chunk takes the head too, the last one the tail: a list's place grows
+// with its tokens, and the join takes the lower place among equal totals.  `tops` has a float for each tile of each thread;
+// `begin` is called once what the launch before this one wrote may be read, `ready` by all threads before anything is
+// written.
 template <class T, int kThreads, class Begin, class Ready>
 __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk, ScanShared<kThreads>& sm, float* tops, BeamItem* list,
                                            BeamStat* stat, Begin&& begin, Ready&& ready) {
@@ -285,8 +286,12 @@ __device__ __forceinline__ void scan_chunk(const BeamArgs& a, int row, int chunk
   const int vecs = (a.vocab - head) / kE, rest = head + vecs * kE;
   const int first = min(vecs, chunk * a.chunk_vecs), end = min(vecs, first + a.chunk_vecs);
   const uint4* body = reinterpret_cast<const uint4*>(x + head);
-  // the token of lane l of the first warp at the row's ends, -1 for none
-  const int edge = chunk > 0 ? -1 : tid < head ? tid : tid >= 8 && tid < 8 + a.vocab - rest ? rest + tid - 8 : -1;
+  // this thread's token at the row's ends, -1 for none (in one expression over both ends the cluster kernels spill)
+  int edge = -1;
+  if (tid < 16) {
+    if (chunk == 0 && tid < head) edge = tid;
+    if (chunk == a.chunks - 1 && tid >= 8 && rest + tid - 8 < a.vocab) edge = rest + tid - 8;
+  }
   Running run;
   // the next vectors are on their way while these are taken in
   auto load = [&](int i, uint4 (&v)[kVecs]) {
