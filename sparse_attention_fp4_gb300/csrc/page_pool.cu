@@ -416,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const CompactArgs 
     }
   });
   if (!lead) return;
-  for (int c = moves + tid; c < a.max_moves; c += kThreads) a.move_src[c] = a.move_dst[c] = -1;
+  // (counted without a sign: the last step of a list of nearly 2^31 moves passes it)
+  for (uint32_t c = moves + tid; c < (uint32_t)a.max_moves; c += kThreads) a.move_src[c] = a.move_dst[c] = -1;
   if (tid == 0) {
     if (lost > 0) record_error(a.status, FP4IDX_ERR_CAPACITY);
     a.counts[0] = moves;
