@@ -634,6 +634,8 @@ int fp4idx_beam_select(const void* logits, int32_t logits_type, int64_t logits_s
  * back.  An id outside [0, num_pages) is handed on as it is and never comes back, a partly
  * filled page with such an id is not copied (BAD_PAGE).  The outputs must not overlap one
  * another or the inputs (page_table_out and cached_out are buffers of their own).
+ * A device (or a part of one) that places no cluster of 16 CTAs takes pools of up to 2^22
+ * pages, here and in fp4idx_compact_pages; larger ones are a CUDA error there.
  */
 int fp4idx_fork_pages(const int32_t* page_table, const int32_t* cached_lens, int64_t n_old, int32_t max_pages,
                       int32_t ratio, const int32_t* parents, int64_t n_new, int64_t num_pages, const uint32_t* pinned,

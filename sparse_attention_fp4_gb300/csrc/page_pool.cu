@@ -18,7 +18,7 @@ namespace fp4idx {
 namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
-constexpr int kMaxCtas = 16;
+constexpr int kMaxCtas = 16, kPortable = 8;  // of a cluster: at most, on any device
 constexpr int kLane = 8, kStep = 32 * kLane;  // columns that a lane, a warp takes at once
 constexpr uint32_t kHalf = 1u << 30;          // beside a row's pages: its last one is partly filled
 constexpr size_t kMaxSmem = 225 * 1024;
@@ -448,21 +448,24 @@ template <class A>
 cudaError_t launch(void (*kernel)(A, int, bool), const A& a, int sets, int share, int64_t entries, size_t rows,
                    cudaStream_t stream) {
   const int64_t words = ((int64_t)a.num_pages + 31) / 32;
-  const int ctas = ctas_of(entries, a.num_pages);
+  const void* f = reinterpret_cast<const void*>(kernel);
+  cudaError_t e = set_smem_attr_once(f, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  int ctas = ctas_of(entries, a.num_pages);
+  if (ctas > kPortable) {
+    int fit = 0;  // (asks for clusters above the portable size, of any call's memory)
+    e = resident_clusters(f, ctas, kThreads, kMaxSmem, &fit);
+    if (e != cudaSuccess) return e;
+    if (fit < 1) ctas = kPortable;
+  }
   const int shift = log2_from((words + ctas - 1) / ctas);
   const size_t part = 4 * ((size_t)sets << shift);
   rows += share * ((size_t)4 << shift);
   const bool full = part * ctas + rows <= kMaxSmem;
   const size_t smem = (full ? part * ctas : part) + rows;
-  const void* f = reinterpret_cast<const void*>(kernel);
-  cudaError_t e = set_smem_attr_once(f, kMaxSmem);
-  if (e != cudaSuccess) return e;
-  if (ctas > 8) {
-    int fit = 0;  // (asks for clusters above the portable size)
-    e = resident_clusters(f, ctas, kThreads, kMaxSmem, &fit);
-    if (e != cudaSuccess) return e;
-    if (fit < 1) return cudaErrorInvalidClusterSize;
-  }
+  // (sixteen CTAs hold the marks of every pool, eight those of up to 2^22 pages; 256 long rows are forked in 13.1 us by
+  // sixteen, 17.8 by eight, a pool of 245,000 pages compacted in 22.4 and 34.5)
+  if (smem > kMaxSmem) return cudaErrorInvalidClusterSize;
   return launch_early(kernel, dim3(ctas), kThreads, smem, ctas, stream, a, shift, full);
 }
 
