@@ -581,14 +581,19 @@ int fp4idx_latent_prefill(const uint16_t* q, int64_t n_q, int32_t n_heads, const
  *               where a group has no candidate left
  *   done_out    [n_rows/n_beams, k] int32, nullable (written): 1 where the row was finished
  *               or the token is end_token, else 0
- * Exponentials and a thread's share of their sum are fp32, what is added up above that, and
- * the totals, has some 36 bits or more.  Totals of different rows closer than about 1e-7 of the
- * logarithm of the sum may change places; within a row the order is that of the logits (but for
- * logits of one row so close that their totals agree to 36 bits).  A row whose score or
- * logits hold a NaN or +inf has no candidate (BAD_VALUE).  The outputs must not overlap one
- * another or the inputs.  workspace: fp4idx_beam_select_workspace_bytes(n_rows, vocab, k)
- * bytes, 16-byte aligned, nothing in it needs to be initialised; calls that may overlap need
- * one each.
+ * The logarithm of a row's sum is off by less than (30 + 6 t + 2.3 ln(vocab)) * 2^-24, however
+ * small it is itself, where t is vocab/2048 for fp32 and vocab/4096 for 16-bit logits, rounded
+ * up, 64 at the most (2.7e-5 for the longest rows; 1e-7 is usual, 6e-7 the most that was seen):
+ * exponentials, a thread's share of their sum and the factors between shares are fp32.  What is
+ * added up above that, and the totals, has some 36 bits or more.  Totals of different rows
+ * closer than twice that error may change places; within a row the order is that of the logits
+ * (but for logits of one row so close that their totals agree to 36 bits).  A total below
+ * fp32's range is written as -inf, with its row and token.  A row whose score or logits hold a
+ * NaN or +inf has no candidate (BAD_VALUE).  The outputs must not overlap one another or the
+ * inputs.  workspace: fp4idx_beam_select_workspace_bytes(n_rows, vocab, k) bytes, 16-byte
+ * aligned, nothing in it needs to be initialised; calls that may overlap need one each.
+ * Work is shared out over all rows, dead ones too: where one row a group is alive (behind the
+ * prompts), the live rows alone with n_beams 1 are faster.
  */
 size_t fp4idx_beam_select_workspace_bytes(int64_t max_rows, int32_t vocab, int32_t k);
 int fp4idx_beam_select(const void* logits, int32_t logits_type, int64_t logits_stride, int32_t vocab,

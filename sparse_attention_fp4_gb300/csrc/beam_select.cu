@@ -51,7 +51,8 @@ __device__ __forceinline__ Two xor_lane(const Two& a, int d) {
   return Two{__shfl_xor_sync(~0u, a.hi, d), __shfl_xor_sync(~0u, a.lo, d)};
 }
 // log(v) for a normal v > 0: v = 2^e f with f in [3/4, 3/2), log f = 2 artanh(s), s = (f - 1) / (f + 1) (the first
-// term of its series in two floats, the others, below 0.006, in one); within 2e-9.
+// term of its series in two floats, the others, below 0.006, in one: 7 roundings and four of sums); within 3.3e-9 (2.8e-9
+// found over 40 million numbers).
 __device__ __forceinline__ Two log_of(const Two& v) {
   int e = (__float_as_int(v.hi) >> 23) - 127;
   float f = __int_as_float((__float_as_int(v.hi) & 0x7FFFFF) | 0x3F800000);
@@ -62,7 +63,7 @@ __device__ __forceinline__ Two log_of(const Two& v) {
   const float low = (__fmaf_rn(-s, d.hi, n) - s * d.lo) / d.hi;  // of n / d
   const float z = s * s;
   const float rest = s * z * (0.33333334f + z * (0.2f + z * (0.14285715f + z * (0.11111111f + z * (0.09090909f + z * 0.07692308f)))));
-  // ln 2 in two parts: the first has 16 bits, so that its product with e is exact
+  // ln 2 in two parts (Cody and Waite): the first has 16 bits, so that its product with e is exact
   const Two base = sum_of(e * 0.693145751953125f, 2.f * s);
   return base + (2.f * (low + rest) + e * 1.4286068203094173e-6f + v.lo / v.hi);
 }
@@ -672,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const
 // them CTAs of 512 threads take one each; above that CTAs of 256 threads (400 rows of 131,072 tokens 29 us against 37,
 // 100 x 6 of 65,537 31 against 36; 256 rows of 131,072 are as fast either way), and 128 for rows of up to kSmallVecs
 // vectors (1,024 rows of 10,000 tokens 17 us against 23, 1,488 rows of 842 with lists of 31 23 against 80; of 4,000
-// vectors 19 either way).
+// vectors 19 either way).  kWave is two CTAs for each of this GPU's 152 SMs.  Dead rows count: 64 groups of four rows of
+// 131,072 tokens, one of them alive, take 15.8 us, their live rows alone 9.7.
 constexpr int kWave = 304, kSmallVecs = 2048;
 // The least and the most vectors of a row that one CTA takes, what it takes to spare the join lists, and the lists that
 // a join has then (one request of 8 or 16 beams 13 and 15 us, with as many chunks as SMs 25 and 27); the candidates of a
