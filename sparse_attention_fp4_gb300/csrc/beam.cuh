@@ -58,7 +58,7 @@ cudaError_t launch_fork_pages(const ForkArgs& a, cudaStream_t stream);
 struct CompactArgs {
   const int32_t *page_table, *cached;
   const uint32_t* pinned;
-  int32_t* remap;  // [num_pages], written for the pages that move
+  int32_t* remap;  // [num_pages], written for every page in use from id counts[1] on, whether it moves or stays
   int32_t *free_pages, *table_out, *move_src, *move_dst, *counts, *status;
   int32_t n_seqs, max_pages, ratio, num_pages, n_free, max_moves;
 };

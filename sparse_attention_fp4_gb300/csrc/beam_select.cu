@@ -4,11 +4,12 @@
 // of the logits, so the scan keeps a row's k largest logits, in lists, next to (largest, sum of exp(logit -
 // largest)); the join turns these into lse and totals and picks a group's k best.
 //
-// Every logit is read once: HBM bounds the scan while it reads (256 rows of 131,072 logits: 10 us of bf16, some 20 of
-// fp32, 6.6 TB/s; with bf16 logits in L2, 7 us, it is the exponential unit).  The rest is latency: 1.5 us to the
-// first logits, 1 us for the bound of a chunk's k largest, 2 for reading the tiles above it again, 1 for sorting what passes,
-// 3 to 7 for the join.  So one launch where a group fits a cluster, no FP64, few barriers.  64 x 4 rows of 131,072
-// bf16 logits take 18.0 us in all (67 MB, 3.7 TB/s), 8 x 32 of fp32 35 (127 MB, 3.6 TB/s), 4 rows of 32,000 7.5 (the host).
+// Every logit is read once, and the tiles that hold a candidate once more (132 MB of 127 for wide beams): HBM bounds the
+// scan while it reads (256 rows of 131,072 logits: 10 us of bf16, some 20 of fp32, 6.6 TB/s; with bf16 logits in L2, 7 us,
+// it is the exponential unit).  The rest is latency: 1.5 us to the first logits, 1 us for the bound of a chunk's k largest, 2
+// for reading the tiles above it again, 1 for sorting what passes, 3 to 7 for the join.  So one launch where a group fits a
+// cluster, no FP64, few barriers.  64 x 4 rows of 131,072 bf16 logits take 18.0 us in all (67 MB, 3.7 TB/s), 8 x 32 of fp32
+// 33.5 to 37 (127 MB, 3.4 to 3.8 TB/s), 4 rows of 32,000 7.5 to 8.3 (the host).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -695,8 +696,7 @@ struct Cut {
 };
 
 // Chunks of a row in a cluster of a group: no more CTAs than run at once, or one.  The cluster spares a launch (64 x 4
-// rows 18.3 us against 19.6) and is taken for up to kSlack vectors more a CTA (16 x 5 rows of 50,001 12.9 us against
-// 14.8 in two launches; with clusters of four 14.4, of fifteen 3 us more than two launches took).
+// rows 18.1 us against 19.7) and is taken for up to kSlack vectors more a CTA (16 x 5 rows of 50,001 8.9 us against 11.1).
 constexpr int kMaxCluster = 8, kSlack = 8192;
 constexpr size_t kSelectSmem = 100 * 1024;
 int32_t cluster_chunks(int64_t n_rows, int32_t beams) {
