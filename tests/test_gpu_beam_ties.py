@@ -1,4 +1,6 @@
 """Beam selection: equal totals of a row whose tokens several CTAs read, and whose end is no vector boundary."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +9,7 @@ from tests import beam_ref as ref
 from tests.test_gpu_beam_select import BF16, FP16, FP32, run
 
 pytestmark = pytest.mark.gpu
+INF = math.inf
 
 
 def tied(seed, R, V, kind, pad=0, offset=0):
@@ -72,3 +75,44 @@ def test_a_tied_row_is_the_same_in_any_batch(kind):
             if R % beams == 0:
                 got, _ = run(x, [0.0 if r % beams == 0 else -40.0 for r in range(R)], beams, 8)
                 assert (got[2] == want).all(), (R, beams)
+
+
+@pytest.mark.parametrize("kind,V", [(BF16, 4104), (FP16, 4104), (FP32, 4100), (FP32, 2052), (BF16, 8200)])
+@pytest.mark.parametrize("beams", [1, 3, 9])
+def test_a_last_part_without_a_vector(kind, V, beams):
+    """Rows off a vector boundary have a vector less, and what is left of their last part are single tokens."""
+    R = 9 * (8 if beams == 1 else 1)
+    x = tied(V + beams, R, V, kind, pad=1)
+    for k in (1, 5, 20):
+        got, status = run(x, [-3.0 * (r % beams) for r in range(R)], beams, k)
+        assert status == 0
+        for g in range(R // beams):
+            for r in set(got[1][g].tolist()):
+                mine = got[2][g][got[1][g] == r]
+                assert mine.tolist() == order(x[r])[:mine.size].tolist(), (k, g, r)
+
+
+@pytest.mark.parametrize("kind", [BF16, FP16, FP32])
+@pytest.mark.parametrize("V", [4100, 4104, 50257])
+@pytest.mark.parametrize("beams", [1, 9])
+def test_rows_of_which_only_the_ends_are_left(kind, V, beams):
+    """Nothing but a row's first or last token is allowed; and what is no number there takes the row away."""
+    R = 9
+    stride = V + 1
+    x = torch.full((R * stride,), -INF, dtype=kind, device="cuda").as_strided((R, V), (stride, 1))
+    for r in range(R):
+        x[r, V - 1 if r % 3 else 0] = -2.0
+    scores = [-1.0 - r for r in range(R)]
+    want = [V - 1 if r % 3 else 0 for r in range(R)]
+    got, status = run(x, scores, beams, 2)
+    assert status == 0
+    if beams == 1:
+        assert got[2][:, 0].tolist() == want and got[0][:, 0].tolist() == scores and (got[1][:, 1] == -1).all()
+    else:
+        assert got[1][0].tolist() == [0, 1] and got[2][0].tolist() == want[:2] and got[0][0].tolist() == scores[:2]
+    for bad in (float("nan"), INF):
+        for at in (0, V - 1):
+            y = x.clone()
+            y[4, at] = bad
+            got, status = run(y, scores, 1, 1)
+            assert status == 12 and got[1][:, 0].tolist() == [r if r != 4 else -1 for r in range(R)]
